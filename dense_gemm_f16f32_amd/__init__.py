@@ -8,6 +8,9 @@ passes their device pointers, element strides (row- or column-major, any leading
 and torch's current HIP stream, and for split K a workspace tensor.  PyTorch is used for
 device memory and streams only.
 
+linear, linear_backward, rms_norm and rms_norm_backward (linear_norm.py) are the operators of a
+transformer block around the product, in a library of their own.
+
 The library is loaded on first use; if it has not been built the call raises at once
 (there is no fallback of any kind).
 """
@@ -276,3 +279,7 @@ def tile_map(num_pid_m, num_pid_n, group_m, xcd_remap, stream=None):
     if rc != OK:
         raise GemmError(rc, "gemm_f16f32_tile_map")
     return out
+
+
+from .linear_norm import (ACTIVATIONS, RMSNormResult, linear, linear_backward,  # noqa: E402,F401
+                          rms_norm, rms_norm_backward)

@@ -13,6 +13,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "gemm_f16f32.hip")
 SO = os.path.join(PKG, "libgemm_f16f32.so")
+# The linear layer and the norm (include/linear_norm.h), a library of its own.
+LN_SRC = os.path.join(PKG, "csrc", "linear_norm.hip")
+LN_SO = os.path.join(PKG, "liblinear_norm.so")
 # The matrix-core rate probe (measurement only: bench.py --mfma-ceiling).
 PROBE_SRC = os.path.join(PKG, "csrc", "mfma_ceiling.hip")
 PROBE_SO = os.path.join(PKG, "libmfma_ceiling.so")
@@ -54,6 +57,7 @@ def kernel_source_hash() -> str:
 # its DMA, persistent, split-K and generic forms).  The compiler's hazard checks do not see
 # those MFMAs, so the code provides the wait states itself (gemm_kernels.hpp, mfma16).
 ASM_MFMA_KERNELS = ("mfma_ceiling",                         # the rate probe (both)
+                    "lk8lin_ring",                          # the linear layer's 256 x 256 tile
                     "ILi256ELi256ELi64ELi2ELi1ELi2ELi2E",   # gemm_dma*, tile 1
                     "gemm_genericILi256ELi256ELb")          # gemm_generic, 256 x 256 tiles
 
@@ -123,10 +127,12 @@ def check_mfma_waits(so_path: str) -> int:
     return checked
 
 
-def build(extra=()) -> str:
-    tmp = SO + ".tmp"
+def _compile(src: str, so: str, extra=()) -> int:
+    """Compiles one library, checks it and moves it in place; returns the number of its kernels
+    whose asm-MFMA wait states were checked."""
+    tmp = so + ".tmp"
     cmd = [HIPCC, *FLAGS, *extra, "-I", os.path.join(ROOT, "include"),
-           "-I", os.path.join(PKG, "csrc"), SRC, "-o", tmp]
+           "-I", os.path.join(PKG, "csrc"), src, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     # hipcc's host pass does not know the packed-fp32 feature and says so; that is harmless.
     msgs = [ln for ln in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in ln]
@@ -145,7 +151,22 @@ def build(extra=()) -> str:
     if n == 0:
         os.remove(tmp)
         raise RuntimeError("no asm-MFMA kernel found to check in the built library")
-    os.replace(tmp, SO)
+    os.replace(tmp, so)
+    return n
+
+
+def build_linear_norm(extra=()) -> str:
+    """Compiles the linear layer and the norm (liblinear_norm.so)."""
+    _compile(LN_SRC, LN_SO, extra)
+    return LN_SO
+
+
+def build(extra=()) -> str:
+    """Compiles every library: the two large ones beside each other, then the rate probe."""
+    from concurrent.futures import ThreadPoolExecutor
+    with ThreadPoolExecutor(2) as pool:
+        for job in [pool.submit(_compile, SRC, SO, extra), pool.submit(build_linear_norm, extra)]:
+            job.result()
     build_probe()
     return SO
 

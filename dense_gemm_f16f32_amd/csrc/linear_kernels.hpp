@@ -1,0 +1,740 @@
+// Device code of the linear layer on gfx950: tiled matrix products on 16-bit or e4m3 operands
+// with the layer's epilogue, out = act(a b scale + bias) + residual.
+//
+// The operand side (panels in LDS, swizzles, buffer->LDS loads, transposing reads, the program
+// map) is the fp16 product's, from gemm_kernels.hpp; it moves 16-byte chunks and does not look
+// inside them.  What differs here:
+//  * the element type: fp16, bf16 or e4m3.  Two e4m3 values ride in each 16-bit slot, so an
+//    e4m3 operand of K values is a k-major matrix of K/2 slots, and one 64-byte piece of a row
+//    feeds v_mfma_f32_32x32x64_f8f6f4, twice the work of the 16-bit instruction on the same
+//    bytes (the unscaled form: scales are applied to the sum, in the epilogue).
+//  * the ragged panel: when the panel depth does not divide K, the panel that holds the last
+//    K mod BK values is multiplied first, so that every other panel starts at a multiple of BK
+//    and keeps the alignment of its rows.
+//  * the epilogue: a wave's block of sums goes through LDS to a layout in which a lane holds 8
+//    consecutive columns of one row, so that bias, residual, pre-activation and result move in
+//    16-byte accesses.
+#pragma once
+
+#include "gemm_kernels.hpp"
+#include "linear_norm.h"
+
+namespace lk {
+
+using gk::dma_panel;
+using gk::elem_off;
+using gk::extent;
+using gk::float16v;
+using gk::float4v;
+using gk::half8;
+using gk::lds_barrier;
+using gk::u32x4;
+using gk::wait_vmcnt;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef int int4v __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes at any 16-bit element
+
+constexpr int kF16 = LINEAR_NORM_F16, kBF16 = LINEAR_NORM_BF16, kE4M3 = LINEAR_NORM_E4M3;
+
+struct LinArgs {
+  const uint16_t* A;      // 16-bit slots: elements, or pairs of e4m3 values
+  const uint16_t* B;
+  int64_t lda, ldb;       // slots
+  int32_t M, N, K;        // K in elements
+  int32_t num_pid_m, num_pid_n, group_m, num_programs;
+  // epilogue; the pointers may be null, except out
+  uint16_t* out;
+  uint16_t* pre;
+  const uint16_t* res;
+  const uint16_t* bias;
+  const float* scale_a;
+  const float* scale_b;
+  int64_t ldo, ldp, ldr;
+  int32_t act, out_type;
+  // split K: slice z sums its panels into W[z][i][j] at W + (z M + i) ldw + j (ldw a multiple
+  // of 8); slices have `per_split` panels, the last one the rest
+  float* W;
+  int64_t ldw;
+  int32_t splits, per_split;
+};
+
+// ---- 16-bit values ---------------------------------------------------------------------
+__device__ __forceinline__ float to_f32(uint16_t v, int type) {
+  return type == kF16 ? (float)__builtin_bit_cast(_Float16, v)
+                      : __builtin_bit_cast(float, (uint32_t)v << 16);
+}
+__device__ __forceinline__ uint16_t to_16(float v, int type) {   // nearest, ties to even
+  return type == kF16 ? __builtin_bit_cast(uint16_t, (_Float16)v)
+                      : __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+__device__ __forceinline__ void unpack8(float (&f)[8], u32x4 v, int type) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = to_f32((uint16_t)(v[e / 2] >> (16 * (e & 1))), type);
+}
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8], int type) {
+  u32x4 v;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    v[d] = (uint32_t)to_16(f[2 * d], type) | ((uint32_t)to_16(f[2 * d + 1], type) << 16);
+  return v;
+}
+// 8 values at p, of which the first n exist (n >= 8: all); the others read as 0.
+__device__ __forceinline__ void load8(float (&f)[8], const uint16_t* p, int n, int type) {
+  if (n >= 8) {
+    unpack8(f, *(const u32x4_any*)p, type);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = e < n ? to_f32(p[e], type) : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8], int n, int type) {
+  if (n >= 8) {
+    *(u32x4_any*)p = pack8(f, type);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e] = to_16(f[e], type);
+  }
+}
+
+// ---- activations -------------------------------------------------------------------------
+// exp through the hardware's 2^x (1 ulp) and its reciprocal (1 ulp): an error of a few 2^-23
+// of the result, far below the 16-bit rounding that follows.
+__device__ __forceinline__ float fast_exp(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896f);
+}
+__device__ __forceinline__ float sigmoid(float x) {   // exp(-x) = inf gives 1 / inf = 0
+  return __builtin_amdgcn_rcpf(1.f + fast_exp(-x));
+}
+// The normal distribution's cumulative function, Phi(v) = erfc(-v / sqrt 2) / 2, by formula
+// 7.1.26 of Abramowitz and Stegun (absolute error of erfc below 1.5e-7): erfc(x) = t (a1 + t (a2
+// + ...)) exp(-x^2), t = 1 / (1 + p x), x >= 0.  `e` returns exp(-v^2 / 2).
+__device__ __forceinline__ float normal_cdf(float v, float& e) {
+  const float x = fabsf(v) * 0.70710678118654752f;
+  e = fast_exp(-0.5f * v * v);
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+  const float q = t * (0.254829592f +
+                       t * (-0.284496736f +
+                            t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  const float tail = 0.5f * q * e;
+  return v < 0.f ? tail : 1.f - tail;
+}
+
+constexpr float kTanhC = 0.79788456080286536f;   // sqrt(2 / pi)
+
+// v * Phi(v) and v * sigmoid(v) with v = -inf are 0 * -inf; their limit is 0 but the formula
+// gives NaN, here as in any evaluation of it.
+__device__ __forceinline__ float act_value(float v, int act) {
+  float e;
+  switch (act) {
+    case LINEAR_ACT_RELU: return v < 0.f ? 0.f : v;   // NaN stays
+    case LINEAR_ACT_GELU: return v * normal_cdf(v, e);
+    // tanh u = 2 sigmoid(2u) - 1
+    case LINEAR_ACT_GELU_TANH: return v * sigmoid(2.f * kTanhC * (v + 0.044715f * v * v * v));
+    case LINEAR_ACT_SILU: return v * sigmoid(v);
+    default: return v;
+  }
+}
+__device__ __forceinline__ float act_slope(float v, int act) {
+  switch (act) {
+    case LINEAR_ACT_RELU: return v > 0.f ? 1.f : 0.f;
+    case LINEAR_ACT_GELU: {
+      float e;
+      const float c = normal_cdf(v, e);
+      return c + v * e * 0.39894228040143268f;   // 1 / sqrt(2 pi)
+    }
+    case LINEAR_ACT_GELU_TANH: {
+      // v p(2u): p + v p (1 - p) 2u'.  p (1 - p) is 0 long before v^2 overflows.
+      const float p = sigmoid(2.f * kTanhC * (v + 0.044715f * v * v * v));
+      return p + v * p * (1.f - p) * (2.f * kTanhC) * (1.f + 0.134145f * v * v);
+    }
+    case LINEAR_ACT_SILU: {
+      const float p = sigmoid(v);
+      return p * (1.f + v * (1.f - p));
+    }
+    default: return 1.f;
+  }
+}
+
+// ---- epilogue ------------------------------------------------------------------------------
+// 8 consecutive columns of one row: v holds the sums.  `bias8` and `sb8` are the columns' bias
+// and scales (0 and 1 where there are none).
+struct Columns {
+  float bias[8], sb[8];
+  int n;   // columns that exist, from the first
+};
+template <int TY>
+__device__ __forceinline__ Columns load_columns(const LinArgs& p, int col) {
+  const int ot = TY == kE4M3 ? p.out_type : TY;
+  Columns c;
+  c.n = p.N - col;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    c.bias[e] = 0.f;
+    c.sb[e] = 1.f;
+  }
+  if (c.n > 0) {
+    if (p.bias) load8(c.bias, p.bias + col, c.n, ot);
+    if (TY == kE4M3 && p.scale_b) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < c.n) c.sb[e] = p.scale_b[col + e];
+    }
+  }
+  return c;
+}
+template <int TY>
+__device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, float (&v)[8],
+                                        const Columns& c) {
+  const int ot = TY == kE4M3 ? p.out_type : TY;
+  if (TY == kE4M3) {
+    const float sa = p.scale_a ? p.scale_a[row] : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * (sa * c.sb[e]) + c.bias[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += c.bias[e];
+  }
+  if (p.pre) store8(p.pre + (int64_t)row * p.ldp + col, v, c.n, ot);
+  if (p.act != LINEAR_ACT_NONE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], p.act);
+  }
+  if (p.res) {
+    float r[8];
+    load8(r, p.res + (int64_t)row * p.ldr + col, c.n, ot);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += r[e];
+  }
+  store8(p.out + (int64_t)row * p.ldo + col, v, c.n, ot);
+}
+
+// ---- tiles -----------------------------------------------------------------------------------
+// A BM x BN tile by WM x WN waves, panels of BK slots.  XB is the MFMA block: 32, or 16 (16-bit
+// types only).  One k step covers KD slots of both operands.
+template <int TY_, int BM_, int BN_, int BK_, bool AKM, bool BKM, int WM_, int WN_, int XB_>
+struct Tile {
+  static constexpr int TY = TY_, BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, XB = XB_;
+  static constexpr int NW = WM * WN;
+  using OA = gk::Opnd<BM, BK, AKM, WM, NW, XB>;
+  using OB = gk::Opnd<BN, BK, BKM, WN, NW, XB>;
+  static constexpr int R = TY == kE4M3 ? 2 : 1;          // 16-byte LDS chunks per fragment
+  static constexpr int KD = OA::KD * R, KS = BK / KD;
+  static constexpr int WTM = BM / WM, WTN = BN / WN, TM = OA::T, TN = OB::T;
+  static constexpr int VN = XB == 16 ? 4 : 16;
+  static constexpr int A_BYTES = OA::BYTES, STAGE = OA::BYTES + OB::BYTES;
+  using Acc = std::conditional_t<XB == 16, float4v, float16v>;
+  using Frag = std::conditional_t<TY == kE4M3, int8v, int4v>;
+  static_assert(TY != kE4M3 || (AKM && BKM && XB == 32), "e4m3 operands are k-major");
+};
+
+template <class T, class O>
+__device__ __forceinline__ typename T::Frag read_frag(const char GK_LDS* st,
+                                                      const int (&o)[O::NOFF], int t, int kk) {
+  if constexpr (T::R == 1) {
+    return __builtin_bit_cast(int4v, gk::read_operand<O>(st, o, t, kk));
+  } else {
+    // any assignment of k to lanes serves, as long as both operands share it
+    const int4v lo = __builtin_bit_cast(int4v, gk::read_operand<O>(st, o, t, 2 * kk));
+    const int4v hi = __builtin_bit_cast(int4v, gk::read_operand<O>(st, o, t, 2 * kk + 1));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void mma(typename T::Acc& acc, const typename T::Frag& a,
+                                    const typename T::Frag& b) {
+  if constexpr (T::TY == kF16 && T::XB == 32)
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a),
+                                                 __builtin_bit_cast(half8, b), acc, 0, 0, 0);
+  else if constexpr (T::TY == kBF16 && T::XB == 32)
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                  __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+  else if constexpr (T::TY == kE4M3 && T::XB == 32)
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, 0, 0, 0);
+}
+
+// In place on accumulator registers (see mfma16 in gemm_kernels.hpp, whose wait states and
+// their check at build time hold here too).
+template <class T>
+__device__ __forceinline__ void mma_inplace(typename T::Acc& acc, const typename T::Frag& a,
+                                            const typename T::Frag& b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (T::TY == kF16)
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+  else if constexpr (T::TY == kBF16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+  else
+    asm volatile("v_mfma_f32_32x32x64_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+#else
+  (void)acc, (void)a, (void)b;   // the host has no such registers
+#endif
+}
+
+// ---- operands --------------------------------------------------------------------------------
+// Buffer resource over `bytes` (even) from a 2-byte aligned address.  The hardware checks each
+// dword of a load against the end; the end is moved up to a whole dword of memory where it cuts
+// one (so its first half is still read), never beyond it.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const uint64_t b = ((uintptr_t)base & 2) ? (uint64_t)bytes
+                                           : ((uint64_t)bytes + 3) & ~(uint64_t)3;
+  const uint32_t hi = (uint32_t)(b >> 32), lo = (uint32_t)b;
+  const uint32_t n = (hi & 0x80000000u) ? 0u : (hi ? 0xFFFFFFFCu : lo);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
+}
+
+// Loads of one operand's panels.
+template <class O>
+struct Loader {
+  const uint16_t* ptr;
+  int64_t ld, ext;
+  int x0;
+  uint32_t off[O::LD];
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int X, int K2, int x0_,
+                                       int w, int lane) {
+    ptr = p;
+    ld = ld_;
+    x0 = x0_;
+    ext = extent<O::KM>(X, K2, ld_);
+    gk::slot_offsets<O>(off, w, lane, ld_);
+  }
+  // Resource of the whole panel whose first k slot is k0 (empty unless live).
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(int64_t k0, bool live) const {
+    const int64_t e0 = elem_off<O::KM>(x0, k0, ld);
+    return make_rsrc(ptr + (live ? e0 : 0), live ? 2 * (ext - e0) : 0);
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int i, char GK_LDS* dst,
+                                       int w) const {
+    gk::buffer_load_lds16(r, (void GK_LDS*)(dst + (i * O::NW + w) * 1024), off[i]);
+  }
+  __device__ __forceinline__ void panel(int64_t k0, bool live, char GK_LDS* dst, int w) const {
+    const __amdgpu_buffer_rsrc_t r = rsrc(k0, live);
+#pragma unroll
+    for (int i = 0; i < O::LD; ++i) load(r, i, dst, w);
+  }
+  // The ragged panel: `rem` elements of k from slot k0 on, zeros after them, through registers.
+  // Each chunk is put together from aligned dwords, so that none straddles the matrix's end.
+  template <int TY>
+  __device__ __forceinline__ void ragged(int64_t k0, int rem, char GK_LDS* dst, int w,
+                                         int lane) const {
+    const int64_t e0 = elem_off<O::KM>(x0, k0, ld);
+    const uint32_t lead = (uint32_t)(uintptr_t)(ptr + e0) & 2u;
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc((const char*)(ptr + e0) - lead, 2 * (ext - e0) + lead);
+#pragma unroll
+    for (int i = 0; i < O::LD; ++i) {
+      const int q = (i * O::NW + w) * 64 + lane;
+      const int row = q / O::CH, c = (q % O::CH) ^ gk::swz<O>(row);
+      u32x4 v = gk::load_chunk<true>(r, off[i] + lead);
+      if constexpr (!O::KM) {
+        if (row >= rem) v = u32x4{0u, 0u, 0u, 0u};
+      } else if constexpr (TY == kE4M3) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int have = rem - (c * 16 + 4 * d);   // bytes of this dword that exist
+          v[d] &= have >= 4 ? ~0u : (have <= 0 ? 0u : (1u << (8 * have)) - 1u);
+        }
+      } else {
+        v = gk::mask_k(v, c * 8, rem);
+      }
+      *(u32x4 GK_LDS*)(dst + q * 16) = v;
+    }
+  }
+};
+
+// ---- a wave's block of sums, through LDS ---------------------------------------------------
+// 32 rows at a time: written as the MFMA leaves them, read as 8 columns a lane.  A row of the
+// slab is 4 floats longer than the block, which puts the 4-row groups that a wave writes at
+// once on different banks.
+template <class T>
+struct Slab {
+  static constexpr int LDW = T::WTN + 4, BYTES = 32 * LDW * 4;
+  static constexpr int LANES = T::WTN / 8, ROWS = 64 / LANES, ITERS = 32 / ROWS;
+};
+
+template <class T, bool SPLIT>
+__device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc (&acc)[T::TM][T::TN],
+                                         int m0, int n0, int wm, int wn, int lane,
+                                         char GK_LDS* slab, float* W) {
+  using S = Slab<T>;
+  constexpr int RB = 32 / T::XB;   // MFMA rows of blocks in a slab
+  float GK_LDS* const s = (float GK_LDS*)slab;
+  const int rr = lane / S::LANES, cc = (lane % S::LANES) * 8;
+  const int col = n0 + wn * T::WTN + cc;
+  const int row0 = m0 + wm * T::WTM;
+  Columns c;
+  if constexpr (!SPLIT) c = load_columns<T::TY>(p, col);
+#pragma unroll
+  for (int t = 0; t < T::TM / RB; ++t) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slab's last reads are done
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int tn = 0; tn < T::TN; ++tn)
+#pragma unroll
+        for (int v = 0; v < T::VN; ++v) {
+          const int r = T::XB == 16 ? b * 16 + 4 * (lane >> 4) + v
+                                    : 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+          s[r * S::LDW + tn * T::XB + (lane & (T::XB - 1))] = acc[t * RB + b][tn][v];
+        }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+    for (int i = 0; i < S::ITERS; ++i) {
+      const int r = i * S::ROWS + rr;
+      const int row = row0 + t * 32 + r;
+      const float4v lo = *(const float4v GK_LDS*)(s + r * S::LDW + cc);
+      const float4v hi = *(const float4v GK_LDS*)(s + r * S::LDW + cc + 4);
+      if (row < p.M && col < p.N) {
+        if constexpr (SPLIT) {   // ldw is a multiple of 8: whole groups
+          float* const w = W + (int64_t)row * p.ldw + col;
+          *(float4v*)w = lo;
+          *(float4v*)(w + 4) = hi;
+        } else {
+          float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          finish8<T::TY>(p, row, col, f, c);
+        }
+      }
+    }
+  }
+}
+
+// k slots of the matrices, and the ragged panel
+struct Panels {
+  int np, rem, k2, first;   // panels, elements of the ragged one (0: none), slots, its slot
+  // slot where panel s (not the ragged one) starts
+  int base;
+};
+template <int TY, int BK>
+__device__ __forceinline__ Panels panels_of(int K) {
+  constexpr int E = TY == kE4M3 ? 2 : 1;   // elements per slot
+  Panels q;
+  q.k2 = (K + E - 1) / E;
+  q.rem = K % (BK * E);
+  q.np = K / (BK * E) + (q.rem ? 1 : 0);
+  q.first = K / (BK * E) * BK;
+  q.base = q.rem ? -BK : 0;
+  return q;
+}
+
+// Program -> tile and k slice: programs are z-major, each slice the whole grouped map.
+template <int BM, int BN>
+__device__ __forceinline__ int tile_of(const LinArgs& p, int h, int& m0, int& n0) {
+  const int z = h / p.num_programs;
+  int pid, pid_m, pid_n;
+  gk::program_tile(h - z * p.num_programs, p.num_programs, p.num_pid_m, p.num_pid_n, p.group_m, 1,
+                   pid, pid_m, pid_n);
+  m0 = pid_m * BM;
+  n0 = pid_n * BN;
+  return z;
+}
+
+// ---------------------------------------------------------------------------------------
+// Staged tile: NS LDS stages, operands read RD k steps ahead, one barrier per panel; panels
+// past the end are empty (zeros, no memory touched).
+// ---------------------------------------------------------------------------------------
+template <class T, int NS, int RD, bool AKM, bool BKM, bool SPLIT>
+__device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, int z,
+                                            char GK_LDS* const (&S)[NS]) {
+  using OA = typename T::OA;
+  using OB = typename T::OB;
+  constexpr int KS = T::KS, BK = T::BK;
+  constexpr int NM = T::TM * T::TN, ND = T::R * (OA::READS + OB::READS), NV = OA::LD + OB::LD;
+  static_assert(NS >= 2 && NS * T::STAGE <= 160 * 1024 && (NS - 2) * NV <= 63, "stages");
+  static_assert(RD >= 1 && RD < KS && (NS * KS) % (RD + 1) == 0, "read-ahead distance");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w / T::WN, wn = w % T::WN;
+  const Panels q = panels_of<T::TY, BK>(p.K);
+  const int s0 = SPLIT ? z * p.per_split : 0;
+  const int s1 = SPLIT ? (s0 + p.per_split < q.np ? s0 + p.per_split : q.np) : q.np;
+  const int np = s1 - s0;   // this slice's panels (at least one if split)
+
+  Loader<OA> la;
+  Loader<OB> lb;
+  la.init(p.A, p.lda, p.M, q.k2, m0, w, lane);
+  lb.init(p.B, p.ldb, p.N, q.k2, n0, w, lane);
+  // Without a ragged panel the matrices' last elements are in the last panel, where the range
+  // check can cut them off (see last_element_slot): their owners write them again.
+  uint16_t va = 0, vb = 0;
+  int pa = -1, pb = -1;
+  if (T::TY != kE4M3 && q.rem == 0 && s1 == q.np) {
+    pa = gk::last_element_slot<OA>(m0, p.M, p.K, p.A, la.ext, tid, va);
+    pb = gk::last_element_slot<OB>(n0, p.N, p.K, p.B, lb.ext, tid, vb);
+  }
+  auto patch = [&](char GK_LDS* base) __attribute__((always_inline)) {
+    if (pa >= 0) *(uint16_t GK_LDS*)(base + pa) = va;
+    if (pb >= 0) *(uint16_t GK_LDS*)(base + T::A_BYTES + pb) = vb;
+  };
+  auto issue = [&](int s, char GK_LDS* base) __attribute__((always_inline)) {
+    const int64_t k0 = (int64_t)q.base + (int64_t)(s0 + s) * BK;
+    la.panel(k0, s < np, base, w);
+    lb.panel(k0, s < np, base + T::A_BYTES, w);
+  };
+  typename T::Acc acc[T::TM][T::TN];
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) acc[i][j] = typename T::Acc{};
+  int oa[OA::NOFF], ob[OB::NOFF];
+  gk::operand_offsets<OA>(oa, wm, lane, 0);
+  gk::operand_offsets<OB>(ob, wn, lane, T::A_BYTES);
+  typename T::Frag fa[RD + 1][T::TM], fb[RD + 1][T::TN];
+  auto read = [&](int slot, const char GK_LDS* st, int kk) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < T::TM; ++t) fa[slot][t] = read_frag<T, OA>(st, oa, t, kk);
+#pragma unroll
+    for (int t = 0; t < T::TN; ++t) fb[slot][t] = read_frag<T, OB>(st, ob, t, kk);
+  };
+  // Panel s at position j of the unrolled loop.  NS == 2: its stage is refilled past the
+  // barrier in its last steps; NS >= 3: the previous panel's stage at its start.
+  auto panel = [&](int s, int j) __attribute__((always_inline)) {
+    char GK_LDS* const cur = S[j];
+    char GK_LDS* const nxt = S[(j + 1) % NS];
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      if (NS >= 3 && kk == 0) issue(s + NS - 1, S[(j + NS - 1) % NS]);
+      if (kk == KS - RD) {
+        wait_vmcnt<(NS - 2) * NV>();    // panel s+1 has landed, this wave's part ...
+        if (s + 2 == np) patch(nxt);
+        lds_barrier();                  // ... and every wave's
+        if (NS == 2) issue(s + 2, cur);
+      }
+      const int ka = kk + RD;
+      if (ka < KS)
+        read((j * KS + ka) % (RD + 1), cur, ka);
+      else
+        read((j * KS + ka) % (RD + 1), nxt, ka - KS);
+      const int f = (j * KS + kk) % (RD + 1);
+#pragma unroll
+      for (int tm = 0; tm < T::TM; ++tm)
+#pragma unroll
+        for (int tn = 0; tn < T::TN; ++tn) mma<T>(acc[tm][tn], fa[f][tm], fb[f][tn]);
+      if (NS >= 3 ? kk == 0 : kk == KS - RD)
+        gk::sched_step<NM, ND, NV>();
+      else
+        gk::sched_step<NM, ND, 0>();
+    }
+  };
+  if (np > 0) {
+    constexpr int kPre = NS == 2 ? 2 : NS - 1;
+    if (q.rem && s0 == 0) {
+      la.template ragged<T::TY>(q.first, q.rem, S[0], w, lane);
+      lb.template ragged<T::TY>(q.first, q.rem, S[0] + T::A_BYTES, w, lane);
+    } else {
+      issue(0, S[0]);
+    }
+#pragma unroll
+    for (int j = 1; j < kPre; ++j) issue(j, S[j]);
+    wait_vmcnt<(kPre - 1) * NV>();
+    if (np == 1) patch(S[0]);
+    lds_barrier();
+#pragma unroll
+    for (int d = 0; d < RD; ++d) read(d, S[0], d);
+  }
+  for (int s = 0; s < np; s += NS) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) panel(s + j, j);
+  }
+  wait_vmcnt<0>();   // the empty loads past the end, before LDS is used again
+  lds_barrier();     // every wave has read its last operands
+  constexpr int PER = (T::NW + NS - 1) / NS;   // slabs per stage
+  static_assert(PER * Slab<T>::BYTES <= T::STAGE, "slabs fit the stages");
+  char GK_LDS* slab = S[0];
+#pragma unroll
+  for (int j = 1; j < NS; ++j)
+    if (w % NS == j) slab = S[j];
+  slab += (w / NS) * Slab<T>::BYTES;
+  epilogue<T, SPLIT>(p, acc, m0, n0, wm, wn, lane, slab,
+                     SPLIT ? p.W + (int64_t)z * p.M * p.ldw : nullptr);
+}
+
+template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM,
+          bool SPLIT>
+__global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
+  using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32>;
+  // stages as separate LDS objects (a refill of one is then seen not to touch another), their
+  // addresses assigned one by one (a list of them would become a table)
+  __shared__ __attribute__((aligned(16))) char stage0[T::STAGE];
+  __shared__ __attribute__((aligned(16))) char stage1[T::STAGE];
+  __shared__ __attribute__((aligned(16))) char stage2[NS > 2 ? T::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char stage3[NS > 3 ? T::STAGE : 16];
+  static_assert(NS == 2 || NS == 4, "stages");
+  char GK_LDS* S[NS];
+  S[0] = (char GK_LDS*)stage0;
+  S[1] = (char GK_LDS*)stage1;
+  if constexpr (NS > 2) {
+    S[2] = (char GK_LDS*)stage2;
+    S[3] = (char GK_LDS*)stage3;
+  }
+  int m0, n0;
+  const int z = tile_of<BM, BN>(p, blockIdx.x, m0, n0);
+  staged_tile<T, NS, RD, AKM, BKM, SPLIT>(p, m0, n0, z, S);
+}
+
+// ---------------------------------------------------------------------------------------
+// The 256 x 256 tile (64 slots deep, 4 waves of 128 x 128): the panels in five 32 KiB LDS slots,
+// B's in a ring of three and A's in a ring of two, two k steps per panel, each scheduled by
+// hand -- see ring_tile in gemm_kernels.hpp, whose order of loads, reads and barriers this is.
+// 16-bit types: 64 MFMAs of 16x16x32 a step; e4m3: 16 of 32x32x64, the same cycles.
+// ---------------------------------------------------------------------------------------
+template <int TY, bool AKM, bool BKM, bool SPLIT>
+__device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, int z,
+                                          char GK_LDS* const (&SA)[2],
+                                          char GK_LDS* const (&SB)[3]) {
+  using T = Tile<TY, 256, 256, 64, AKM, BKM, 2, 2, TY == kE4M3 ? 32 : 16>;
+  using OA = typename T::OA;
+  using OB = typename T::OB;
+  constexpr int BK = 64, NM = T::TM * T::TN, NF = T::TM + T::TN;
+  constexpr int LE = NM / 8, RE = NM / NF;   // MFMAs between loads, between fragment reads
+  static_assert(T::KS == 2 && OA::LD == 8 && OB::LD == 8 && NM % 8 == 0 && NM % NF == 0, "ring");
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w / 2, wn = w % 2;
+  const Panels q = panels_of<TY, BK>(p.K);
+  const int s0 = SPLIT ? z * p.per_split : 0;
+  const int s1 = SPLIT ? (s0 + p.per_split < q.np ? s0 + p.per_split : q.np) : q.np;
+  const int np = s1 - s0;
+  Loader<OA> la;
+  Loader<OB> lb;
+  la.init(p.A, p.lda, p.M, q.k2, m0, w, lane);
+  lb.init(p.B, p.ldb, p.N, q.k2, n0, w, lane);
+  uint16_t va = 0, vb = 0;
+  int pa = -1, pb = -1;
+  if (TY != kE4M3 && q.rem == 0 && s1 == q.np) {
+    pa = gk::last_element_slot<OA>(m0, p.M, p.K, p.A, la.ext, tid, va);
+    pb = gk::last_element_slot<OB>(n0, p.N, p.K, p.B, lb.ext, tid, vb);
+  }
+  auto patch = [&](char GK_LDS* a, char GK_LDS* b) __attribute__((always_inline)) {
+    if (pa >= 0) *(uint16_t GK_LDS*)(a + pa) = va;
+    if (pb >= 0) *(uint16_t GK_LDS*)(b + pb) = vb;
+  };
+  typename T::Acc acc[T::TM][T::TN];
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) acc[i][j] = typename T::Acc{};
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  asm volatile("s_nop 7" ::: "memory");
+
+  int oa[OA::NOFF], ob[OB::NOFF];
+  gk::operand_offsets<OA>(oa, wm, lane, 0);
+  gk::operand_offsets<OB>(ob, wn, lane, 0);
+  typename T::Frag fa[2][T::TM], fb[2][T::TN];
+  auto k_of = [&](int s) { return (int64_t)q.base + (int64_t)(s0 + s) * BK; };
+  // refill resources: B's of the panel loaded in the next first step, A's of the second step's
+  __amdgpu_buffer_rsrc_t rb = lb.rsrc(k_of(2), 2 < np), ra = rb;
+
+  if (np > 0) {
+    if (q.rem && s0 == 0) {
+      la.template ragged<TY>(q.first, q.rem, SA[0], w, lane);
+      lb.template ragged<TY>(q.first, q.rem, SB[0], w, lane);
+    } else {
+      la.panel(k_of(0), true, SA[0], w);
+      lb.panel(k_of(0), true, SB[0], w);
+    }
+    la.panel(k_of(1), 1 < np, SA[1], w);
+    lb.panel(k_of(1), 1 < np, SB[1], w);
+    wait_vmcnt<OA::LD + OB::LD>();
+    if (np == 1) patch(SA[0], SB[0]);
+    lds_barrier();
+#pragma unroll
+    for (int t = 0; t < T::TN; ++t) fb[0][t] = read_frag<T, OB>(SB[0], ob, t, 0);
+#pragma unroll
+    for (int t = 0; t < T::TM; ++t) fa[0][t] = read_frag<T, OA>(SA[0], oa, t, 0);
+  }
+  auto panel = [&](int s, int j) __attribute__((always_inline)) {
+    char GK_LDS* const a_cur = SA[j % 2];
+    char GK_LDS* const b_cur = SB[j % 3];
+    char GK_LDS* const a_nxt = SA[(j + 1) % 2];
+    char GK_LDS* const b_nxt = SB[(j + 1) % 3];
+    char GK_LDS* const b_new = SB[(j + 2) % 3];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      if (i % LE == LE / 4) lb.load(rb, i / LE, b_new, w);
+      mma_inplace<T>(acc[i / T::TN][i % T::TN], fa[0][i / T::TN], fb[0][i % T::TN]);
+      if (i == 2 * LE) ra = la.rsrc(k_of(s + 2), s + 2 < np);
+      if (i == 3 * LE) asm volatile("" : "+s"(ra));
+      if (i % RE == 0) {
+        const int r = i / RE;
+        if (r < T::TN)
+          fb[1][r] = read_frag<T, OB>(b_cur, ob, r, 1);
+        else
+          fa[1][r - T::TN] = read_frag<T, OA>(a_cur, oa, r - T::TN, 1);
+      }
+    }
+    wait_vmcnt<OB::LD>();      // panel s+1 has landed (this wave's part) ...
+    if (s + 2 == np) patch(a_nxt, b_nxt);
+    lds_barrier();             // ... every wave's; and every wave has read A of panel s
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      if (i % LE == LE / 4) la.load(ra, i / LE, a_cur, w);
+      mma_inplace<T>(acc[i / T::TN][i % T::TN], fa[1][i / T::TN], fb[1][i % T::TN]);
+      if (i == 2 * LE) rb = lb.rsrc(k_of(s + 3), s + 3 < np);
+      if (i == 3 * LE) asm volatile("" : "+s"(rb));
+      if (i % RE == 0) {
+        const int r = i / RE;
+        if (r < T::TN)
+          fb[0][r] = read_frag<T, OB>(b_nxt, ob, r, 0);
+        else
+          fa[0][r - T::TN] = read_frag<T, OA>(a_nxt, oa, r - T::TN, 0);
+      }
+    }
+  };
+  for (int s = 0; s < np; s += 6) {
+#pragma unroll
+    for (int j = 0; j < 6; ++j) {
+      if (s + j >= np) break;
+      panel(s + j, j);
+    }
+  }
+  wait_vmcnt<0>();
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  lds_barrier();   // every wave has read its last operands
+  static_assert(Slab<T>::BYTES <= 32768, "a slab fits a slot");
+  char GK_LDS* slab = SA[0];
+  if (w == 1) slab = SA[1];
+  if (w == 2) slab = SB[0];
+  if (w == 3) slab = SB[1];
+  epilogue<T, SPLIT>(p, acc, m0, n0, wm, wn, lane, slab,
+                     SPLIT ? p.W + (int64_t)z * p.M * p.ldw : nullptr);
+}
+
+template <int TY, bool AKM, bool BKM, bool SPLIT>
+__global__ void __launch_bounds__(256) lin_ring(LinArgs p) {
+  GK_DECLARE_RING()
+  int m0, n0;
+  const int z = tile_of<256, 256>(p, blockIdx.x, m0, n0);
+  ring_tile<TY, AKM, BKM, SPLIT>(p, m0, n0, z, SA, SB);
+}
+
+// The k slices added in order, then the epilogue; one thread per 8 columns.
+template <int TY>
+__global__ void __launch_bounds__(256) lin_reduce(LinArgs p) {
+  const uint32_t q8 = (uint32_t)(p.ldw >> 3);
+  const uint32_t t = blockIdx.x * 256u + threadIdx.x;   // M q8 < 2^31, checked on the host
+  if (t >= (uint32_t)p.M * q8) return;
+  const uint32_t row = t / q8;
+  const int col = (int)(t - row * q8) * 8;
+  const float* w = p.W + (int64_t)row * p.ldw + col;
+  const int64_t slice = (int64_t)p.M * p.ldw;
+  float4v lo = *(const float4v*)w, hi = *(const float4v*)(w + 4);
+  for (int z = 1; z < p.splits; ++z) {
+    lo += *(const float4v*)(w + z * slice);
+    hi += *(const float4v*)(w + z * slice + 4);
+  }
+  float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  finish8<TY>(p, (int)row, col, f, load_columns<TY>(p, col));
+}
+
+}  // namespace lk

@@ -1,0 +1,618 @@
+// C-ABI of the linear layer and the root-mean-square norm: argument checks, kernel choice,
+// launches.  The declarations and their contracts are in include/linear_norm.h.
+#include "linear_norm.h"
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include "linear_launch.hpp"
+#include "norm_kernels.hpp"
+
+namespace {
+
+using lk::GemmPlan;
+using lk::LinArgs;
+
+constexpr int64_t kMax = (int64_t)1 << 31;
+constexpr int kCUs = 256;
+
+int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
+int64_t round_up(int64_t x, int64_t y) { return cdiv(x, y) * y; }
+
+bool is16(int64_t type) { return type == LINEAR_NORM_F16 || type == LINEAR_NORM_BF16; }
+
+// ---- matrices ------------------------------------------------------------------------------
+// Bytes from a matrix's first element to one past its last (rows ld apart); saturating.
+struct Region {
+  const void* p;
+  uint64_t n;
+};
+Region region(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
+  if (p == nullptr || rows <= 0 || cols <= 0) return {p, 0};
+  const __int128 b = (__int128)elem * ((__int128)(rows - 1) * ld + cols);
+  return {p, b > (__int128)UINT64_MAX ? UINT64_MAX : (uint64_t)b};
+}
+bool overlap(const Region& a, const Region& b) {
+  if (a.n == 0 || b.n == 0) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x >= y ? x - y < b.n : y - x < a.n;
+}
+// Whether any of the nw written regions meets another of them or any of the nr read ones.
+bool conflict(const Region* w, int nw, const Region* r, int nr) {
+  for (int i = 0; i < nw; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(w[i], w[j])) return true;
+    for (int j = 0; j < nr; ++j)
+      if (overlap(w[i], r[j])) return true;
+  }
+  return false;
+}
+
+// A row-major matrix: row stride (of no meaning for one row) and alignment.
+int check_rows(const void* p, int64_t rows, int64_t cols, int64_t* ld, int64_t elem, bool needed) {
+  if (rows == 0 || cols == 0) return GEMM_F16F32_OK;
+  if (p == nullptr) return needed ? GEMM_F16F32_ERR_NULL : GEMM_F16F32_OK;
+  if ((uintptr_t)p % elem) return GEMM_F16F32_ERR_OPTS;
+  if (rows == 1) *ld = cols;
+  if (*ld < cols) return GEMM_F16F32_ERR_LD;
+  // byte offsets inside the matrix stay below 2^62
+  if (*ld > ((int64_t)1 << 60) / rows) return GEMM_F16F32_ERR_TOO_LARGE;
+  return GEMM_F16F32_OK;
+}
+
+// A product's operand: X rows (of a) or columns (of b), K deep, element (x, k) at
+// x * sx + k * sk.  km: k-contiguous, rows of ld; else x-contiguous, k rows of ld.
+struct Operand {
+  const void* p;
+  int64_t ld;
+  bool km;
+};
+int operand(const void* p, int64_t X, int64_t K, int64_t sx, int64_t sk, int64_t type,
+            Operand* o) {
+  const int64_t elem = type == LINEAR_NORM_E4M3 ? 1 : 2;
+  *o = {p, K > 1 ? K : 1, true};
+  if (X == 0 || K == 0) return GEMM_F16F32_OK;
+  if (p == nullptr) return GEMM_F16F32_ERR_NULL;
+  if ((uintptr_t)p % (elem == 1 ? 16 : 2)) return GEMM_F16F32_ERR_OPTS;
+  if ((sk == 1 || K == 1) && (X == 1 || sx >= K)) {
+    if (X > 1) o->ld = sx;
+  } else if (elem == 2 && (sx == 1 || X == 1) && sk >= X) {
+    o->ld = sk;
+    o->km = false;
+  } else {
+    return GEMM_F16F32_ERR_LD;
+  }
+  if (elem == 1) {
+    if (X == 1) o->ld = round_up(K, 16);
+    if (o->ld % 16) return GEMM_F16F32_ERR_LD;
+  }
+  if (o->ld > ((int64_t)1 << 60) / (o->km ? X : K)) return GEMM_F16F32_ERR_TOO_LARGE;
+  return GEMM_F16F32_OK;
+}
+Region operand_region(const Operand& o, int64_t X, int64_t K, int64_t type) {
+  const int64_t e = type == LINEAR_NORM_E4M3 ? 1 : 2;
+  return o.km ? region(o.p, X, K, o.ld, e) : region(o.p, K, X, o.ld, e);
+}
+
+// ---- matrix products -------------------------------------------------------------------------
+// Slices of k so that about all CUs have a workgroup: at most 16, each of at least `least`
+// panels.
+int slices(int64_t programs, int64_t panels, int64_t least) {
+  int s = 1;
+  while (s < 16 && programs * s * 2 <= kCUs && panels / (s * 2) >= least) s *= 2;
+  return s;
+}
+
+// The path, tile and split of an M x N x K product (M, N > 0).
+int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b,
+              GemmPlan* g) {
+  const int64_t E = type == LINEAR_NORM_E4M3 ? 2 : 1;
+  *g = {};
+  g->akm = a.km;
+  g->bkm = b.km;
+  g->ldw = round_up(N, 8);
+  const int64_t panels = cdiv(K, lk::kTileDepth * E);
+  int64_t depth = panels, least = 8;
+  if (M <= lk::kSkinnyRows && a.km) {
+    g->path = b.km ? lk::kPathSkinnyK : lk::kPathSkinnyN;
+    g->cols = b.km ? 16 : (N >= 128 * kCUs ? 128 : 64);
+    g->programs = cdiv(N, g->cols);
+    if (!b.km) depth = cdiv(K, 32);
+    least = b.km ? 32 : 64;
+    if (g->programs >= 64) least = depth + 1;
+  } else {
+    g->path = lk::kPathTiles;
+    // the largest tile whose grid about covers the CUs; panels' 32-bit offsets hold
+    auto fits = [&](int t) {
+      const lk::TileShape& s = lk::kTileShapes[t];
+      const int64_t ra = a.km ? s.bm : lk::kTileDepth, rb = b.km ? s.bn : lk::kTileDepth;
+      return ra * (a.ld / E) < kMax && rb * (b.ld / E) < kMax;
+    };
+    auto tiles = [&](int t) {
+      return cdiv(M, lk::kTileShapes[t].bm) * cdiv(N, lk::kTileShapes[t].bn);
+    };
+    g->tile = lk::kTile64;
+    if (tiles(lk::kTile128) >= 200 && fits(lk::kTile128)) g->tile = lk::kTile128;
+    if (tiles(lk::kTile256) >= 200 && fits(lk::kTile256)) g->tile = lk::kTile256;
+    if (!fits(g->tile)) return GEMM_F16F32_ERR_TOO_LARGE;
+    g->programs = tiles(g->tile);
+  }
+  g->splits = slices(g->programs, depth, least);
+  g->per_split = (int)cdiv(depth, g->splits);
+  if (g->splits > 1) g->splits = (int)cdiv(depth, g->per_split);
+  if (g->splits > 1) {
+    // the reduction's 32-bit thread index
+    if (M * (g->ldw / 8) >= kMax) return GEMM_F16F32_ERR_TOO_LARGE;
+    g->w_bytes = g->splits * M * g->ldw * 4;
+  }
+  if (g->programs * g->splits >= kMax) return GEMM_F16F32_ERR_TOO_LARGE;
+  return GEMM_F16F32_OK;
+}
+
+// The kernel arguments of a product, epilogue left empty.
+LinArgs product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b,
+                const GemmPlan& g, void* ws) {
+  const int64_t E = type == LINEAR_NORM_E4M3 ? 2 : 1;
+  LinArgs p = {};
+  p.A = (const uint16_t*)a.p;
+  p.B = (const uint16_t*)b.p;
+  p.lda = a.ld / E;
+  p.ldb = b.ld / E;
+  p.M = (int32_t)M;
+  p.N = (int32_t)N;
+  p.K = (int32_t)K;
+  if (g.path == lk::kPathTiles) {
+    p.num_pid_m = (int32_t)cdiv(M, lk::kTileShapes[g.tile].bm);
+    p.num_pid_n = (int32_t)cdiv(N, lk::kTileShapes[g.tile].bn);
+    const int group = g.tile == lk::kTile256 ? 8 : 4;
+    p.group_m = p.num_pid_m < group ? p.num_pid_m : group;
+  }
+  p.num_programs = (int32_t)g.programs;
+  p.out_type = (int32_t)type;
+  p.W = (float*)ws;
+  p.ldw = g.ldw;
+  p.splits = g.splits;
+  p.per_split = g.per_split;
+  return p;
+}
+
+int launch(int64_t type, const GemmPlan& g, const LinArgs& p, void* stream) {
+  const hipStream_t s = (hipStream_t)stream;
+  const hipError_t e = type == LINEAR_NORM_F16    ? lk::launch_type<lk::kF16>(g, p, s)
+                       : type == LINEAR_NORM_BF16 ? lk::launch_type<lk::kBF16>(g, p, s)
+                                                  : lk::launch_type<lk::kE4M3>(g, p, s);
+  return e == hipSuccess ? GEMM_F16F32_OK : GEMM_F16F32_ERR_HIP;
+}
+
+int check_workspace(const void* ws, int64_t have, int64_t need) {
+  if (need == 0) return GEMM_F16F32_OK;
+  return ws == nullptr || have < need || ((uintptr_t)ws & 15) ? GEMM_F16F32_ERR_WORKSPACE
+                                                              : GEMM_F16F32_OK;
+}
+
+bool bad_dim(int64_t d) { return d < 0 || d >= kMax; }
+
+// ---- linear_forward ----------------------------------------------------------------------------
+struct ForwardPlan {
+  Operand a, b;
+  GemmPlan g;
+  bool empty;
+};
+int plan_forward(linear_forward_args& x, ForwardPlan* f) {
+  f->empty = true;
+  f->g = {};
+  if (bad_dim(x.m) || bad_dim(x.n) || bad_dim(x.k)) return GEMM_F16F32_ERR_DIM;
+  if (!is16(x.type) && x.type != LINEAR_NORM_E4M3) return GEMM_F16F32_ERR_OPTS;
+  if (!is16(x.out_type) || (is16(x.type) && x.out_type != x.type)) return GEMM_F16F32_ERR_OPTS;
+  if (x.activation < LINEAR_ACT_NONE || x.activation > LINEAR_ACT_SILU)
+    return GEMM_F16F32_ERR_OPTS;
+  if (is16(x.type) && (x.scale_a || x.scale_b)) return GEMM_F16F32_ERR_OPTS;
+  if (x.m == 0 || x.n == 0) return GEMM_F16F32_OK;
+  f->empty = false;
+  int rc = operand(x.a, x.m, x.k, x.a_row, x.a_col, x.type, &f->a);
+  if (rc == 0) rc = operand(x.b, x.n, x.k, x.b_col, x.b_row, x.type, &f->b);
+  if (rc == 0) rc = check_rows(x.out, x.m, x.n, &x.out_row, 2, true);
+  if (rc == 0) rc = check_rows(x.pre, x.m, x.n, &x.pre_row, 2, false);
+  if (rc == 0) rc = check_rows(x.residual, x.m, x.n, &x.residual_row, 2, false);
+  if (rc != 0) return rc;
+  if (((uintptr_t)x.bias & 1) || (((uintptr_t)x.scale_a | (uintptr_t)x.scale_b) & 3))
+    return GEMM_F16F32_ERR_OPTS;
+  const Region w[] = {region(x.out, x.m, x.n, x.out_row, 2), region(x.pre, x.m, x.n, x.pre_row, 2)};
+  const Region r[] = {operand_region(f->a, x.m, x.k, x.type), operand_region(f->b, x.n, x.k, x.type),
+                      region(x.bias, 1, x.n, x.n, 2), region(x.scale_a, 1, x.m, x.m, 4),
+                      region(x.scale_b, 1, x.n, x.n, 4)};
+  if (conflict(w, 2, r, 5)) return GEMM_F16F32_ERR_OVERLAP;
+  const Region res = region(x.residual, x.m, x.n, x.residual_row, 2);
+  const bool in_place = x.residual == x.out && x.residual_row == x.out_row;
+  if (overlap(w[1], res) || (!in_place && overlap(w[0], res))) return GEMM_F16F32_ERR_OVERLAP;
+  return plan_gemm(x.type, x.m, x.n, x.k, f->a, f->b, &f->g);
+}
+
+// ---- linear_backward ----------------------------------------------------------------------------
+struct BackwardPlan {
+  bool empty, dact;          // nothing at all to do; the element-wise pass runs
+  Operand b, a, dt;          // b as da's right operand; a and dpre as db's
+  bool db_cols;              // db is column-major: the product is its transpose
+  GemmPlan gda, gdb;
+  int64_t ldd, ldp;          // dpre's row stride, the partial column sums'
+  int row_blocks, rows_per_block;
+  int64_t dpre_bytes, part_bytes, w_bytes;
+};
+int plan_backward(linear_backward_args& x, BackwardPlan* f) {
+  *f = {};
+  f->empty = true;
+  if (bad_dim(x.m) || bad_dim(x.n) || bad_dim(x.k)) return GEMM_F16F32_ERR_DIM;
+  if (!is16(x.type)) return GEMM_F16F32_ERR_OPTS;
+  if (x.activation < LINEAR_ACT_NONE || x.activation > LINEAR_ACT_SILU)
+    return GEMM_F16F32_ERR_OPTS;
+  const bool act = x.activation != LINEAR_ACT_NONE;
+  f->empty = false;
+  int rc = check_rows(x.dc, x.m, x.n, &x.dc_row, 2, true);
+  if (rc == 0 && act) rc = check_rows(x.pre, x.m, x.n, &x.pre_row, 2, true);
+  if (rc == 0) rc = check_rows(x.da, x.m, x.k, &x.da_row, 2, false);
+  if (rc != 0) return rc;
+  if ((uintptr_t)x.dbias & 1) return GEMM_F16F32_ERR_OPTS;
+  Region ra = {}, rb = {}, rdb = {};
+  if (x.da && x.m > 0 && x.k > 0) {
+    rc = operand(x.b, x.k, x.n, x.b_row, x.b_col, x.type, &f->b);
+    if (rc != 0) return rc;
+    rb = operand_region(f->b, x.k, x.n, x.type);
+  }
+  if (x.db && x.k > 0 && x.n > 0) {
+    rc = operand(x.a, x.k, x.m, x.a_col, x.a_row, x.type, &f->a);
+    if (rc != 0) return rc;
+    ra = operand_region(f->a, x.k, x.m, x.type);
+    // db's order: a unit stride along n, or along k
+    if ((x.db_col == 1 || x.n == 1) && (x.k == 1 || x.db_row >= x.n)) {
+      rc = check_rows(x.db, x.k, x.n, &x.db_row, 2, true);
+      rdb = region(x.db, x.k, x.n, x.db_row, 2);
+    } else if (x.db_row == 1 || x.k == 1) {
+      f->db_cols = true;
+      rc = check_rows(x.db, x.n, x.k, &x.db_col, 2, true);
+      rdb = region(x.db, x.n, x.k, x.db_col, 2);
+    } else {
+      rc = GEMM_F16F32_ERR_LD;
+    }
+    if (rc != 0) return rc;
+  }
+  const Region w[] = {region(x.da, x.m, x.k, x.da_row, 2), rdb, region(x.dbias, 1, x.n, x.n, 2)};
+  const Region r[] = {region(x.dc, x.m, x.n, x.dc_row, 2), ra, rb,
+                      region(act ? x.pre : nullptr, x.m, x.n, x.pre_row, 2)};
+  if (conflict(w, 3, r, 4)) return GEMM_F16F32_ERR_OVERLAP;
+
+  // the element-wise pass: dpre (rows on 128-byte lines), and blocks of rows for its column sums
+  f->dact = x.n > 0 && ((act && x.m > 0) || x.dbias);
+  if (f->dact && act) {
+    f->ldd = round_up(x.n, 64);
+    f->dpre_bytes = round_up(x.m * f->ldd * 2, 256);
+  }
+  if (f->dact) {
+    const int64_t cols = cdiv(x.n, 512);
+    int64_t blocks = cdiv(x.m, 16);
+    const int64_t most = cdiv(4 * kCUs, cols);
+    if (blocks > most) blocks = most;
+    if (blocks < 1) blocks = 1;
+    f->rows_per_block = (int)round_up(cdiv(x.m, blocks), 4);
+    f->row_blocks = x.m > 0 ? (int)cdiv(x.m, f->rows_per_block) : 0;
+    if (x.dbias) {
+      f->ldp = round_up(x.n, 8);
+      f->part_bytes = round_up(f->row_blocks * f->ldp * 4, 256);
+    }
+  }
+  const int64_t ldd = act ? f->ldd : (x.dc_row > 0 ? x.dc_row : 1);
+  if (x.da && x.m > 0 && x.k > 0) {
+    const Operand d = {x.dc, ldd, true};
+    rc = plan_gemm(x.type, x.m, x.k, x.n, d, f->b, &f->gda);
+    if (rc != 0) return rc;
+    if (f->gda.w_bytes > f->w_bytes) f->w_bytes = f->gda.w_bytes;
+  }
+  if (x.db && x.k > 0 && x.n > 0) {
+    f->dt = {x.dc, ldd, false};
+    rc = f->db_cols ? plan_gemm(x.type, x.n, x.k, x.m, f->dt, f->a, &f->gdb)
+                    : plan_gemm(x.type, x.k, x.n, x.m, f->a, f->dt, &f->gdb);
+    if (rc != 0) return rc;
+    if (f->gdb.w_bytes > f->w_bytes) f->w_bytes = f->gdb.w_bytes;
+  }
+  return GEMM_F16F32_OK;
+}
+
+// ---- norm ----------------------------------------------------------------------------------------
+constexpr int64_t kRowsPerLaunch = 1 << 21;   // 2^21 rows of up to 1024 threads
+
+int check_norm(int64_t rows, int64_t dim, int64_t type) {
+  if (bad_dim(rows) || dim < 1 || dim >= kMax) return GEMM_F16F32_ERR_DIM;
+  return is16(type) ? GEMM_F16F32_OK : GEMM_F16F32_ERR_OPTS;
+}
+
+// Waves a row and steps of 512 columns a wave that hold a row of `dim` in registers; C = 0 (long
+// rows): none.
+template <class F>
+void with_row_shape(int64_t dim, F f) {
+  if (dim <= 512) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+  else if (dim <= 1024) f(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
+  else if (dim <= 2048) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  else if (dim <= 4096) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  else if (dim <= 8192) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+  else if (dim <= 16384) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
+}
+
+template <int TY, bool Q8>
+void norm_forward(const nk::NormArgs& p, hipStream_t s) {
+  with_row_shape(p.dim, [&](auto nw, auto c) {
+    hipLaunchKernelGGL((nk::rms_norm_fwd<TY, Q8, nw.value, c.value>), dim3((uint32_t)p.rows),
+                       dim3(64 * nw.value), 0, s, p);
+  });
+}
+template <int TY>
+void norm_backward(const nk::NormBwdArgs& p, int grid, hipStream_t s) {
+  with_row_shape(p.dim, [&](auto nw, auto c) {
+    hipLaunchKernelGGL((nk::rms_norm_bwd<TY, nw.value, c.value>), dim3((uint32_t)grid),
+                       dim3(64 * nw.value), 0, s, p);
+  });
+}
+
+// Workgroups of the norm's backward pass, each with a row of partial dweight sums.
+int backward_groups(int64_t rows) { return (int)(rows < 2 * kCUs ? rows : 2 * kCUs); }
+
+int64_t norm_backward_bytes(const rms_norm_backward_args& x) {
+  return x.dweight ? backward_groups(x.rows) * round_up(x.dim, 8) * 4 : 0;
+}
+
+template <int TY>
+void launch_sum(const float* part, int64_t ldp, int n, int64_t cols, void* out, hipStream_t s) {
+  hipLaunchKernelGGL((nk::sum_partials<TY>), dim3((uint32_t)cdiv(cols, 16)), dim3(256), 0, s, part,
+                     ldp, n, (int)cols, (uint16_t*)out);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t linear_forward_workspace(const linear_forward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  linear_forward_args x = *args;
+  ForwardPlan f;
+  const int rc = plan_forward(x, &f);
+  return rc != GEMM_F16F32_OK ? rc : f.g.w_bytes;
+}
+
+int linear_forward(const linear_forward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  linear_forward_args x = *args;
+  ForwardPlan f;
+  int rc = plan_forward(x, &f);
+  if (rc != GEMM_F16F32_OK || f.empty) return rc;
+  rc = check_workspace(x.workspace, x.workspace_bytes, f.g.w_bytes);
+  if (rc != GEMM_F16F32_OK) return rc;
+  if (f.g.w_bytes > 0) {
+    const Region w = {x.workspace, (uint64_t)f.g.w_bytes};
+    const Region o[] = {region(x.out, x.m, x.n, x.out_row, 2), region(x.pre, x.m, x.n, x.pre_row, 2),
+                        region(x.residual, x.m, x.n, x.residual_row, 2),
+                        operand_region(f.a, x.m, x.k, x.type), operand_region(f.b, x.n, x.k, x.type),
+                        region(x.bias, 1, x.n, x.n, 2), region(x.scale_a, 1, x.m, x.m, 4),
+                        region(x.scale_b, 1, x.n, x.n, 4)};
+    if (conflict(&w, 1, o, 8)) return GEMM_F16F32_ERR_OVERLAP;
+  }
+  LinArgs p = product(x.type, x.m, x.n, x.k, f.a, f.b, f.g, x.workspace);
+  p.out = (uint16_t*)x.out;
+  p.ldo = x.out_row;
+  p.pre = (uint16_t*)x.pre;
+  p.ldp = x.pre_row;
+  p.res = (const uint16_t*)x.residual;
+  p.ldr = x.residual_row;
+  p.bias = (const uint16_t*)x.bias;
+  p.scale_a = x.scale_a;
+  p.scale_b = x.scale_b;
+  p.act = (int32_t)x.activation;
+  p.out_type = (int32_t)x.out_type;
+  return launch(x.type, f.g, p, x.stream);
+}
+
+int64_t linear_backward_workspace(const linear_backward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  linear_backward_args x = *args;
+  BackwardPlan f;
+  const int rc = plan_backward(x, &f);
+  return rc != GEMM_F16F32_OK ? rc : f.dpre_bytes + f.part_bytes + f.w_bytes;
+}
+
+int linear_backward(const linear_backward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  linear_backward_args x = *args;
+  BackwardPlan f;
+  int rc = plan_backward(x, &f);
+  if (rc != GEMM_F16F32_OK) return rc;
+  const int64_t need = f.dpre_bytes + f.part_bytes + f.w_bytes;
+  rc = check_workspace(x.workspace, x.workspace_bytes, need);
+  if (rc != GEMM_F16F32_OK) return rc;
+  if (need > 0) {
+    const Region w = {x.workspace, (uint64_t)need};
+    const Region o[] = {region(x.dc, x.m, x.n, x.dc_row, 2), region(x.pre, x.m, x.n, x.pre_row, 2),
+                        region(x.da, x.m, x.k, x.da_row, 2), region(x.dbias, 1, x.n, x.n, 2),
+                        operand_region(f.a, x.k, x.m, x.type), operand_region(f.b, x.k, x.n, x.type),
+                        f.db_cols ? region(x.db, x.n, x.k, x.db_col, 2)
+                                  : region(x.db, x.k, x.n, x.db_row, 2)};
+    if (conflict(&w, 1, o, 7)) return GEMM_F16F32_ERR_OVERLAP;
+  }
+  const bool bf = x.type == LINEAR_NORM_BF16;
+  const hipStream_t s = (hipStream_t)x.stream;
+  char* const ws = (char*)x.workspace;
+  const bool act = x.activation != LINEAR_ACT_NONE;
+  const void* dpre = x.dc;
+  if (f.dact) {
+    float* const part = x.dbias ? (float*)(ws + f.dpre_bytes) : nullptr;
+    if (f.row_blocks > 0) {
+      nk::DactArgs d = {};
+      d.dc = (const uint16_t*)x.dc;
+      d.dc_row = x.dc_row;
+      if (act) {
+        d.pre = (const uint16_t*)x.pre;
+        d.pre_row = x.pre_row;
+        d.dpre = (uint16_t*)ws;
+        d.dpre_row = f.ldd;
+        dpre = ws;
+      }
+      d.part = part;
+      d.ldp = f.ldp;
+      d.m = (int32_t)x.m;
+      d.n = (int32_t)x.n;
+      d.act = (int32_t)x.activation;
+      d.row_blocks = f.row_blocks;
+      d.rows_per_block = f.rows_per_block;
+      const dim3 grid((uint32_t)(cdiv(x.n, 512) * f.row_blocks));
+      if (bf)
+        hipLaunchKernelGGL((nk::lin_dact<lk::kBF16>), grid, dim3(256), 0, s, d);
+      else
+        hipLaunchKernelGGL((nk::lin_dact<lk::kF16>), grid, dim3(256), 0, s, d);
+    }
+    if (x.dbias) {
+      if (bf)
+        launch_sum<lk::kBF16>(part, f.ldp, f.row_blocks, x.n, x.dbias, s);
+      else
+        launch_sum<lk::kF16>(part, f.ldp, f.row_blocks, x.n, x.dbias, s);
+    }
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  void* const W = ws ? ws + f.dpre_bytes + f.part_bytes : nullptr;
+  if (f.gda.programs > 0) {
+    const Operand d = {dpre, act ? f.ldd : x.dc_row, true};
+    LinArgs p = product(x.type, x.m, x.k, x.n, d, f.b, f.gda, W);
+    p.out = (uint16_t*)x.da;
+    p.ldo = x.da_row;
+    rc = launch(x.type, f.gda, p, x.stream);
+    if (rc != GEMM_F16F32_OK) return rc;
+  }
+  if (f.gdb.programs > 0) {
+    Operand d = f.dt;
+    d.p = dpre;
+    LinArgs p = f.db_cols ? product(x.type, x.n, x.k, x.m, d, f.a, f.gdb, W)
+                          : product(x.type, x.k, x.n, x.m, f.a, d, f.gdb, W);
+    p.out = (uint16_t*)x.db;
+    p.ldo = f.db_cols ? x.db_col : x.db_row;
+    rc = launch(x.type, f.gdb, p, x.stream);
+  }
+  return rc;
+}
+
+int rms_norm_forward(const rms_norm_forward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  rms_norm_forward_args x = *args;
+  int rc = check_norm(x.rows, x.dim, x.type);
+  if (rc != GEMM_F16F32_OK) return rc;
+  const bool q8 = x.out_type == LINEAR_NORM_E4M3;
+  if ((!q8 && x.out_type != x.type) || !(x.eps >= 0.0) || (x.scale && !q8))
+    return GEMM_F16F32_ERR_OPTS;
+  if (x.rows == 0) return GEMM_F16F32_OK;
+  rc = check_rows(x.x, x.rows, x.dim, &x.x_row, 2, true);
+  if (rc == 0) rc = check_rows(x.residual, x.rows, x.dim, &x.residual_row, 2, false);
+  if (rc == 0) rc = check_rows(x.y, x.rows, x.dim, &x.y_row, q8 ? 1 : 2, true);
+  if (rc == 0) rc = check_rows(x.h, x.rows, x.dim, &x.h_row, 2, x.residual != nullptr);
+  if (rc != 0) return rc;
+  if (x.weight == nullptr || (q8 && x.scale == nullptr)) return GEMM_F16F32_ERR_NULL;
+  if (((uintptr_t)x.weight & 1) || (((uintptr_t)x.scale | (uintptr_t)x.rstd) & 3))
+    return GEMM_F16F32_ERR_OPTS;
+  const Region rx = region(x.x, x.rows, x.dim, x.x_row, 2);
+  const Region rr = region(x.residual, x.rows, x.dim, x.residual_row, 2);
+  const Region rh = region(x.h, x.rows, x.dim, x.h_row, 2);
+  const Region w[] = {region(x.y, x.rows, x.dim, x.y_row, q8 ? 1 : 2),
+                      region(x.scale, 1, x.rows, x.rows, 4), region(x.rstd, 1, x.rows, x.rows, 4),
+                      rh};
+  const Region r[] = {rx, rr, region(x.weight, 1, x.dim, x.dim, 2)};
+  if (conflict(w, 3, r, 3) || conflict(w, 4, r + 2, 1)) return GEMM_F16F32_ERR_OVERLAP;
+  if ((!(x.h == x.x && x.h_row == x.x_row) && overlap(rh, rx)) ||
+      (!(x.h == x.residual && x.h_row == x.residual_row) && overlap(rh, rr)))
+    return GEMM_F16F32_ERR_OVERLAP;
+  const int64_t ys = q8 ? 1 : 2;
+  for (int64_t r0 = 0; r0 < x.rows; r0 += kRowsPerLaunch) {
+    nk::NormArgs p = {};
+    p.x = (const uint16_t*)x.x + r0 * x.x_row;
+    p.x_row = x.x_row;
+    if (x.residual) p.res = (const uint16_t*)x.residual + r0 * x.residual_row;
+    p.res_row = x.residual_row;
+    p.weight = (const uint16_t*)x.weight;
+    p.y = (char*)x.y + ys * r0 * x.y_row;
+    p.y_row = x.y_row;
+    if (x.scale) p.scale = x.scale + r0;
+    if (x.h) p.h = (uint16_t*)x.h + r0 * x.h_row;
+    p.h_row = x.h_row;
+    if (x.rstd) p.rstd = x.rstd + r0;
+    p.rows = (int32_t)(x.rows - r0 < kRowsPerLaunch ? x.rows - r0 : kRowsPerLaunch);
+    p.dim = (int32_t)x.dim;
+    p.eps = (float)x.eps;
+    p.inv_dim = (float)(1.0 / (double)x.dim);
+    const hipStream_t s = (hipStream_t)x.stream;
+    if (x.type == LINEAR_NORM_BF16)
+      q8 ? norm_forward<lk::kBF16, true>(p, s) : norm_forward<lk::kBF16, false>(p, s);
+    else
+      q8 ? norm_forward<lk::kF16, true>(p, s) : norm_forward<lk::kF16, false>(p, s);
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  return GEMM_F16F32_OK;
+}
+
+int64_t rms_norm_backward_workspace(const rms_norm_backward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  const int rc = check_norm(args->rows, args->dim, args->type);
+  return rc != GEMM_F16F32_OK ? rc : norm_backward_bytes(*args);
+}
+
+int rms_norm_backward(const rms_norm_backward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  rms_norm_backward_args x = *args;
+  int rc = check_norm(x.rows, x.dim, x.type);
+  if (rc == 0) rc = check_rows(x.dy, x.rows, x.dim, &x.dy_row, 2, true);
+  if (rc == 0) rc = check_rows(x.h, x.rows, x.dim, &x.h_row, 2, true);
+  if (rc == 0) rc = check_rows(x.dh, x.rows, x.dim, &x.dh_row, 2, false);
+  if (rc == 0) rc = check_rows(x.dx, x.rows, x.dim, &x.dx_row, 2, true);
+  if (rc != 0) return rc;
+  if (x.rows > 0 && (x.weight == nullptr || x.rstd == nullptr)) return GEMM_F16F32_ERR_NULL;
+  if ((((uintptr_t)x.weight | (uintptr_t)x.dweight) & 1) || ((uintptr_t)x.rstd & 3))
+    return GEMM_F16F32_ERR_OPTS;
+  const int64_t need = norm_backward_bytes(x);
+  rc = check_workspace(x.workspace, x.workspace_bytes, need);
+  if (rc != GEMM_F16F32_OK) return rc;
+  const Region rdx = region(x.dx, x.rows, x.dim, x.dx_row, 2);
+  const Region rdy = region(x.dy, x.rows, x.dim, x.dy_row, 2);
+  const Region rdh = region(x.dh, x.rows, x.dim, x.dh_row, 2);
+  const Region w[] = {region(x.dweight, 1, x.dim, x.dim, 2), {x.workspace, (uint64_t)need}, rdx};
+  const Region r[] = {region(x.h, x.rows, x.dim, x.h_row, 2),
+                      region(x.weight, 1, x.dim, x.dim, 2), region(x.rstd, 1, x.rows, x.rows, 4),
+                      rdy, rdh};
+  if (conflict(w, 2, r, 5) || conflict(w, 3, r, 3)) return GEMM_F16F32_ERR_OVERLAP;
+  if ((!(x.dx == x.dy && x.dx_row == x.dy_row) && overlap(rdx, rdy)) ||
+      (!(x.dx == x.dh && x.dx_row == x.dh_row) && overlap(rdx, rdh)))
+    return GEMM_F16F32_ERR_OVERLAP;
+  const hipStream_t s = (hipStream_t)x.stream;
+  const bool bf = x.type == LINEAR_NORM_BF16;
+  const int groups = backward_groups(x.rows);
+  const int64_t ldp = round_up(x.dim, 8);
+  if (groups > 0) {
+    nk::NormBwdArgs p = {};
+    p.dy = (const uint16_t*)x.dy;
+    p.dy_row = x.dy_row;
+    p.h = (const uint16_t*)x.h;
+    p.h_row = x.h_row;
+    p.weight = (const uint16_t*)x.weight;
+    p.rstd = x.rstd;
+    p.dh = (const uint16_t*)x.dh;
+    p.dh_row = x.dh_row;
+    p.dx = (uint16_t*)x.dx;
+    p.dx_row = x.dx_row;
+    p.part = x.dweight ? (float*)x.workspace : nullptr;
+    p.ldp = ldp;
+    p.rows = (int32_t)x.rows;
+    p.dim = (int32_t)x.dim;
+    p.inv_dim = (float)(1.0 / (double)x.dim);
+    bf ? norm_backward<lk::kBF16>(p, groups, s) : norm_backward<lk::kF16>(p, groups, s);
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  if (x.dweight) {
+    bf ? launch_sum<lk::kBF16>((const float*)x.workspace, ldp, groups, x.dim, x.dweight, s)
+       : launch_sum<lk::kF16>((const float*)x.workspace, ldp, groups, x.dim, x.dweight, s);
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  return GEMM_F16F32_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,382 @@
+// Device code of the root-mean-square norm, its backward pass, and the element-wise part of the
+// linear layer's backward pass.  All of them move each element once; HBM bounds them.
+#pragma once
+
+#include "linear_kernels.hpp"
+
+namespace nk {
+
+using namespace lk;
+
+// Sum over the NW waves of a workgroup, given to every thread; `s` holds NW floats.
+template <int NW>
+__device__ __forceinline__ float group_sum(float v, float* s) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v += s[i];
+  }
+  return v;
+}
+template <int NW>
+__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* s) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t o = __shfl_xor(v, d);
+    v = v > o ? v : o;
+  }
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0u;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v = v > s[i] ? v : s[i];
+  }
+  return v;
+}
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* res;
+  const uint16_t* weight;
+  void* y;
+  float* scale;
+  uint16_t* h;
+  float* rstd;
+  int64_t x_row, res_row, y_row, h_row;
+  int32_t rows, dim;
+  float eps, inv_dim;
+};
+
+// scale of a row in e4m3 from the bits of its largest magnitude (NaN sorts above infinity).  A
+// row of zeros, or one that holds a NaN, takes 1.  The lower bound keeps 1 / scale finite for
+// rows below 448 2^-126.
+__device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
+  const float amax = __builtin_bit_cast(float, amax_bits);
+  return amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) {
+  return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+}
+// 8 values to e4m3, nearest, ties to even (|v| <= 448 up to the rounding of 1 / scale)
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], float inv) {
+  uint2 o;
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, hi, true);
+  o.x = (uint32_t)lo;
+  o.y = (uint32_t)hi;
+  return o;
+}
+struct __attribute__((packed)) Bytes8 {
+  uint32_t x, y;
+};
+__device__ __forceinline__ void store_e4m3x8(uint8_t* p, const float (&v)[8], float inv, int n) {
+  const uint2 q = to_e4m3x8(v, inv);
+  if (n >= 8) {
+    *(Bytes8*)p = Bytes8{q.x, q.y};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+  }
+}
+
+// One row a workgroup of 64 NW threads, 8 columns a thread at a time.  C > 0: rows of at most
+// 512 NW C columns, held in registers.  C == 0: longer rows, read again (from h, or x without a
+// residual) for each step that needs them.
+template <int TY, bool Q8, int NW, int C>
+__global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
+  __shared__ float ssum[NW];
+  __shared__ uint32_t smax[NW];
+  constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
+  const int64_t row = blockIdx.x;
+  const uint16_t* const x = p.x + row * p.x_row;
+  const uint16_t* const res = p.res ? p.res + row * p.res_row : nullptr;
+  uint16_t* const h = p.h ? p.h + row * p.h_row : nullptr;
+  const int c0 = threadIdx.x * 8;
+  const int steps = C > 0 ? C : (p.dim + STEP - 1) / STEP;
+  float hv[CR][8], wv[CR][8];
+  auto load_h = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
+    load8(v, x + col, p.dim - col, TY);
+    if (res) {
+      float r[8];
+      load8(r, res + col, p.dim - col, TY);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += r[e];
+    }
+  };
+  float sum = 0.f;
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) load_h(c0 + i * STEP, hv[i]);
+#pragma unroll
+    for (int i = 0; i < C; ++i) load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int col = c0 + i * STEP;
+      if (h && col < p.dim) store8(h + col, hv[i], p.dim - col, TY);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += hv[i][e] * hv[i][e];
+    }
+  } else {
+    for (int i = 0; i < steps; ++i) {
+      load_h(c0 + i * STEP, hv[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += hv[0][e] * hv[0][e];
+    }
+  }
+  const float rstd = 1.f / sqrtf(group_sum<NW>(sum, ssum) * p.inv_dim + p.eps);
+  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  // y of step i
+  auto norm = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
+    const int col = c0 + i * STEP;
+    float w[8];
+    if constexpr (C == 0) {
+      load_h(col, v);
+      load8(w, p.weight + col, p.dim - col, TY);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (C > 0)
+        v[e] = hv[i][e] * rstd * wv[i][e];
+      else
+        v[e] = v[e] * rstd * w[e];
+    }
+  };
+  float inv = 1.f;
+  if constexpr (Q8) {
+    uint32_t m = 0u;
+#pragma unroll CR
+    for (int i = 0; i < steps; ++i) {
+      float v[8];
+      norm(i, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = abs_bits(v[e]);   // columns past dim are 0 (their weight reads as 0)
+        m = m > b ? m : b;
+      }
+    }
+    const float scale = e4m3_scale(group_max<NW>(m, smax));
+    if (threadIdx.x == 0) p.scale[row] = scale;
+    inv = 1.f / scale;
+  }
+#pragma unroll CR
+  for (int i = 0; i < steps; ++i) {
+    const int col = c0 + i * STEP;
+    if (col >= p.dim) break;
+    float v[8];
+    norm(i, v);
+    if constexpr (Q8)
+      store_e4m3x8((uint8_t*)p.y + row * p.y_row + col, v, inv, p.dim - col);
+    else
+      store8((uint16_t*)p.y + row * p.y_row + col, v, p.dim - col, TY);
+    // h may be x's or the residual's memory: without registers it is written last
+    if constexpr (C == 0) {
+      if (h) {
+        load_h(col, v);
+        store8(h + col, v, p.dim - col, TY);
+      }
+    }
+  }
+}
+
+struct NormBwdArgs {
+  const uint16_t* dy;
+  const uint16_t* h;
+  const uint16_t* weight;
+  const float* rstd;
+  const uint16_t* dh;
+  uint16_t* dx;
+  uint16_t* dweight;
+  float* part;   // one row of partial dweight sums a workgroup, ldp floats apart
+  int64_t dy_row, h_row, dh_row, dx_row, ldp;
+  int32_t rows, dim;
+  float inv_dim;
+};
+
+// Workgroup b takes rows b, b + grid, ...; each thread keeps its columns' dweight sums in
+// registers and writes them once.  C == 0: long rows, the sums kept in the workgroup's own row
+// of the workspace instead.
+template <int TY, int NW, int C>
+__global__ void __launch_bounds__(64 * NW) rms_norm_bwd(NormBwdArgs p) {
+  __shared__ float ssum[2][NW];
+  constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
+  const int c0 = threadIdx.x * 8;
+  const int steps = C > 0 ? C : (p.dim + STEP - 1) / STEP;
+  float wv[CR][8], dw[CR][8];
+  float* const part = p.part ? p.part + blockIdx.x * p.ldp : nullptr;
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+    }
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const float rstd = p.rstd[row];
+    const uint16_t* const dy = p.dy + row * p.dy_row;
+    const uint16_t* const h = p.h + row * p.h_row;
+    const uint16_t* const dh = p.dh ? p.dh + row * p.dh_row : nullptr;
+    uint16_t* const dx = p.dx + row * p.dx_row;
+    float gv[CR][8], xv[CR][8], dv[CR][8];
+    float sum = 0.f;
+    // g and xh of step i, and dy
+    auto load = [&](int i, float (&g)[8], float (&x)[8], float (&d)[8])
+                    __attribute__((always_inline)) {
+      const int col = c0 + i * STEP, n = p.dim - col;
+      load8(d, dy + col, n, TY);
+      load8(x, h + col, n, TY);
+      float w[8];
+      if constexpr (C == 0) load8(w, p.weight + col, n, TY);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] *= rstd;
+        g[e] = d[e] * (C > 0 ? wv[C > 0 ? i : 0][e] : w[e]);
+      }
+    };
+    float dhv[CR][8];
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        load(i, gv[i], xv[i], dv[i]);
+        if (dh) load8(dhv[i], dh + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum += gv[i][e] * xv[i][e];
+          dw[i][e] += dv[i][e] * xv[i][e];
+        }
+    } else {
+      for (int i = 0; i < steps; ++i) {
+        load(i, gv[0], xv[0], dv[0]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += gv[0][e] * xv[0][e];
+      }
+    }
+    // two sets of sums in turn, so that one barrier a row is enough
+    const float mean = group_sum<NW>(sum, ssum[turn]) * p.inv_dim;
+#pragma unroll CR
+    for (int i = 0; i < steps; ++i) {
+      const int col = c0 + i * STEP, n = p.dim - col;
+      if (n <= 0) break;
+      constexpr bool R = C > 0;
+      const int j = R ? i : 0;
+      if constexpr (!R) {
+        load(i, gv[0], xv[0], dv[0]);
+        if (dh) load8(dhv[0], dh + col, n, TY);
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            part[col + e] = (row == blockIdx.x ? 0.f : part[col + e]) + dv[0][e] * xv[0][e];
+        }
+      }
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = rstd * (gv[j][e] - xv[j][e] * mean);
+        if (dh) v[e] += dhv[j][e];
+      }
+      store8(dx + col, v, n, TY);
+    }
+  }
+  if constexpr (C > 0) {
+    if (part) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int col = c0 + i * STEP;
+        if (col < p.dim) {   // ldp is a multiple of 8: whole groups
+          *(float4v*)(part + col) = float4v{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+          *(float4v*)(part + col + 4) = float4v{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+        }
+      }
+    }
+  }
+}
+
+// out[j] = the sum of n partial rows, in order within a thread and then over the 16 threads of a
+// column: 16 columns a workgroup of 256.
+template <int TY>
+__global__ void __launch_bounds__(256) sum_partials(const float* part, int64_t ldp, int n,
+                                                    int cols, uint16_t* out) {
+  __shared__ float s[16][17];
+  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int col = blockIdx.x * 16 + c;
+  float v = 0.f;
+  if (col < cols)
+    for (int i = r; i < n; i += 16) v += part[(int64_t)i * ldp + col];
+  s[r][c] = v;
+  __syncthreads();
+  if (r == 0 && col < cols) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += s[i][c];
+    out[col] = to_16(v, TY);
+  }
+}
+
+struct DactArgs {
+  const uint16_t* dc;
+  const uint16_t* pre;   // null: dpre is dc
+  uint16_t* dpre;
+  float* part;           // one row of column sums a row block, or null
+  int64_t dc_row, pre_row, dpre_row, ldp;
+  int32_t m, n, act;
+  int32_t row_blocks, rows_per_block;
+};
+
+// dpre = dc act'(pre) and its column sums over a block of rows: 512 columns a workgroup, 4 rows
+// at a time.
+template <int TY>
+__global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
+  __shared__ float s[3][512];
+  const int cb = blockIdx.x / p.row_blocks, rb = blockIdx.x - cb * p.row_blocks;
+  const int t = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int col = cb * 512 + t * 8, n = p.n - col;
+  const int r1 = (rb + 1) * p.rows_per_block < p.m ? (rb + 1) * p.rows_per_block : p.m;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  if (n > 0) {
+#pragma unroll 4
+    for (int row = rb * p.rows_per_block + g; row < r1; row += 4) {
+      float v[8];
+      load8(v, p.dc + row * p.dc_row + col, n, TY);
+      if (p.pre) {
+        float u[8];
+        load8(u, p.pre + row * p.pre_row + col, n, TY);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= act_slope(u[e], p.act);
+        store8(p.dpre + row * p.dpre_row + col, v, n, TY);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[e];
+    }
+  }
+  if (p.part == nullptr) return;
+  if (g > 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[g - 1][t * 8 + e] = sum[e];
+  }
+  __syncthreads();
+  if (g == 0 && n > 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += s[i][t * 8 + e];
+    float* const o = p.part + rb * p.ldp + col;   // ldp is a multiple of 8
+    *(float4v*)o = float4v{sum[0], sum[1], sum[2], sum[3]};
+    *(float4v*)(o + 4) = float4v{sum[4], sum[5], sum[6], sum[7]};
+  }
+}
+
+}  // namespace nk
