@@ -16,6 +16,9 @@ SO = os.path.join(PKG, "libgemm_f16f32.so")
 # The linear layer and the norm (include/linear_norm.h), a library of its own.
 LN_SRC = os.path.join(PKG, "csrc", "linear_norm.hip")
 LN_SO = os.path.join(PKG, "liblinear_norm.so")
+# Its CPython module for torch tensors (host code only).
+BINDING_SRC = os.path.join(PKG, "csrc", "torch_binding.cpp")
+BINDING_SO = os.path.join(PKG, "_linear_norm.so")
 # The matrix-core rate probe (measurement only: bench.py --mfma-ceiling).
 PROBE_SRC = os.path.join(PKG, "csrc", "mfma_ceiling.hip")
 PROBE_SO = os.path.join(PKG, "libmfma_ceiling.so")
@@ -161,11 +164,41 @@ def build_linear_norm(extra=()) -> str:
     return LN_SO
 
 
+def build_binding() -> str:
+    """Compiles the torch binding against the installed torch and liblinear_norm.so."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = BINDING_SO + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(rocm, "include"), BINDING_SRC, "-o", tmp,
+           "-L", PKG, "-l:" + os.path.basename(LN_SO), "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + os.path.join(base, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on the torch binding:\n" + r.stdout + r.stderr)
+    os.replace(tmp, BINDING_SO)
+    return BINDING_SO
+
+
 def build(extra=()) -> str:
-    """Compiles every library: the two large ones beside each other, then the rate probe."""
+    """Compiles everything: the fp16 product beside the linear layer and the norm (and their
+    binding), then the rate probe."""
     from concurrent.futures import ThreadPoolExecutor
+
+    def layer():
+        build_linear_norm(extra)
+        build_binding()
+
     with ThreadPoolExecutor(2) as pool:
-        for job in [pool.submit(_compile, SRC, SO, extra), pool.submit(build_linear_norm, extra)]:
+        for job in [pool.submit(_compile, SRC, SO, extra), pool.submit(layer)]:
             job.result()
     build_probe()
     return SO

@@ -2,6 +2,7 @@
 CPU: every call here is refused, or has nothing to launch, so pointers are only numbers."""
 import ctypes
 import os
+import struct
 
 import pytest
 
@@ -21,22 +22,26 @@ NORM = ("rows dim type out_type x x_row residual residual_row weight y y_row sca
         "eps stream").split()
 NORM_BACKWARD = ("rows dim type dy dy_row h h_row weight rstd dh dh_row dx dx_row dweight "
                  "workspace workspace_bytes stream").split()
+# the argument structures are arrays of 8-byte fields
+FORWARD_STRUCT = BACKWARD_STRUCT = struct.Struct("24q")
+NORM_STRUCT = struct.Struct("15qdq")
+NORM_BACKWARD_STRUCT = struct.Struct("17q")
 G = 1 << 44   # spacing of the made-up addresses
 
 
-def args(names, struct, base, **change):
+def args(names, layout, base, **change):
     d = dict.fromkeys(names, 0)
     d.update(base)
     d.update(change)
     assert set(d) == set(names)
-    return struct.pack(*(d[n] for n in names))
+    return layout.pack(*(d[n] for n in names))
 
 
 def forward(call="linear_forward", **change):
     base = dict(m=64, n=96, k=128, type=F16, out_type=F16, a=G, a_row=128, a_col=1, b=2 * G,
                 b_row=96, b_col=1, bias=3 * G, residual=4 * G, residual_row=96, out=5 * G,
                 out_row=96, pre=6 * G, pre_row=96)
-    return getattr(ln.lib(), call)(args(FORWARD, ln._FORWARD, base, **change))
+    return getattr(ln.lib(), call)(args(FORWARD, FORWARD_STRUCT, base, **change))
 
 
 def forward8(**change):
@@ -49,21 +54,21 @@ def backward(call="linear_backward", **change):
                 a_col=1, b=3 * G, b_row=1, b_col=128, pre=4 * G, pre_row=96, da=5 * G, da_row=128,
                 db=6 * G, db_row=1, db_col=128, dbias=7 * G, workspace=8 * G,
                 workspace_bytes=G)
-    return getattr(ln.lib(), call)(args(BACKWARD, ln._BACKWARD, base, **change))
+    return getattr(ln.lib(), call)(args(BACKWARD, BACKWARD_STRUCT, base, **change))
 
 
 def norm(**change):
     base = dict(rows=4, dim=64, type=F16, out_type=F16, x=G, x_row=64, residual=2 * G,
                 residual_row=64, weight=3 * G, y=4 * G, y_row=64, h=5 * G, h_row=64, rstd=6 * G,
                 eps=1e-5)
-    return ln.lib().rms_norm_forward(args(NORM, ln._NORM, base, **change))
+    return ln.lib().rms_norm_forward(args(NORM, NORM_STRUCT, base, **change))
 
 
 def norm_backward(call="rms_norm_backward", **change):
     base = dict(rows=4, dim=64, type=F16, dy=G, dy_row=64, h=2 * G, h_row=64, weight=3 * G,
                 rstd=4 * G, dh=5 * G, dh_row=64, dx=6 * G, dx_row=64, dweight=7 * G,
                 workspace=8 * G, workspace_bytes=G)
-    return getattr(ln.lib(), call)(args(NORM_BACKWARD, ln._NORM_BACKWARD, base, **change))
+    return getattr(ln.lib(), call)(args(NORM_BACKWARD, NORM_BACKWARD_STRUCT, base, **change))
 
 
 def test_null_arguments():
@@ -177,15 +182,15 @@ def test_structures_match_the_header():
     import re
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     text = open(os.path.join(root, "include", "linear_norm.h")).read()
-    for name, fields, struct in (("linear_forward_args", FORWARD, ln._FORWARD),
-                                 ("linear_backward_args", BACKWARD, ln._BACKWARD),
-                                 ("rms_norm_forward_args", NORM, ln._NORM),
-                                 ("rms_norm_backward_args", NORM_BACKWARD, ln._NORM_BACKWARD)):
+    for name, fields, layout in (("linear_forward_args", FORWARD, FORWARD_STRUCT),
+                                 ("linear_backward_args", BACKWARD, BACKWARD_STRUCT),
+                                 ("rms_norm_forward_args", NORM, NORM_STRUCT),
+                                 ("rms_norm_backward_args", NORM_BACKWARD, NORM_BACKWARD_STRUCT)):
         body = re.search(r"typedef struct " + name + r" \{(.*?)\} ", text, re.S).group(1)
         body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
         found = [re.sub(r".*[ *]", "", f.strip()) for line in body.split(";") if line.strip()
                  for f in line.split(",")]
-        assert found == fields and struct.size == 8 * len(fields)
+        assert found == fields and layout.size == 8 * len(fields)
     assert ctypes.sizeof(ctypes.c_void_p) == 8
 
 
