@@ -158,6 +158,36 @@ __device__ __forceinline__ float act_slope(float v, int act) {
   }
 }
 
+// The choice is made once for 8 values: made for each, its branches cost more than the values.
+__device__ __forceinline__ void act8(float (&v)[8], int act) {
+#define LK_ACT8(A)                                              \
+  case A:                                                       \
+    _Pragma("unroll") for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], A); \
+    break;
+  switch (act) {
+    LK_ACT8(LINEAR_ACT_RELU)
+    LK_ACT8(LINEAR_ACT_GELU)
+    LK_ACT8(LINEAR_ACT_GELU_TANH)
+    LK_ACT8(LINEAR_ACT_SILU)
+    default: break;
+  }
+#undef LK_ACT8
+}
+__device__ __forceinline__ void slope8(float (&v)[8], const float (&u)[8], int act) {
+#define LK_SLOPE8(A)                                                 \
+  case A:                                                            \
+    _Pragma("unroll") for (int e = 0; e < 8; ++e) v[e] *= act_slope(u[e], A); \
+    break;
+  switch (act) {
+    LK_SLOPE8(LINEAR_ACT_RELU)
+    LK_SLOPE8(LINEAR_ACT_GELU)
+    LK_SLOPE8(LINEAR_ACT_GELU_TANH)
+    LK_SLOPE8(LINEAR_ACT_SILU)
+    default: break;
+  }
+#undef LK_SLOPE8
+}
+
 // ---- epilogue ------------------------------------------------------------------------------
 // 8 consecutive columns of one row: v holds the sums.  `bias8` and `sb8` are the columns' bias
 // and scales (0 and 1 where there are none).
@@ -198,10 +228,7 @@ __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, floa
     for (int e = 0; e < 8; ++e) v[e] += c.bias[e];
   }
   if (p.pre) store8(p.pre + (int64_t)row * p.ldp + col, v, c.n, ot);
-  if (p.act != LINEAR_ACT_NONE) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], p.act);
-  }
+  act8(v, p.act);
   if (p.res) {
     float r[8];
     load8(r, p.res + (int64_t)row * p.ldr + col, c.n, ot);
@@ -541,11 +568,17 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, in
   lds_barrier();     // every wave has read its last operands
   constexpr int PER = (T::NW + NS - 1) / NS;   // slabs per stage
   static_assert(PER * Slab<T>::BYTES <= T::STAGE, "slabs fit the stages");
-  char GK_LDS* slab = S[0];
+  // The wave's stage, chosen among opaque addresses: recognised as S[w % NS], the compiler puts S
+  // itself into LDS and has every workgroup read its dispatch packet from host memory for the
+  // workgroup's shape, about 0.5 us a workgroup, one after the other.
+  uint32_t slab_at = 0;
 #pragma unroll
-  for (int j = 1; j < NS; ++j)
-    if (w % NS == j) slab = S[j];
-  slab += (w / NS) * Slab<T>::BYTES;
+  for (int j = 0; j < NS; ++j) {
+    uint32_t at = (uint32_t)(uintptr_t)S[j];
+    asm volatile("" : "+s"(at));
+    if (w % NS == j) slab_at = at;
+  }
+  char GK_LDS* const slab = (char GK_LDS*)(uintptr_t)slab_at + (w / NS) * Slab<T>::BYTES;
   epilogue<T, SPLIT>(p, acc, m0, n0, wm, wn, lane, slab,
                      SPLIT ? p.W + (int64_t)z * p.M * p.ldw : nullptr);
 }
@@ -560,14 +593,12 @@ __global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
   __shared__ __attribute__((aligned(16))) char stage1[T::STAGE];
   __shared__ __attribute__((aligned(16))) char stage2[NS > 2 ? T::STAGE : 16];
   __shared__ __attribute__((aligned(16))) char stage3[NS > 3 ? T::STAGE : 16];
-  static_assert(NS == 2 || NS == 4, "stages");
+  static_assert(NS >= 2 && NS <= 4, "stages");
   char GK_LDS* S[NS];
   S[0] = (char GK_LDS*)stage0;
   S[1] = (char GK_LDS*)stage1;
-  if constexpr (NS > 2) {
-    S[2] = (char GK_LDS*)stage2;
-    S[3] = (char GK_LDS*)stage3;
-  }
+  if constexpr (NS > 2) S[2] = (char GK_LDS*)stage2;
+  if constexpr (NS > 3) S[3] = (char GK_LDS*)stage3;
   int m0, n0;
   const int z = tile_of<BM, BN>(p, blockIdx.x, m0, n0);
   staged_tile<T, NS, RD, AKM, BKM, SPLIT>(p, m0, n0, z, S);

@@ -354,8 +354,7 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
       if (p.pre) {
         float u[8];
         load8(u, p.pre + row * p.pre_row + col, n, TY);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= act_slope(u[e], p.act);
+        slope8(v, u, p.act);
         store8(p.dpre + row * p.dpre_row + col, v, n, TY);
       }
 #pragma unroll
