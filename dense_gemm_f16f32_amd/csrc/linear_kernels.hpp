@@ -32,6 +32,9 @@ using gk::u32x4;
 using gk::wait_vmcnt;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float2v __attribute__((ext_vector_type(2)));
 typedef int int8v __attribute__((ext_vector_type(8)));
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes at any 16-bit element
@@ -76,8 +79,11 @@ __device__ __forceinline__ void unpack8(float (&f)[8], u32x4 v, int type) {
 __device__ __forceinline__ u32x4 pack8(const float (&f)[8], int type) {
   u32x4 v;
 #pragma unroll
-  for (int d = 0; d < 4; ++d)
-    v[d] = (uint32_t)to_16(f[2 * d], type) | ((uint32_t)to_16(f[2 * d + 1], type) << 16);
+  for (int d = 0; d < 4; ++d) {
+    const float2v x = {f[2 * d], f[2 * d + 1]};
+    v[d] = type == kF16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(x, half2v))
+                        : __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+  }
   return v;
 }
 // 8 values at p, of which the first n exist (n >= 8: all); the others read as 0.
@@ -158,20 +164,21 @@ __device__ __forceinline__ float act_slope(float v, int act) {
   }
 }
 
-// The choice is made once for 8 values: made for each, its branches cost more than the values.
-__device__ __forceinline__ void act8(float (&v)[8], int act) {
-#define LK_ACT8(A)                                              \
+// The choice is made once for several values: made for each, its branches cost more than the values.
+template <int N>
+__device__ __forceinline__ void act_n(float (&v)[N], int act) {
+#define LK_ACT(A)                                              \
   case A:                                                       \
-    _Pragma("unroll") for (int e = 0; e < 8; ++e) v[e] = act_value(v[e], A); \
+    _Pragma("unroll") for (int e = 0; e < N; ++e) v[e] = act_value(v[e], A); \
     break;
   switch (act) {
-    LK_ACT8(LINEAR_ACT_RELU)
-    LK_ACT8(LINEAR_ACT_GELU)
-    LK_ACT8(LINEAR_ACT_GELU_TANH)
-    LK_ACT8(LINEAR_ACT_SILU)
+    LK_ACT(LINEAR_ACT_RELU)
+    LK_ACT(LINEAR_ACT_GELU)
+    LK_ACT(LINEAR_ACT_GELU_TANH)
+    LK_ACT(LINEAR_ACT_SILU)
     default: break;
   }
-#undef LK_ACT8
+#undef LK_ACT
 }
 __device__ __forceinline__ void slope8(float (&v)[8], const float (&u)[8], int act) {
 #define LK_SLOPE8(A)                                                 \
@@ -228,7 +235,7 @@ __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, floa
     for (int e = 0; e < 8; ++e) v[e] += c.bias[e];
   }
   if (p.pre) store8(p.pre + (int64_t)row * p.ldp + col, v, c.n, ot);
-  act8(v, p.act);
+  act_n(v, p.act);
   if (p.res) {
     float r[8];
     load8(r, p.res + (int64_t)row * p.ldr + col, c.n, ot);
@@ -270,17 +277,20 @@ __device__ __forceinline__ typename T::Frag read_frag(const char GK_LDS* st,
   }
 }
 
+// The blocks are computed transposed (b's columns as the rows of the product): a lane then holds
+// 4 consecutive columns of one row of the result -- with XB = 16, row l % 16, columns 4 (l / 16)
+// + v; with XB = 32, row l % 32, columns 8 (v / 4) + 4 (l / 32) + v % 4.
 template <class T>
 __device__ __forceinline__ void mma(typename T::Acc& acc, const typename T::Frag& a,
                                     const typename T::Frag& b) {
-  if constexpr (T::TY == kF16 && T::XB == 32)
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a),
-                                                 __builtin_bit_cast(half8, b), acc, 0, 0, 0);
-  else if constexpr (T::TY == kBF16 && T::XB == 32)
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                  __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
-  else if constexpr (T::TY == kE4M3 && T::XB == 32)
-    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 0, 0, 0, 0, 0, 0);
+  if constexpr (T::TY == kF16)
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, b),
+                                                 __builtin_bit_cast(half8, a), acc, 0, 0, 0);
+  else if constexpr (T::TY == kBF16)
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
+                                                  __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
+  else
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, 0, 0, 0, 0, 0, 0);
 }
 
 // In place on accumulator registers (see mfma16 in gemm_kernels.hpp, whose wait states and
@@ -290,11 +300,11 @@ __device__ __forceinline__ void mma_inplace(typename T::Acc& acc, const typename
                                             const typename T::Frag& b) {
 #if defined(__HIP_DEVICE_COMPILE__)
   if constexpr (T::TY == kF16)
-    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
   else if constexpr (T::TY == kBF16)
-    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
   else
-    asm volatile("v_mfma_f32_32x32x64_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    asm volatile("v_mfma_f32_32x32x64_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 #else
   (void)acc, (void)a, (void)b;   // the host has no such registers
 #endif
@@ -372,13 +382,14 @@ struct Loader {
 };
 
 // ---- a wave's block of sums, through LDS ---------------------------------------------------
-// 32 rows at a time: written as the MFMA leaves them, read as 8 columns a lane.  A row of the
-// slab is 4 floats longer than the block, which puts the 4-row groups that a wave writes at
-// once on different banks.
+// 32 rows at a time: written in 4-column pieces as the MFMA leaves them, read as 8 columns a
+// lane.  A row of the slab is 4 floats longer than the block, which puts the 16 rows that a
+// wave writes in one LDS cycle on different banks.
 template <class T>
 struct Slab {
   static constexpr int LDW = T::WTN + 4, BYTES = 32 * LDW * 4;
   static constexpr int LANES = T::WTN / 8, ROWS = 64 / LANES, ITERS = 32 / ROWS;
+  static constexpr int U = ITERS < 4 ? ITERS : 4;   // rows of a lane in flight
 };
 
 template <class T, bool SPLIT>
@@ -387,12 +398,16 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
                                          char GK_LDS* slab, float* W) {
   using S = Slab<T>;
   constexpr int RB = 32 / T::XB;   // MFMA rows of blocks in a slab
+  constexpr int U = S::U;
   float GK_LDS* const s = (float GK_LDS*)slab;
   const int rr = lane / S::LANES, cc = (lane % S::LANES) * 8;
   const int col = n0 + wn * T::WTN + cc;
-  const int row0 = m0 + wm * T::WTM;
+  const int row0 = m0 + wm * T::WTM + rr;
+  const bool whole = m0 + T::BM <= p.M && n0 + T::BN <= p.N;
+  const int ot = T::TY == kE4M3 ? p.out_type : T::TY;
   Columns c;
   if constexpr (!SPLIT) c = load_columns<T::TY>(p, col);
+  const float GK_LDS* const sr = s + rr * S::LDW + cc;
 #pragma unroll
   for (int t = 0; t < T::TM / RB; ++t) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slab's last reads are done
@@ -401,28 +416,73 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
 #pragma unroll
       for (int tn = 0; tn < T::TN; ++tn)
 #pragma unroll
-        for (int v = 0; v < T::VN; ++v) {
-          const int r = T::XB == 16 ? b * 16 + 4 * (lane >> 4) + v
-                                    : 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-          s[r * S::LDW + tn * T::XB + (lane & (T::XB - 1))] = acc[t * RB + b][tn][v];
+        for (int v = 0; v < T::VN; v += 4) {
+          const int r = b * 16 + (lane & (T::XB - 1));
+          const int x = tn * T::XB + (T::XB == 16 ? 4 * (lane >> 4) : 2 * v + 4 * (lane >> 5));
+          const typename T::Acc& q = acc[t * RB + b][tn];
+          *(float4v GK_LDS*)(s + r * S::LDW + x) = float4v{q[v], q[v + 1], q[v + 2], q[v + 3]};
         }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int row_t = row0 + t * 32;
+    if (SPLIT || !whole) {
 #pragma unroll 1
-    for (int i = 0; i < S::ITERS; ++i) {
-      const int r = i * S::ROWS + rr;
-      const int row = row0 + t * 32 + r;
-      const float4v lo = *(const float4v GK_LDS*)(s + r * S::LDW + cc);
-      const float4v hi = *(const float4v GK_LDS*)(s + r * S::LDW + cc + 4);
-      if (row < p.M && col < p.N) {
-        if constexpr (SPLIT) {   // ldw is a multiple of 8: whole groups
-          float* const w = W + (int64_t)row * p.ldw + col;
-          *(float4v*)w = lo;
-          *(float4v*)(w + 4) = hi;
-        } else {
-          float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          finish8<T::TY>(p, row, col, f, c);
+      for (int i = 0; i < S::ITERS; ++i) {
+        const int row = row_t + i * S::ROWS;
+        const float4v lo = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW);
+        const float4v hi = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW + 4);
+        if (row < p.M && col < p.N) {
+          if constexpr (SPLIT) {   // ldw is a multiple of 8: whole groups
+            float* const w = W + (int64_t)row * p.ldw + col;
+            *(float4v*)w = lo;
+            *(float4v*)(w + 4) = hi;
+          } else {
+            float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            finish8<T::TY>(p, row, col, f, c);
+          }
         }
       }
+      continue;
+    }
+    // a tile inside the matrix: no bounds, U rows of a lane at once
+#pragma unroll 1
+    for (int i = 0; i < S::ITERS; i += U) {
+      float f[U * 8];
+      u32x4 res[U];
+      float sa[U];
+      const int64_t row = row_t + i * S::ROWS;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (T::TY == kE4M3) sa[u] = p.scale_a ? p.scale_a[row + u * S::ROWS] : 1.f;
+        if (p.res) res[u] = *(const u32x4_any*)(p.res + (row + u * S::ROWS) * p.ldr + col);
+        const float GK_LDS* const q = sr + (i + u) * S::ROWS * S::LDW;
+        const float4v lo = *(const float4v GK_LDS*)q, hi = *(const float4v GK_LDS*)(q + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = e < 4 ? lo[e & 3] : hi[e & 3];
+          f[u * 8 + e] = T::TY == kE4M3 ? v * (sa[u] * c.sb[e]) + c.bias[e] : v + c.bias[e];
+        }
+      }
+      auto put = [&](uint16_t* base, int64_t ld) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = f[u * 8 + e];
+          *(u32x4_any*)(base + (row + u * S::ROWS) * ld + col) = pack8(v, ot);
+        }
+      };
+      if (p.pre) put(p.pre, p.ldp);
+      act_n(f, p.act);
+      if (p.res) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float r[8];
+          unpack8(r, res[u], ot);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[u * 8 + e] += r[e];
+        }
+      }
+      put(p.out, p.ldo);
     }
   }
 }
