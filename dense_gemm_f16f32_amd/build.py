@@ -70,7 +70,7 @@ def _asm_mfma_kernel(name: str) -> bool:
         "gemm_generic" not in name or "ELi2ELi2ELb" in name)
 
 
-def disassemble(so_path: str) -> str:
+def disassemble(so_path: str, *options: str) -> str:
     """AMD assembly of the gfx950 code object inside a library built here."""
     import tempfile
     with tempfile.TemporaryDirectory() as d:
@@ -81,7 +81,8 @@ def disassemble(so_path: str) -> str:
         subprocess.run([os.path.join(LLVM, "clang-offload-bundler"), "--unbundle", "--type=o",
                         f"--input={fat}", "--targets=hipv4-amdgcn-amd-amdhsa--gfx950",
                         f"--output={co}"], check=True, capture_output=True)
-        return subprocess.run([os.path.join(LLVM, "llvm-objdump"), "-d", "--mcpu=gfx950", co],
+        return subprocess.run([os.path.join(LLVM, "llvm-objdump"), *(options or ("-d",)),
+                               "--mcpu=gfx950", co],
                               check=True, capture_output=True, text=True).stdout
 
 
@@ -130,6 +131,20 @@ def check_mfma_waits(so_path: str) -> int:
     return checked
 
 
+def kernels_with_private_arrays(so_path: str) -> list:
+    """Kernels of a library built here that keep an array in scratch memory, or in LDS by thread:
+    for the latter the compiler has every workgroup read its dispatch packet, which lies in host
+    memory (about 0.5 us a workgroup, one after the other)."""
+    import re
+    text = disassemble(so_path, "-D", "-j", ".rodata")
+    found = []
+    for block in text.split(".amdhsa_kernel ")[1:]:
+        field = dict(re.findall(r"\.amdhsa_(\w+) (\d+)", block.split(".end_amdhsa_kernel")[0]))
+        if field["private_segment_fixed_size"] != "0" or field["user_sgpr_dispatch_ptr"] != "0":
+            found.append(block.split()[0])
+    return found
+
+
 def _compile(src: str, so: str, extra=()) -> int:
     """Compiles one library, checks it and moves it in place; returns the number of its kernels
     whose asm-MFMA wait states were checked."""
@@ -161,6 +176,9 @@ def _compile(src: str, so: str, extra=()) -> int:
 def build_linear_norm(extra=()) -> str:
     """Compiles the linear layer and the norm (liblinear_norm.so)."""
     _compile(LN_SRC, LN_SO, extra)
+    found = kernels_with_private_arrays(LN_SO)
+    if found:
+        raise RuntimeError("kernels with arrays in memory: " + ", ".join(found))
     return LN_SO
 
 

@@ -46,7 +46,7 @@ struct LinArgs {
   const uint16_t* B;
   int64_t lda, ldb;       // slots
   int32_t M, N, K;        // K in elements
-  int32_t num_pid_m, num_pid_n, group_m, num_programs;
+  int32_t num_pid_m, num_pid_n, group_m, num_programs, xcd_remap;
   // epilogue; the pointers may be null, except out
   uint16_t* out;
   uint16_t* pre;
@@ -56,12 +56,26 @@ struct LinArgs {
   const float* scale_b;
   int64_t ldo, ldp, ldr;
   int32_t act, out_type;
-  // split K: slice z sums its panels into W[z][i][j] at W + (z M + i) ldw + j (ldw a multiple
-  // of 8); slices have `per_split` panels, the last one the rest
+  // Split K: the tiles from `first_split` on (all, some or none) are computed in `splits` slices
+  // of k, `per_split` panels each, the last one the rest.  Slice z of the i-th of them leaves
+  // its sums in W, a BM x BN block at (i splits + z) BM BN; lin_reduce adds the slices.
   float* W;
-  int64_t ldw;
-  int32_t splits, per_split;
+  int32_t first_split, splits, per_split;
 };
+
+// A workgroup's tile and k slice: the whole tiles first, then the slices, all tiles of slice 0,
+// all of slice 1 ...
+struct Work {
+  int tile, z;       // z < 0: the whole k range
+  float* w;          // the slice's block of W
+};
+template <int BM, int BN>
+__device__ __forceinline__ Work work_of(const LinArgs& p, int h) {
+  if (h < p.first_split) return {h, -1, nullptr};
+  const int r = p.num_programs - p.first_split, u = h - p.first_split;
+  const int z = u / r, i = u - z * r;
+  return {p.first_split + i, z, p.W + ((int64_t)i * p.splits + z) * (BM * BN)};
+}
 
 // ---- 16-bit values ---------------------------------------------------------------------
 __device__ __forceinline__ float to_f32(uint16_t v, int type) {
@@ -392,10 +406,10 @@ struct Slab {
   static constexpr int U = ITERS < 4 ? ITERS : 4;   // rows of a lane in flight
 };
 
-template <class T, bool SPLIT>
+template <class T>
 __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc (&acc)[T::TM][T::TN],
                                          int m0, int n0, int wm, int wn, int lane,
-                                         char GK_LDS* slab, float* W) {
+                                         char GK_LDS* slab, float* W) {   // W: a slice's block, or null
   using S = Slab<T>;
   constexpr int RB = 32 / T::XB;   // MFMA rows of blocks in a slab
   constexpr int U = S::U;
@@ -405,8 +419,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
   const int row0 = m0 + wm * T::WTM + rr;
   const bool whole = m0 + T::BM <= p.M && n0 + T::BN <= p.N;
   const int ot = T::TY == kE4M3 ? p.out_type : T::TY;
-  Columns c;
-  if constexpr (!SPLIT) c = load_columns<T::TY>(p, col);
+  const Columns c = load_columns<T::TY>(p, col);
   const float GK_LDS* const sr = s + rr * S::LDW + cc;
 #pragma unroll
   for (int t = 0; t < T::TM / RB; ++t) {
@@ -424,21 +437,25 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
         }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int row_t = row0 + t * 32;
-    if (SPLIT || !whole) {
+    if (W != nullptr) {
+      float* const w = W + (int64_t)(wm * T::WTM + t * 32 + rr) * T::BN + wn * T::WTN + cc;
+#pragma unroll
+      for (int i = 0; i < S::ITERS; ++i) {
+        const float GK_LDS* const q = sr + i * S::ROWS * S::LDW;
+        *(float4v*)(w + i * S::ROWS * T::BN) = *(const float4v GK_LDS*)q;
+        *(float4v*)(w + i * S::ROWS * T::BN + 4) = *(const float4v GK_LDS*)(q + 4);
+      }
+      continue;
+    }
+    if (!whole) {
 #pragma unroll 1
       for (int i = 0; i < S::ITERS; ++i) {
         const int row = row_t + i * S::ROWS;
         const float4v lo = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW);
         const float4v hi = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW + 4);
         if (row < p.M && col < p.N) {
-          if constexpr (SPLIT) {   // ldw is a multiple of 8: whole groups
-            float* const w = W + (int64_t)row * p.ldw + col;
-            *(float4v*)w = lo;
-            *(float4v*)(w + 4) = hi;
-          } else {
-            float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            finish8<T::TY>(p, row, col, f, c);
-          }
+          float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          finish8<T::TY>(p, row, col, f, c);
         }
       }
       continue;
@@ -505,24 +522,22 @@ __device__ __forceinline__ Panels panels_of(int K) {
   return q;
 }
 
-// Program -> tile and k slice: programs are z-major, each slice the whole grouped map.
+// Corner of a tile.
 template <int BM, int BN>
-__device__ __forceinline__ int tile_of(const LinArgs& p, int h, int& m0, int& n0) {
-  const int z = h / p.num_programs;
+__device__ __forceinline__ void corner_of(const LinArgs& p, int tile, int& m0, int& n0) {
   int pid, pid_m, pid_n;
-  gk::program_tile(h - z * p.num_programs, p.num_programs, p.num_pid_m, p.num_pid_n, p.group_m, 1,
-                   pid, pid_m, pid_n);
+  gk::program_tile(tile, p.num_programs, p.num_pid_m, p.num_pid_n, p.group_m,
+                   p.xcd_remap, pid, pid_m, pid_n);
   m0 = pid_m * BM;
   n0 = pid_n * BN;
-  return z;
 }
 
 // ---------------------------------------------------------------------------------------
 // Staged tile: NS LDS stages, operands read RD k steps ahead, one barrier per panel; panels
 // past the end are empty (zeros, no memory touched).
 // ---------------------------------------------------------------------------------------
-template <class T, int NS, int RD, bool AKM, bool BKM, bool SPLIT>
-__device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, int z,
+template <class T, int NS, int RD, bool AKM, bool BKM>
+__device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, const Work& k,
                                             char GK_LDS* const (&S)[NS]) {
   using OA = typename T::OA;
   using OB = typename T::OB;
@@ -534,8 +549,8 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, in
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w / T::WN, wn = w % T::WN;
   const Panels q = panels_of<T::TY, BK>(p.K);
-  const int s0 = SPLIT ? z * p.per_split : 0;
-  const int s1 = SPLIT ? (s0 + p.per_split < q.np ? s0 + p.per_split : q.np) : q.np;
+  const int s0 = k.z < 0 ? 0 : k.z * p.per_split;
+  const int s1 = k.z >= 0 && s0 + p.per_split < q.np ? s0 + p.per_split : q.np;
   const int np = s1 - s0;   // this slice's panels (at least one if split)
 
   Loader<OA> la;
@@ -639,12 +654,10 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, in
     if (w % NS == j) slab_at = at;
   }
   char GK_LDS* const slab = (char GK_LDS*)(uintptr_t)slab_at + (w / NS) * Slab<T>::BYTES;
-  epilogue<T, SPLIT>(p, acc, m0, n0, wm, wn, lane, slab,
-                     SPLIT ? p.W + (int64_t)z * p.M * p.ldw : nullptr);
+  epilogue<T>(p, acc, m0, n0, wm, wn, lane, slab, k.w);
 }
 
-template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM,
-          bool SPLIT>
+template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM>
 __global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
   using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32>;
   // stages as separate LDS objects (a refill of one is then seen not to touch another), their
@@ -660,8 +673,9 @@ __global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
   if constexpr (NS > 2) S[2] = (char GK_LDS*)stage2;
   if constexpr (NS > 3) S[3] = (char GK_LDS*)stage3;
   int m0, n0;
-  const int z = tile_of<BM, BN>(p, blockIdx.x, m0, n0);
-  staged_tile<T, NS, RD, AKM, BKM, SPLIT>(p, m0, n0, z, S);
+  const Work k = work_of<BM, BN>(p, blockIdx.x);
+  corner_of<BM, BN>(p, k.tile, m0, n0);
+  staged_tile<T, NS, RD, AKM, BKM>(p, m0, n0, k, S);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -670,8 +684,8 @@ __global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
 // hand -- see ring_tile in gemm_kernels.hpp, whose order of loads, reads and barriers this is.
 // 16-bit types: 64 MFMAs of 16x16x32 a step; e4m3: 16 of 32x32x64, the same cycles.
 // ---------------------------------------------------------------------------------------
-template <int TY, bool AKM, bool BKM, bool SPLIT>
-__device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, int z,
+template <int TY, bool AKM, bool BKM>
+__device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, const Work& k,
                                           char GK_LDS* const (&SA)[2],
                                           char GK_LDS* const (&SB)[3]) {
   using T = Tile<TY, 256, 256, 64, AKM, BKM, 2, 2, TY == kE4M3 ? 32 : 16>;
@@ -686,8 +700,8 @@ __device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, int 
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w / 2, wn = w % 2;
   const Panels q = panels_of<TY, BK>(p.K);
-  const int s0 = SPLIT ? z * p.per_split : 0;
-  const int s1 = SPLIT ? (s0 + p.per_split < q.np ? s0 + p.per_split : q.np) : q.np;
+  const int s0 = k.z < 0 ? 0 : k.z * p.per_split;
+  const int s1 = k.z >= 0 && s0 + p.per_split < q.np ? s0 + p.per_split : q.np;
   const int np = s1 - s0;
   Loader<OA> la;
   Loader<OB> lb;
@@ -797,35 +811,38 @@ __device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, int 
   if (w == 1) slab = SA[1];
   if (w == 2) slab = SB[0];
   if (w == 3) slab = SB[1];
-  epilogue<T, SPLIT>(p, acc, m0, n0, wm, wn, lane, slab,
-                     SPLIT ? p.W + (int64_t)z * p.M * p.ldw : nullptr);
+  epilogue<T>(p, acc, m0, n0, wm, wn, lane, slab, k.w);
 }
 
-template <int TY, bool AKM, bool BKM, bool SPLIT>
+template <int TY, bool AKM, bool BKM>
 __global__ void __launch_bounds__(256) lin_ring(LinArgs p) {
   GK_DECLARE_RING()
   int m0, n0;
-  const int z = tile_of<256, 256>(p, blockIdx.x, m0, n0);
-  ring_tile<TY, AKM, BKM, SPLIT>(p, m0, n0, z, SA, SB);
+  const Work k = work_of<256, 256>(p, blockIdx.x);
+  corner_of<256, 256>(p, k.tile, m0, n0);
+  ring_tile<TY, AKM, BKM>(p, m0, n0, k, SA, SB);
 }
 
-// The k slices added in order, then the epilogue; one thread per 8 columns.
-template <int TY>
+// The k slices of the split tiles added in order, then the epilogue; a thread per 8 columns, 256
+// threads a workgroup, `per_tile` workgroups a BM x BN tile (the last one not always full).
+template <int TY, int BM, int BN>
 __global__ void __launch_bounds__(256) lin_reduce(LinArgs p) {
-  const uint32_t q8 = (uint32_t)(p.ldw >> 3);
-  const uint32_t t = blockIdx.x * 256u + threadIdx.x;   // M q8 < 2^31, checked on the host
-  if (t >= (uint32_t)p.M * q8) return;
-  const uint32_t row = t / q8;
-  const int col = (int)(t - row * q8) * 8;
-  const float* w = p.W + (int64_t)row * p.ldw + col;
-  const int64_t slice = (int64_t)p.M * p.ldw;
+  constexpr int Q = BN / 8, PER = (BM * Q + 255) / 256;
+  const int i = blockIdx.x / PER, t = (blockIdx.x - i * PER) * 256 + threadIdx.x;
+  if (t >= BM * Q) return;
+  int m0, n0;
+  corner_of<BM, BN>(p, p.first_split + i, m0, n0);
+  const int r = t / Q, c = (t - r * Q) * 8, row = m0 + r, col = n0 + c;
+  if (row >= p.M || col >= p.N) return;
+  const float* w = p.W + (int64_t)i * p.splits * (BM * BN) + r * BN + c;
   float4v lo = *(const float4v*)w, hi = *(const float4v*)(w + 4);
+#pragma unroll 4
   for (int z = 1; z < p.splits; ++z) {
-    lo += *(const float4v*)(w + z * slice);
-    hi += *(const float4v*)(w + z * slice + 4);
+    lo += *(const float4v*)(w + (int64_t)z * (BM * BN));
+    hi += *(const float4v*)(w + (int64_t)z * (BM * BN) + 4);
   }
   float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  finish8<TY>(p, (int)row, col, f, load_columns<TY>(p, col));
+  finish8<TY>(p, row, col, f, load_columns<TY>(p, col));
 }
 
 }  // namespace lk

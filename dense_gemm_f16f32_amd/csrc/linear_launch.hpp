@@ -17,70 +17,82 @@ constexpr int kTileDepth = 64;   // slots
 enum { kPathTiles, kPathSkinnyK, kPathSkinnyN };
 constexpr int kSkinnyRows = 16;   // rows of the skinny kernels' one MFMA block
 
-// How one matrix product runs.
+// How one matrix product runs: `programs` workgroups a pass over the result, of which those from
+// `whole` on are split into `splits` slices of `per_split` panels (tiles) or units (skinny) of
+// k, with w_bytes of workspace for their sums.
 struct GemmPlan {
   int path, tile, cols;   // cols: skinny columns a workgroup
   bool akm, bkm;
-  int splits, per_split;  // per_split in panels (tiles) or units (skinny)
-  int64_t programs;       // workgroups of one slice
-  int64_t ldw, w_bytes;   // split K's partial sums (0: none)
+  int64_t programs, whole;
+  int splits, per_split;
+  int64_t w_bytes;
+  int64_t grid() const { return whole + (programs - whole) * splits; }
 };
 
-template <int TY, bool AKM, bool BKM, bool SPLIT>
+template <int TY, bool AKM, bool BKM>
 void launch_tile(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
   // operands of a panel are read as many k steps ahead as a panel of the type has, less one
   constexpr int RD = TY == kE4M3 ? 1 : 3;
   switch (g.tile) {
     case kTile256:
-      hipLaunchKernelGGL((lin_ring<TY, AKM, BKM, SPLIT>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((lin_ring<TY, AKM, BKM>), grid, dim3(256), 0, s, a);
       break;
     case kTile128:
-      hipLaunchKernelGGL((lin_staged<TY, 128, 128, 64, 2, RD, 2, 2, AKM, BKM, SPLIT>), grid,
-                         dim3(256), 0, s, a);
+      hipLaunchKernelGGL((lin_staged<TY, 128, 128, 64, 2, RD, 2, 2, AKM, BKM>), grid, dim3(256), 0,
+                         s, a);
       break;
     default:
-      hipLaunchKernelGGL((lin_staged<TY, 64, 64, 64, 4, RD, 2, 2, AKM, BKM, SPLIT>), grid,
-                         dim3(256), 0, s, a);
+      hipLaunchKernelGGL((lin_staged<TY, 64, 64, 64, 4, RD, 2, 2, AKM, BKM>), grid, dim3(256), 0, s,
+                         a);
   }
 }
 
-template <int TY, bool AKM, bool BKM>
-void launch_layout(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
-  if (g.splits > 1)
-    launch_tile<TY, AKM, BKM, true>(g, a, grid, s);
-  else
-    launch_tile<TY, AKM, BKM, false>(g, a, grid, s);
+template <int TY, int BM, int BN>
+void launch_reduce(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
+  constexpr int PER = (BM * BN / 8 + 255) / 256;
+  hipLaunchKernelGGL((lin_reduce<TY, BM, BN>), dim3((uint32_t)((g.programs - g.whole) * PER)),
+                     dim3(256), 0, s, a);
 }
 
 template <int TY>
 hipError_t launch_type(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)(g.programs * g.splits));
+  const dim3 grid((uint32_t)g.grid());
   if (g.path == kPathSkinnyK) {
-    hipLaunchKernelGGL((lin_skinny_k<TY, 8>), grid, dim3(512), 0, s, a);
+    if (g.cols == 16)
+      hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8>), grid, dim3(512), 0, s, a);
+    else if (g.cols == 32)
+      hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8>), grid, dim3(512), 0, s, a);
+    else
+      hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8>), grid, dim3(512), 0, s, a);
   } else if (g.path == kPathSkinnyN) {
     if constexpr (TY != kE4M3) {
-      if (g.cols == 128)
-        hipLaunchKernelGGL((lin_skinny_n<TY, 8, 8>), grid, dim3(512), 0, s, a);
-      else
-        hipLaunchKernelGGL((lin_skinny_n<TY, 4, 8>), grid, dim3(512), 0, s, a);
+      hipLaunchKernelGGL((lin_skinny_n<TY, 4, 8>), grid, dim3(512), 0, s, a);
     }
   } else if constexpr (TY == kE4M3) {
-    launch_layout<TY, true, true>(g, a, grid, s);
+    launch_tile<TY, true, true>(g, a, grid, s);
   } else if (g.akm) {
     if (g.bkm)
-      launch_layout<TY, true, true>(g, a, grid, s);
+      launch_tile<TY, true, true>(g, a, grid, s);
     else
-      launch_layout<TY, true, false>(g, a, grid, s);
+      launch_tile<TY, true, false>(g, a, grid, s);
   } else {
     if (g.bkm)
-      launch_layout<TY, false, true>(g, a, grid, s);
+      launch_tile<TY, false, true>(g, a, grid, s);
     else
-      launch_layout<TY, false, false>(g, a, grid, s);
+      launch_tile<TY, false, false>(g, a, grid, s);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.splits == 1) return e;
-  const int64_t threads = (int64_t)a.M * (a.ldw / 8);
-  hipLaunchKernelGGL((lin_reduce<TY>), dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0, s, a);
+  if (g.path != kPathTiles)
+    g.cols == 16   ? launch_reduce<TY, 16, 16>(g, a, s)
+    : g.cols == 32 ? launch_reduce<TY, 16, 32>(g, a, s)
+                   : launch_reduce<TY, 16, 64>(g, a, s);
+  else if (g.tile == kTile256)
+    launch_reduce<TY, 256, 256>(g, a, s);
+  else if (g.tile == kTile128)
+    launch_reduce<TY, 128, 128>(g, a, s);
+  else
+    launch_reduce<TY, 64, 64>(g, a, s);
   return hipGetLastError();
 }
 

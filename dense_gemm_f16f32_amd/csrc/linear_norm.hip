@@ -95,12 +95,35 @@ Region operand_region(const Operand& o, int64_t X, int64_t K, int64_t type) {
 }
 
 // ---- matrix products -------------------------------------------------------------------------
-// Slices of k so that about all CUs have a workgroup: at most 16, each of at least `least`
-// panels.
-int slices(int64_t programs, int64_t panels, int64_t least) {
-  int s = 1;
-  while (s < 16 && programs * s * 2 <= kCUs && panels / (s * 2) >= least) s *= 2;
-  return s;
+// Sets a plan's split: the tiles from `whole` on in `splits` slices of `depth` panels or units.
+void set_split(GemmPlan* g, int64_t whole, int64_t depth, int64_t splits, int64_t block) {
+  g->whole = g->programs;
+  g->splits = 1;
+  g->per_split = (int)depth;
+  if (splits < 2 || depth < 2) return;
+  const int64_t per = cdiv(depth, splits);
+  splits = cdiv(depth, per);   // no slice is empty
+  if (splits < 2) return;
+  g->whole = whole;
+  g->splits = (int)splits;
+  g->per_split = (int)per;
+  g->w_bytes = (g->programs - whole) * splits * block * 4;
+}
+
+// Time of one round of a tile's workgroups in us, fixed + panels * panel, with at most one
+// workgroup a CU and with more.  Fitted to bf16 products over M in 32 .. 4096, N in 256 .. 8192
+// and K in 256 .. 8192 (an e4m3 panel holds twice the k and takes the same time).  Checked
+// against all tiles with 1 .. 16 slices on 81 shapes (bf16 with b in both orders, odd sizes,
+// e4m3): the plan chosen is within 5 % of the fastest at 76 and within 12 % at all.
+struct TileCost {
+  double panel1, fixed1, panel, fixed;
+  int per_cu;   // workgroups that a CU holds
+};
+constexpr TileCost kTileCosts[lk::kTiles] = {
+    {1.32, 12.0, 1.32, 12.0, 1}, {0.71, 4.5, 0.85, 8.0, 2}, {0.215, 3.7, 0.37, 4.8, 2}};
+double round_cost(const TileCost& c, int64_t workgroups, int64_t panels) {
+  if (workgroups <= 0) return 0.0;
+  return workgroups <= kCUs ? c.fixed1 + panels * c.panel1 : c.fixed + panels * c.panel;
 }
 
 // The path, tile and split of an M x N x K product (M, N > 0).
@@ -110,42 +133,58 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
   *g = {};
   g->akm = a.km;
   g->bkm = b.km;
-  g->ldw = round_up(N, 8);
   const int64_t panels = cdiv(K, lk::kTileDepth * E);
-  int64_t depth = panels, least = 8;
   if (M <= lk::kSkinnyRows && a.km) {
     g->path = b.km ? lk::kPathSkinnyK : lk::kPathSkinnyN;
-    g->cols = b.km ? 16 : (N >= 128 * kCUs ? 128 : 64);
+    // b k-contiguous: a is read once per workgroup, so with many rows the workgroups take more
+    // columns, as long as every CU has one (16 rows, N = 16384, K = 4096: 16 columns 39.8 us, 64
+    // 32.8; one row: 27.3 and 31.4).
+    g->cols = 64;
+    if (b.km)
+      while (g->cols > 16 && (M <= 8 || cdiv(N, g->cols) < kCUs)) g->cols /= 2;
     g->programs = cdiv(N, g->cols);
-    if (!b.km) depth = cdiv(K, 32);
-    least = b.km ? 32 : 64;
-    if (g->programs >= 64) least = depth + 1;
+    // Few columns leave CUs idle: slices of k, of 16 units at least, up to a workgroup a CU.
+    // Below 64 units the second launch costs more (512 columns, K = 8192: 7.0 against 12 us; 1024
+    // columns in e4m3, K = 4096: 6.5 against 5.5).
+    const int64_t depth = b.km ? panels : cdiv(K, 32);
+    int64_t z = 1;
+    while (depth >= 64 && z < 16 && g->programs * z * 2 <= kCUs && depth / (z * 2) >= 16) z *= 2;
+    set_split(g, 0, depth, z, 16 * g->cols);
   } else {
     g->path = lk::kPathTiles;
-    // the largest tile whose grid about covers the CUs; panels' 32-bit offsets hold
-    auto fits = [&](int t) {
+    double best = 0.0;
+    GemmPlan chosen = *g;
+    for (int t = 0; t < lk::kTiles; ++t) {
       const lk::TileShape& s = lk::kTileShapes[t];
+      const TileCost& c = kTileCosts[t];
+      // panels' 32-bit offsets
       const int64_t ra = a.km ? s.bm : lk::kTileDepth, rb = b.km ? s.bn : lk::kTileDepth;
-      return ra * (a.ld / E) < kMax && rb * (b.ld / E) < kMax;
-    };
-    auto tiles = [&](int t) {
-      return cdiv(M, lk::kTileShapes[t].bm) * cdiv(N, lk::kTileShapes[t].bn);
-    };
-    g->tile = lk::kTile64;
-    if (tiles(lk::kTile128) >= 200 && fits(lk::kTile128)) g->tile = lk::kTile128;
-    if (tiles(lk::kTile256) >= 200 && fits(lk::kTile256)) g->tile = lk::kTile256;
-    if (!fits(g->tile)) return GEMM_F16F32_ERR_TOO_LARGE;
-    g->programs = tiles(g->tile);
+      if (ra * (a.ld / E) >= kMax || rb * (b.ld / E) >= kMax) continue;
+      const int64_t P = cdiv(M, s.bm) * cdiv(N, s.bn), slots = (int64_t)kCUs * c.per_cu;
+      const int64_t rounds = P / slots, rest = P % slots;
+      auto consider = [&](int64_t whole, int64_t splits) {
+        // full rounds, then the rest in slices; the second launch and the sums' way through
+        // memory (mostly through the caches) for a split
+        const int64_t per = cdiv(panels, splits), tail = P - whole;
+        double cost = (double)(whole / slots) * round_cost(c, slots, panels);
+        cost += round_cost(c, tail * splits, per);
+        if (splits > 1) cost += 3.0 + (double)(tail * splits) * s.bm * s.bn * 8 / 8.0e6;
+        if (best == 0.0 || cost < best) {
+          best = cost;
+          chosen.tile = t;
+          chosen.programs = P;
+          chosen.w_bytes = 0;
+          set_split(&chosen, whole, panels, splits, (int64_t)s.bm * s.bn);
+        }
+      };
+      consider(rounds * slots, 1);
+      for (int64_t z = 2; z <= 16 && rest > 0 && rest * z <= slots && panels >= 4 * z; ++z)
+        consider(rounds * slots, z);
+    }
+    if (best == 0.0) return GEMM_F16F32_ERR_TOO_LARGE;
+    *g = chosen;
   }
-  g->splits = slices(g->programs, depth, least);
-  g->per_split = (int)cdiv(depth, g->splits);
-  if (g->splits > 1) g->splits = (int)cdiv(depth, g->per_split);
-  if (g->splits > 1) {
-    // the reduction's 32-bit thread index
-    if (M * (g->ldw / 8) >= kMax) return GEMM_F16F32_ERR_TOO_LARGE;
-    g->w_bytes = g->splits * M * g->ldw * 4;
-  }
-  if (g->programs * g->splits >= kMax) return GEMM_F16F32_ERR_TOO_LARGE;
+  if (g->grid() >= kMax) return GEMM_F16F32_ERR_TOO_LARGE;
   return GEMM_F16F32_OK;
 }
 
@@ -161,16 +200,18 @@ LinArgs product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a,
   p.M = (int32_t)M;
   p.N = (int32_t)N;
   p.K = (int32_t)K;
-  if (g.path == lk::kPathTiles) {
-    p.num_pid_m = (int32_t)cdiv(M, lk::kTileShapes[g.tile].bm);
-    p.num_pid_n = (int32_t)cdiv(N, lk::kTileShapes[g.tile].bn);
-    const int group = g.tile == lk::kTile256 ? 8 : 4;
-    p.group_m = p.num_pid_m < group ? p.num_pid_m : group;
-  }
+  const bool tiles = g.path == lk::kPathTiles;
+  p.num_pid_m = (int32_t)(tiles ? cdiv(M, lk::kTileShapes[g.tile].bm) : 1);
+  p.num_pid_n = (int32_t)(g.programs / p.num_pid_m);
+  const int group = tiles && g.tile == lk::kTile256 ? 8 : 4;
+  p.group_m = p.num_pid_m < group ? p.num_pid_m : group;
+  // Tiles that share operands go to one XCD's cache; with one row of tiles they share none of
+  // b, and neighbours on different XCDs read it faster (1 x 16384 x 4096: 26.3 against 31.9 us).
+  p.xcd_remap = p.num_pid_m > 1;
   p.num_programs = (int32_t)g.programs;
   p.out_type = (int32_t)type;
   p.W = (float*)ws;
-  p.ldw = g.ldw;
+  p.first_split = (int32_t)g.whole;
   p.splits = g.splits;
   p.per_split = g.per_split;
   return p;
@@ -189,6 +230,9 @@ int check_workspace(const void* ws, int64_t have, int64_t need) {
   return ws == nullptr || have < need || ((uintptr_t)ws & 15) ? GEMM_F16F32_ERR_WORKSPACE
                                                               : GEMM_F16F32_OK;
 }
+
+// Partial column sums of `groups` workgroups, in whole blocks of 32 columns.
+int64_t partial_bytes(int64_t groups, int64_t cols) { return groups * round_up(cols, 32) * 4; }
 
 bool bad_dim(int64_t d) { return d < 0 || d >= kMax; }
 
@@ -234,7 +278,7 @@ struct BackwardPlan {
   Operand b, a, dt;          // b as da's right operand; a and dpre as db's
   bool db_cols;              // db is column-major: the product is its transpose
   GemmPlan gda, gdb;
-  int64_t ldd, ldp;          // dpre's row stride, the partial column sums'
+  int64_t ldd;               // dpre's row stride
   int row_blocks, rows_per_block;
   int64_t dpre_bytes, part_bytes, w_bytes;
 };
@@ -295,8 +339,7 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     f->rows_per_block = (int)round_up(cdiv(x.m, blocks), 4);
     f->row_blocks = x.m > 0 ? (int)cdiv(x.m, f->rows_per_block) : 0;
     if (x.dbias) {
-      f->ldp = round_up(x.n, 8);
-      f->part_bytes = round_up(f->row_blocks * f->ldp * 4, 256);
+      f->part_bytes = round_up(partial_bytes(f->row_blocks, x.n), 256);
     }
   }
   const int64_t ldd = act ? f->ldd : (x.dc_row > 0 ? x.dc_row : 1);
@@ -347,8 +390,12 @@ void norm_forward(const nk::NormArgs& p, hipStream_t s) {
 template <int TY>
 void norm_backward(const nk::NormBwdArgs& p, int grid, hipStream_t s) {
   with_row_shape(p.dim, [&](auto nw, auto c) {
-    hipLaunchKernelGGL((nk::rms_norm_bwd<TY, nw.value, c.value>), dim3((uint32_t)grid),
-                       dim3(64 * nw.value), 0, s, p);
+    if constexpr (c.value > 0)
+      hipLaunchKernelGGL((nk::rms_norm_bwd<TY, nw.value, c.value>), dim3((uint32_t)grid),
+                         dim3(64 * nw.value), 0, s, p);
+    else
+      hipLaunchKernelGGL((nk::rms_norm_bwd_long<TY, nw.value>), dim3((uint32_t)grid),
+                         dim3(64 * nw.value), 0, s, p);
   });
 }
 
@@ -356,13 +403,13 @@ void norm_backward(const nk::NormBwdArgs& p, int grid, hipStream_t s) {
 int backward_groups(int64_t rows) { return (int)(rows < 2 * kCUs ? rows : 2 * kCUs); }
 
 int64_t norm_backward_bytes(const rms_norm_backward_args& x) {
-  return x.dweight ? backward_groups(x.rows) * round_up(x.dim, 8) * 4 : 0;
+  return x.dweight ? partial_bytes(backward_groups(x.rows), x.dim) : 0;
 }
 
 template <int TY>
-void launch_sum(const float* part, int64_t ldp, int n, int64_t cols, void* out, hipStream_t s) {
-  hipLaunchKernelGGL((nk::sum_partials<TY>), dim3((uint32_t)cdiv(cols, 16)), dim3(256), 0, s, part,
-                     ldp, n, (int)cols, (uint16_t*)out);
+void launch_sum(const float* part, int n, int64_t cols, void* out, hipStream_t s) {
+  hipLaunchKernelGGL((nk::sum_partials<TY>), dim3((uint32_t)cdiv(cols, 32)), dim3(256), 0, s, part, n,
+                     (int)cols, (uint16_t*)out);
 }
 
 }  // namespace
@@ -454,7 +501,6 @@ int linear_backward(const linear_backward_args* args) {
         dpre = ws;
       }
       d.part = part;
-      d.ldp = f.ldp;
       d.m = (int32_t)x.m;
       d.n = (int32_t)x.n;
       d.act = (int32_t)x.activation;
@@ -468,9 +514,9 @@ int linear_backward(const linear_backward_args* args) {
     }
     if (x.dbias) {
       if (bf)
-        launch_sum<lk::kBF16>(part, f.ldp, f.row_blocks, x.n, x.dbias, s);
+        launch_sum<lk::kBF16>(part, f.row_blocks, x.n, x.dbias, s);
       else
-        launch_sum<lk::kF16>(part, f.ldp, f.row_blocks, x.n, x.dbias, s);
+        launch_sum<lk::kF16>(part, f.row_blocks, x.n, x.dbias, s);
     }
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
@@ -586,7 +632,6 @@ int rms_norm_backward(const rms_norm_backward_args* args) {
   const hipStream_t s = (hipStream_t)x.stream;
   const bool bf = x.type == LINEAR_NORM_BF16;
   const int groups = backward_groups(x.rows);
-  const int64_t ldp = round_up(x.dim, 8);
   if (groups > 0) {
     nk::NormBwdArgs p = {};
     p.dy = (const uint16_t*)x.dy;
@@ -600,16 +645,15 @@ int rms_norm_backward(const rms_norm_backward_args* args) {
     p.dx = (uint16_t*)x.dx;
     p.dx_row = x.dx_row;
     p.part = x.dweight ? (float*)x.workspace : nullptr;
-    p.ldp = ldp;
-    p.rows = (int32_t)x.rows;
+      p.rows = (int32_t)x.rows;
     p.dim = (int32_t)x.dim;
     p.inv_dim = (float)(1.0 / (double)x.dim);
     bf ? norm_backward<lk::kBF16>(p, groups, s) : norm_backward<lk::kF16>(p, groups, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   if (x.dweight) {
-    bf ? launch_sum<lk::kBF16>((const float*)x.workspace, ldp, groups, x.dim, x.dweight, s)
-       : launch_sum<lk::kF16>((const float*)x.workspace, ldp, groups, x.dim, x.dweight, s);
+    bf ? launch_sum<lk::kBF16>((const float*)x.workspace, groups, x.dim, x.dweight, s)
+       : launch_sum<lk::kF16>((const float*)x.workspace, groups, x.dim, x.dweight, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   return GEMM_F16F32_OK;

@@ -195,132 +195,180 @@ struct NormBwdArgs {
   const uint16_t* dh;
   uint16_t* dx;
   uint16_t* dweight;
-  float* part;   // one row of partial dweight sums a workgroup, ldp floats apart
-  int64_t dy_row, h_row, dh_row, dx_row, ldp;
+  float* part;   // partial dweight sums of every workgroup, or null
+  int64_t dy_row, h_row, dh_row, dx_row;
   int32_t rows, dim;
   float inv_dim;
 };
 
-// Workgroup b takes rows b, b + grid, ...; each thread keeps its columns' dweight sums in
-// registers and writes them once.  C == 0: long rows, the sums kept in the workgroup's own row
-// of the workspace instead.
+// Partial column sums: `groups` workgroups each leave one float a column, stored as blocks of 32
+// columns by `groups` rows, so that the workgroup that adds a block's rows reads one contiguous
+// piece.
+__device__ __forceinline__ float* partial(float* part, int groups, int group, int col) {
+  return part + ((int64_t)(col >> 5) * groups + group) * 32 + (col & 31);
+}
+__device__ __forceinline__ void store_partial8(float* part, int groups, int group, int col,
+                                               const float (&v)[8]) {   // col: a multiple of 8
+  float* const o = partial(part, groups, group, col);
+  *(float4v*)o = float4v{v[0], v[1], v[2], v[3]};
+  *(float4v*)(o + 4) = float4v{v[4], v[5], v[6], v[7]};
+}
+
+// 8 16-bit values at p, of which the first n exist (the others 0), unconverted.
+__device__ __forceinline__ u32x4 raw8(const uint16_t* p, int n) {
+  if (n >= 8) return *(const u32x4_any*)p;
+  u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+  return v;
+}
+
+// Workgroup b takes rows b, b + grid, ... of at most 512 NW C columns; the next row's values are
+// loaded before the current row is worked on.  Each thread keeps its columns' dweight sums in
+// registers and writes them once.
 template <int TY, int NW, int C>
 __global__ void __launch_bounds__(64 * NW) rms_norm_bwd(NormBwdArgs p) {
   __shared__ float ssum[2][NW];
-  constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
+  constexpr int STEP = 512 * NW;
   const int c0 = threadIdx.x * 8;
-  const int steps = C > 0 ? C : (p.dim + STEP - 1) / STEP;
-  float wv[CR][8], dw[CR][8];
-  float* const part = p.part ? p.part + blockIdx.x * p.ldp : nullptr;
-  if constexpr (C > 0) {
+  float wv[C][8], dw[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+  }
+  struct Row {
+    u32x4 d[C], h[C], r[C];   // dy, h, dh
+    float4v s;                // rstd first; a lone float's padding would be copied through memory
+  };
+  auto load = [&](Row& q, int64_t row) __attribute__((always_inline)) {
+    q.s[0] = p.rstd[row];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+      const int col = c0 + i * STEP, n = p.dim - col;
+      q.d[i] = raw8(p.dy + row * p.dy_row + col, n);
+      q.h[i] = raw8(p.h + row * p.h_row + col, n);
+      q.r[i] = p.dh ? raw8(p.dh + row * p.dh_row + col, n) : u32x4{0u, 0u, 0u, 0u};
     }
-  }
+  };
+  // 16 waves have 128 registers a lane, too few for two rows
+  constexpr bool kAhead = NW < 16;
+  Row cur, nxt;
+  if (kAhead) load(cur, blockIdx.x);   // the grid is at most the rows
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    const float rstd = p.rstd[row];
-    const uint16_t* const dy = p.dy + row * p.dy_row;
-    const uint16_t* const h = p.h + row * p.h_row;
-    const uint16_t* const dh = p.dh ? p.dh + row * p.dh_row : nullptr;
-    uint16_t* const dx = p.dx + row * p.dx_row;
-    float gv[CR][8], xv[CR][8], dv[CR][8];
+    if (!kAhead) load(cur, row);
+    nxt = cur;
+    if (kAhead && row + gridDim.x < p.rows) load(nxt, row + gridDim.x);
+    const float rstd = cur.s[0];
     float sum = 0.f;
-    // g and xh of step i, and dy
-    auto load = [&](int i, float (&g)[8], float (&x)[8], float (&d)[8])
-                    __attribute__((always_inline)) {
-      const int col = c0 + i * STEP, n = p.dim - col;
-      load8(d, dy + col, n, TY);
-      load8(x, h + col, n, TY);
-      float w[8];
-      if constexpr (C == 0) load8(w, p.weight + col, n, TY);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float d[8], x[8];
+      unpack8(d, cur.d[i], TY);
+      unpack8(x, cur.h[i], TY);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] *= rstd;
-        g[e] = d[e] * (C > 0 ? wv[C > 0 ? i : 0][e] : w[e]);
-      }
-    };
-    float dhv[CR][8];
-    if constexpr (C > 0) {
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        load(i, gv[i], xv[i], dv[i]);
-        if (dh) load8(dhv[i], dh + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
-      }
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sum += gv[i][e] * xv[i][e];
-          dw[i][e] += dv[i][e] * xv[i][e];
-        }
-    } else {
-      for (int i = 0; i < steps; ++i) {
-        load(i, gv[0], xv[0], dv[0]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += gv[0][e] * xv[0][e];
+        dw[i][e] += d[e] * x[e];
+        sum += d[e] * wv[i][e] * x[e];
       }
     }
     // two sets of sums in turn, so that one barrier a row is enough
     const float mean = group_sum<NW>(sum, ssum[turn]) * p.inv_dim;
-#pragma unroll CR
-    for (int i = 0; i < steps; ++i) {
-      const int col = c0 + i * STEP, n = p.dim - col;
-      if (n <= 0) break;
-      constexpr bool R = C > 0;
-      const int j = R ? i : 0;
-      if constexpr (!R) {
-        load(i, gv[0], xv[0], dv[0]);
-        if (dh) load8(dhv[0], dh + col, n, TY);
-        if (part) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            part[col + e] = (row == blockIdx.x ? 0.f : part[col + e]) + dv[0][e] * xv[0][e];
-        }
-      }
-      float v[8];
+    for (int i = 0; i < C; ++i) {
+      const int col = c0 + i * STEP;
+      float d[8], x[8], r[8];
+      unpack8(d, cur.d[i], TY);
+      unpack8(x, cur.h[i], TY);
+      unpack8(r, cur.r[i], TY);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        r[e] += rstd * (d[e] * wv[i][e] - x[e] * rstd * mean);
+      if (col < p.dim) store8(p.dx + row * p.dx_row + col, r, p.dim - col, TY);
+    }
+    cur = nxt;
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int col = c0 + i * STEP;
+    if (col < p.dim) store_partial8(p.part, gridDim.x, blockIdx.x, col, dw[i]);
+  }
+}
+
+// Rows too long for registers: read twice, the dweight sums kept in the workgroup's
+// part of the workspace.
+template <int TY, int NW>
+__global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
+  __shared__ float ssum[2][NW];
+  constexpr int STEP = 512 * NW;
+  const int c0 = threadIdx.x * 8;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const float rstd = p.rstd[row];
+    auto load = [&](int col, float (&g)[8], float (&x)[8], float (&d)[8])
+                    __attribute__((always_inline)) {
+      const int n = p.dim - col;
+      float w[8];
+      load8(d, p.dy + row * p.dy_row + col, n, TY);
+      load8(x, p.h + row * p.h_row + col, n, TY);
+      load8(w, p.weight + col, n, TY);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = rstd * (gv[j][e] - xv[j][e] * mean);
-        if (dh) v[e] += dhv[j][e];
+        x[e] *= rstd;
+        g[e] = d[e] * w[e];
       }
-      store8(dx + col, v, n, TY);
-    }
-  }
-  if constexpr (C > 0) {
-    if (part) {
+    };
+    float g[8], x[8], d[8], sum = 0.f;
+    for (int col = c0; col < p.dim; col += STEP) {
+      load(col, g, x, d);
 #pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int col = c0 + i * STEP;
-        if (col < p.dim) {   // ldp is a multiple of 8: whole groups
-          *(float4v*)(part + col) = float4v{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
-          *(float4v*)(part + col + 4) = float4v{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
-        }
+      for (int e = 0; e < 8; ++e) sum += g[e] * x[e];
+    }
+    const float mean = group_sum<NW>(sum, ssum[turn]) * p.inv_dim;
+    for (int col = c0; col < p.dim; col += STEP) {
+      float v[8];
+      load(col, g, x, d);
+      if (p.dh)
+        load8(v, p.dh + row * p.dh_row + col, p.dim - col, TY);
+      else
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += rstd * (g[e] - x[e] * mean);
+      if (p.part) {
+        float* const o = partial(p.part, gridDim.x, blockIdx.x, col);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = (row == blockIdx.x ? 0.f : o[e]) + d[e] * x[e];
       }
+      store8(p.dx + row * p.dx_row + col, v, p.dim - col, TY);
     }
   }
 }
 
-// out[j] = the sum of n partial rows, in order within a thread and then over the 16 threads of a
-// column: 16 columns a workgroup of 256.
+// out[j] = the sum of n partial sums, in order within a thread and then over the 32 threads of a
+// column: one block of 32 columns a workgroup, 4 a thread.
 template <int TY>
-__global__ void __launch_bounds__(256) sum_partials(const float* part, int64_t ldp, int n,
-                                                    int cols, uint16_t* out) {
-  __shared__ float s[16][17];
-  const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int col = blockIdx.x * 16 + c;
-  float v = 0.f;
-  if (col < cols)
-    for (int i = r; i < n; i += 16) v += part[(int64_t)i * ldp + col];
+__global__ void __launch_bounds__(256) sum_partials(const float* part, int n, int cols,
+                                                    uint16_t* out) {
+  __shared__ float4v s[32][9];
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+  const float* const q = part + (int64_t)blockIdx.x * n * 32 + c * 4;
+  float4v v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = r; i < n; i += 32) v += *(const float4v*)(q + i * 32);
   s[r][c] = v;
   __syncthreads();
-  if (r == 0 && col < cols) {
+  const int t = threadIdx.x;
+  if (t < 32 && blockIdx.x * 32 + t < cols) {
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) v += s[i][c];
-    out[col] = to_16(v, TY);
+    for (int i = 0; i < 32; ++i) sum += s[i][t / 4][t % 4];
+    out[blockIdx.x * 32 + t] = to_16(sum, TY);
   }
 }
 
@@ -328,8 +376,8 @@ struct DactArgs {
   const uint16_t* dc;
   const uint16_t* pre;   // null: dpre is dc
   uint16_t* dpre;
-  float* part;           // one row of column sums a row block, or null
-  int64_t dc_row, pre_row, dpre_row, ldp;
+  float* part;           // partial column sums of every row block, or null
+  int64_t dc_row, pre_row, dpre_row;
   int32_t m, n, act;
   int32_t row_blocks, rows_per_block;
 };
@@ -372,9 +420,7 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
     for (int i = 0; i < 3; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += s[i][t * 8 + e];
-    float* const o = p.part + rb * p.ldp + col;   // ldp is a multiple of 8
-    *(float4v*)o = float4v{sum[0], sum[1], sum[2], sum[3]};
-    *(float4v*)(o + 4) = float4v{sum[4], sum[5], sum[6], sum[7]};
+    store_partial8(p.part, p.row_blocks, rb, col, sum);
   }
 }
 

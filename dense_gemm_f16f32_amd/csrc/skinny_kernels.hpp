@@ -42,7 +42,7 @@ __device__ __forceinline__ int4v load16_tail(const uint16_t* row, int k, int K) 
 // col_of(c, l % 16), added in wave order, then the epilogue (or the split's partial sums).
 template <int TY, int NW, int NC, int NB, class ColOf>
 __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc)[NB],
-                                           float GK_LDS* s, int n0, int z, ColOf col_of) {
+                                           float GK_LDS* s, int n0, float* W, ColOf col_of) {
   constexpr int LDC = NC + 4;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
 #pragma unroll
@@ -62,8 +62,8 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
     for (int u = 0; u < NW; ++u)
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] += s[(u * 16 + row) * LDC + cc + e];
-    if (p.splits > 1) {
-      float* const o = p.W + ((int64_t)z * p.M + row) * p.ldw + col;
+    if (W != nullptr) {
+      float* const o = W + row * NC + cc;
       *(float4v*)o = float4v{f[0], f[1], f[2], f[3]};
       *(float4v*)(o + 4) = float4v{f[4], f[5], f[6], f[7]};
     } else {
@@ -72,62 +72,76 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
   }
 }
 
-// b stored k-contiguous (column-major): 16 columns a workgroup.  One unit is 128 bytes of every
-// row: lane l takes the 16-byte chunks l / 16 and 4 + l / 16 of row l % 16, of a and of b
-// alike, so the order of k inside the unit is the same for both.
-template <int TY, int NW>
+// b stored k-contiguous (column-major): 16 NB columns a workgroup.  One unit is 128 bytes of
+// every row: lane l takes the 16-byte chunks l / 16 and 4 + l / 16 of row l % 16, of a and of b
+// alike, so the order of k inside the unit is the same for both.  The loads of U units are in
+// flight at once.
+template <int TY, int NB, int NW>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   constexpr int UE = TY == kE4M3 ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk
-  __shared__ float s[NW * 16 * 20];
+  constexpr int NC = 16 * NB, U = NB == 1 ? 4 : 2;
+  __shared__ float s[NW * 16 * (NC + 4)];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nb = (p.N + 15) / 16;
-  const int z = blockIdx.x / nb, n0 = (blockIdx.x - z * nb) * 16;
+  const Work wk = work_of<16, NC>(p, blockIdx.x);
+  int m0, n0;
+  corner_of<16, NC>(p, wk.tile, m0, n0);
   const int x = lane & 15, g = lane >> 4;
   // rows and columns that do not exist repeat the last one; their sums are not stored
   const uint16_t* const pa = p.A + (int64_t)(x < p.M ? x : p.M - 1) * p.lda;
-  const uint16_t* const pb = p.B + (int64_t)(n0 + x < p.N ? n0 + x : p.N - 1) * p.ldb;
-  float4v acc[1] = {float4v{0.f, 0.f, 0.f, 0.f}};
-  auto mul = [&](const int4v (&a)[2], const int4v (&b)[2]) __attribute__((always_inline)) {
+  const uint16_t* pb[NB];
+  float4v acc[NB];
+#pragma unroll
+  for (int c = 0; c < NB; ++c) {
+    const int col = n0 + 16 * c + x;
+    pb[c] = p.B + (int64_t)(col < p.N ? col : p.N - 1) * p.ldb;
+    acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
+  }
+  auto mul = [&](int c, const int4v (&a)[2], const int4v (&b)[2]) __attribute__((always_inline)) {
     if constexpr (TY == kE4M3) {
-      acc[0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+      acc[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
           __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7),
-          __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7), acc[0], 0, 0, 0, 0, 0, 0);
+          __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7), acc[c], 0, 0, 0, 0, 0, 0);
     } else {
-      mma16x16<TY>(acc[0], a[0], b[0]);
-      mma16x16<TY>(acc[0], a[1], b[1]);
+      mma16x16<TY>(acc[c], a[0], b[0]);
+      mma16x16<TY>(acc[c], a[1], b[1]);
     }
   };
   const int units = (p.K + UE - 1) / UE, whole = p.K / UE;
-  const int u0 = p.splits > 1 ? z * p.per_split : 0;
-  const int u1 = p.splits > 1 && u0 + p.per_split < units ? u0 + p.per_split : units;
+  const int u0 = wk.z < 0 ? 0 : wk.z * p.per_split;
+  const int u1 = wk.z >= 0 && u0 + p.per_split < units ? u0 + p.per_split : units;
   const int uw = u1 < whole ? u1 : whole;
-  constexpr int U = 4;
   int u = u0 + w;
   for (; u + (U - 1) * NW < uw; u += U * NW) {
-    int4v a[U][2], b[U][2];
+    int4v a[U][2], b[U][NB][2];
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int64_t k = (int64_t)(u + i * NW) * 64 + (h * 4 + g) * 8;   // in 16-bit slots
-        b[i][h] = load16(pb + k);
+#pragma unroll
+        for (int c = 0; c < NB; ++c) b[i][c][h] = load16(pb[c] + k);
         a[i][h] = load16(pa + k);
       }
 #pragma unroll
-    for (int i = 0; i < U; ++i) mul(a[i], b[i]);
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int c = 0; c < NB; ++c) mul(c, a[i], b[i][c]);
   }
   for (; u < u1; u += NW) {
-    int4v a[2], b[2];
+    int4v a[2], b[NB][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = u * UE + (h * 4 + g) * CE;
-      b[h] = load16_tail<TY>(pb, k, p.K);
+#pragma unroll
+      for (int c = 0; c < NB; ++c) b[c][h] = load16_tail<TY>(pb[c], k, p.K);
       a[h] = load16_tail<TY>(pa, k, p.K);
     }
-    mul(a, b);
+#pragma unroll
+    for (int c = 0; c < NB; ++c) mul(c, a, b[c]);
   }
-  join_waves<TY, NW, 16>(p, acc, (float GK_LDS*)s, n0, z, [](int, int i) { return i; });
+  join_waves<TY, NW, NC>(p, acc, (float GK_LDS*)s, n0, wk.w,
+                         [](int c, int i) { return c * 16 + i; });
 }
 
 // b stored n-contiguous (row-major): 16 CP columns a workgroup.  Lane l takes CP consecutive
@@ -141,8 +155,9 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
   __shared__ float s[NW * 16 * (NC + 4)];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nb = (p.N + NC - 1) / NC;
-  const int z = blockIdx.x / nb, n0 = (blockIdx.x - z * nb) * NC;
+  const Work wk = work_of<16, NC>(p, blockIdx.x);
+  int m0, n0;
+  corner_of<16, NC>(p, wk.tile, m0, n0);
   const int x = lane & 15, g = lane >> 4;
   const uint16_t* const pa = p.A + (int64_t)(x < p.M ? x : p.M - 1) * p.lda + 8 * g;
   const int col = n0 + x * CP;
@@ -174,8 +189,8 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
     }
   };
   const int units = (p.K + 31) / 32, whole = p.K / 32;
-  const int u0 = p.splits > 1 ? z * p.per_split : 0;
-  const int u1 = p.splits > 1 && u0 + p.per_split < units ? u0 + p.per_split : units;
+  const int u0 = wk.z < 0 ? 0 : wk.z * p.per_split;
+  const int u1 = wk.z >= 0 && u0 + p.per_split < units ? u0 + p.per_split : units;
   const int uw = u1 < whole ? u1 : whole;
   constexpr int U = 2;
   int u = u0 + w;
@@ -200,7 +215,7 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
       b[r] = k + 8 * g + r < p.K ? row(pb + ((int64_t)k + r) * p.ldb) : vec(0u);
     mul(load16_tail<TY>(pa - 8 * g, k + 8 * g, p.K), b);
   }
-  join_waves<TY, NW, NC>(p, acc, (float GK_LDS*)s, n0, z,
+  join_waves<TY, NW, NC>(p, acc, (float GK_LDS*)s, n0, wk.w,
                          [](int c, int i) { return i * CP + c; });
 }
 
