@@ -100,22 +100,56 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8], int type) {
   }
   return v;
 }
-// 8 values at p, of which the first n exist (n >= 8: all); the others read as 0.
-__device__ __forceinline__ void load8(float (&f)[8], const uint16_t* p, int n, int type) {
-  if (n >= 8) {
-    unpack8(f, *(const u32x4_any*)p, type);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = e < n ? to_f32(p[e], type) : 0.f;
+// 8 16-bit values at p, of which the first n exist (n >= 8: all, n <= 0: none); the others are 0
+// and not read.  p is n values before its row's end.  `back`: the row has 8 values at least;
+// then a lane at its end reads the row's last 8 and shifts, one load like every other lane's
+// (value by value, the lanes at a row's end cost a norm of 4092 columns half as much again).
+__device__ __forceinline__ u32x4 raw8(const uint16_t* p, int n, bool back) {
+  if (back) {
+    const int s = n >= 8 ? 0 : 8 - n;
+    u32x4 v = *(const u32x4_any*)(p - s);
+    if (s > 0) {
+      const uint64_t lo = (uint64_t)v[0] | ((uint64_t)v[1] << 32);
+      const uint64_t hi = (uint64_t)v[2] | ((uint64_t)v[3] << 32);
+      const uint64_t l = s >= 8 ? 0 : s >= 4 ? hi >> (16 * (s - 4)) : (lo >> (16 * s)) | (hi << (64 - 16 * s));
+      const uint64_t h = s >= 4 ? 0 : hi >> (16 * s);
+      v = u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+    }
+    return v;
   }
-}
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8], int n, int type) {
-  if (n >= 8) {
-    *(u32x4_any*)p = pack8(f, type);
-  } else {
+  u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) p[e] = to_16(f[e], type);
+  for (int e = 0; e < 8; ++e)
+    if (e < n) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+  return v;
+}
+__device__ __forceinline__ void load8(float (&f)[8], const uint16_t* p, int n, int type,
+                                      bool back) {
+  unpack8(f, raw8(p, n, back), type);
+}
+struct __attribute__((packed, aligned(2))) Half4 {
+  uint32_t x, y;
+};
+struct __attribute__((packed, aligned(2))) Half2 {
+  uint32_t x;
+};
+__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8], int n, int type) {
+  u32x4 v = pack8(f, type);
+  if (n >= 8) {
+    *(u32x4_any*)p = v;
+  } else {   // in pieces of 4, 2 and 1
+    if (n & 4) {
+      *(Half4*)p = Half4{v[0], v[1]};
+      p += 4;
+      v[0] = v[2];
+      v[1] = v[3];
+    }
+    if (n & 2) {
+      *(Half2*)p = Half2{v[0]};
+      p += 2;
+      v[0] = v[1];
+    }
+    if (n & 1) *p = (uint16_t)v[0];
   }
 }
 
@@ -227,7 +261,7 @@ __device__ __forceinline__ Columns load_columns(const LinArgs& p, int col) {
     c.sb[e] = 1.f;
   }
   if (c.n > 0) {
-    if (p.bias) load8(c.bias, p.bias + col, c.n, ot);
+    if (p.bias) load8(c.bias, p.bias + col, c.n, ot, p.N >= 8);
     if (TY == kE4M3 && p.scale_b) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -252,7 +286,7 @@ __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, floa
   act_n(v, p.act);
   if (p.res) {
     float r[8];
-    load8(r, p.res + (int64_t)row * p.ldr + col, c.n, ot);
+    load8(r, p.res + (int64_t)row * p.ldr + col, c.n, ot, p.N >= 8);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += r[e];
   }

@@ -93,6 +93,7 @@ __device__ __forceinline__ void store_e4m3x8(uint8_t* p, const float (&v)[8], fl
 // residual) for each step that needs them.
 template <int TY, bool Q8, int NW, int C>
 __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
+  const bool back = p.dim >= 8;
   __shared__ float ssum[NW];
   __shared__ uint32_t smax[NW];
   constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
@@ -104,10 +105,10 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
   const int steps = C > 0 ? C : (p.dim + STEP - 1) / STEP;
   float hv[CR][8], wv[CR][8];
   auto load_h = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
-    load8(v, x + col, p.dim - col, TY);
+    load8(v, x + col, p.dim - col, TY, back);
     if (res) {
       float r[8];
-      load8(r, res + col, p.dim - col, TY);
+      load8(r, res + col, p.dim - col, TY, back);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += r[e];
     }
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
 #pragma unroll
     for (int i = 0; i < C; ++i) load_h(c0 + i * STEP, hv[i]);
 #pragma unroll
-    for (int i = 0; i < C; ++i) load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
+    for (int i = 0; i < C; ++i) load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY, back);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = c0 + i * STEP;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
     float w[8];
     if constexpr (C == 0) {
       load_h(col, v);
-      load8(w, p.weight + col, p.dim - col, TY);
+      load8(w, p.weight + col, p.dim - col, TY, back);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -214,28 +215,22 @@ __device__ __forceinline__ void store_partial8(float* part, int groups, int grou
   *(float4v*)(o + 4) = float4v{v[4], v[5], v[6], v[7]};
 }
 
-// 8 16-bit values at p, of which the first n exist (the others 0), unconverted.
-__device__ __forceinline__ u32x4 raw8(const uint16_t* p, int n) {
-  if (n >= 8) return *(const u32x4_any*)p;
-  u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < n) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
-  return v;
-}
-
-// Workgroup b takes rows b, b + grid, ... of at most 512 NW C columns; the next row's values are
-// loaded before the current row is worked on.  Each thread keeps its columns' dweight sums in
-// registers and writes them once.
-template <int TY, int NW, int C>
-__global__ void __launch_bounds__(64 * NW) rms_norm_bwd(NormBwdArgs p) {
+// RW rows of at most 512 NW C columns at a time, NW waves each: workgroup b takes rows b RW ..,
+// (b + grid) RW .., ...; where registers allow, the next row's values are loaded before the
+// current row is worked on.  Each thread keeps its columns' dweight sums in registers; the
+// workgroup adds and writes them once.  Short rows (one wave each) go four to a workgroup.
+template <int TY, int NW, int C, int RW>
+__global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
+  static_assert(NW == 1 || RW == 1, "rows of several waves share the workgroup's barrier");
+  const bool back = p.dim >= 8;
   __shared__ float ssum[2][NW];
   constexpr int STEP = 512 * NW;
-  const int c0 = threadIdx.x * 8;
+  const int c0 = (RW > 1 ? threadIdx.x & 63 : threadIdx.x) * 8;
+  const int rw = RW > 1 ? threadIdx.x >> 6 : 0;
   float wv[C][8], dw[C][8];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY);
+    load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY, back);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
   }
@@ -248,20 +243,20 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd(NormBwdArgs p) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = c0 + i * STEP, n = p.dim - col;
-      q.d[i] = raw8(p.dy + row * p.dy_row + col, n);
-      q.h[i] = raw8(p.h + row * p.h_row + col, n);
-      q.r[i] = p.dh ? raw8(p.dh + row * p.dh_row + col, n) : u32x4{0u, 0u, 0u, 0u};
+      q.d[i] = raw8(p.dy + row * p.dy_row + col, n, back);
+      q.h[i] = raw8(p.h + row * p.h_row + col, n, back);
+      q.r[i] = p.dh ? raw8(p.dh + row * p.dh_row + col, n, back) : u32x4{0u, 0u, 0u, 0u};
     }
   };
-  // 16 waves have 128 registers a lane, too few for two rows
-  constexpr bool kAhead = NW < 16;
+  constexpr bool kAhead = C <= 2;
+  const int64_t first = (int64_t)blockIdx.x * RW + rw, step = (int64_t)gridDim.x * RW;
   Row cur, nxt;
-  if (kAhead) load(cur, blockIdx.x);   // the grid is at most the rows
+  if (kAhead && first < p.rows) load(cur, first);
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
     if (!kAhead) load(cur, row);
     nxt = cur;
-    if (kAhead && row + gridDim.x < p.rows) load(nxt, row + gridDim.x);
+    if (kAhead && row + step < p.rows) load(nxt, row + step);
     const float rstd = cur.s[0];
     float sum = 0.f;
 #pragma unroll
@@ -293,6 +288,23 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd(NormBwdArgs p) {
     cur = nxt;
   }
   if (p.part == nullptr) return;
+  if constexpr (RW > 1) {   // the other rows' sums, in their order
+    __shared__ float sdw[RW - 1][C * 512];
+    if (rw > 0) {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sdw[rw - 1][(i * 8 + e) * 64 + (threadIdx.x & 63)] = dw[i][e];
+    }
+    __syncthreads();
+    if (rw > 0) return;
+#pragma unroll
+    for (int r = 0; r < RW - 1; ++r)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] += sdw[r][(i * 8 + e) * 64 + threadIdx.x];
+  }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int col = c0 + i * STEP;
@@ -304,6 +316,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd(NormBwdArgs p) {
 // part of the workspace.
 template <int TY, int NW>
 __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
+  const bool back = p.dim >= 8;
   __shared__ float ssum[2][NW];
   constexpr int STEP = 512 * NW;
   const int c0 = threadIdx.x * 8;
@@ -314,9 +327,9 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
                     __attribute__((always_inline)) {
       const int n = p.dim - col;
       float w[8];
-      load8(d, p.dy + row * p.dy_row + col, n, TY);
-      load8(x, p.h + row * p.h_row + col, n, TY);
-      load8(w, p.weight + col, n, TY);
+      load8(d, p.dy + row * p.dy_row + col, n, TY, back);
+      load8(x, p.h + row * p.h_row + col, n, TY, back);
+      load8(w, p.weight + col, n, TY, back);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] *= rstd;
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
       float v[8];
       load(col, g, x, d);
       if (p.dh)
-        load8(v, p.dh + row * p.dh_row + col, p.dim - col, TY);
+        load8(v, p.dh + row * p.dh_row + col, p.dim - col, TY, back);
       else
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
@@ -398,10 +411,10 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
 #pragma unroll 4
     for (int row = rb * p.rows_per_block + g; row < r1; row += 4) {
       float v[8];
-      load8(v, p.dc + row * p.dc_row + col, n, TY);
+      load8(v, p.dc + row * p.dc_row + col, n, TY, p.n >= 8);
       if (p.pre) {
         float u[8];
-        load8(u, p.pre + row * p.pre_row + col, n, TY);
+        load8(u, p.pre + row * p.pre_row + col, n, TY, p.n >= 8);
         slope8(v, u, p.act);
         store8(p.dpre + row * p.dpre_row + col, v, n, TY);
       }
