@@ -691,25 +691,79 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, co
   epilogue<T>(p, acc, m0, n0, wm, wn, lane, slab, k.w);
 }
 
+// The NS LDS stages of a staged tile as separate objects (a refill of one is then seen not to
+// touch another), their addresses assigned one by one (a list of them would become a table).
+#define LK_DECLARE_STAGES(NS, BYTES)                                             \
+  __shared__ __attribute__((aligned(16))) char stage0[BYTES];                    \
+  __shared__ __attribute__((aligned(16))) char stage1[BYTES];                    \
+  __shared__ __attribute__((aligned(16))) char stage2[(NS) > 2 ? (BYTES) : 16];  \
+  __shared__ __attribute__((aligned(16))) char stage3[(NS) > 3 ? (BYTES) : 16];  \
+  static_assert(NS == 2 || NS == 4, "stages");                                   \
+  char GK_LDS* S[NS];                                                            \
+  S[0] = (char GK_LDS*)stage0;                                                   \
+  S[1] = (char GK_LDS*)stage1;                                                   \
+  if constexpr ((NS) > 2) {                                                      \
+    S[2] = (char GK_LDS*)stage2;                                                 \
+    S[3] = (char GK_LDS*)stage3;                                                 \
+  }
+
 template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM>
 __global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
   using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32>;
-  // stages as separate LDS objects (a refill of one is then seen not to touch another), their
-  // addresses assigned one by one (a list of them would become a table)
-  __shared__ __attribute__((aligned(16))) char stage0[T::STAGE];
-  __shared__ __attribute__((aligned(16))) char stage1[T::STAGE];
-  __shared__ __attribute__((aligned(16))) char stage2[NS > 2 ? T::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) char stage3[NS > 3 ? T::STAGE : 16];
-  static_assert(NS >= 2 && NS <= 4, "stages");
-  char GK_LDS* S[NS];
-  S[0] = (char GK_LDS*)stage0;
-  S[1] = (char GK_LDS*)stage1;
-  if constexpr (NS > 2) S[2] = (char GK_LDS*)stage2;
-  if constexpr (NS > 3) S[3] = (char GK_LDS*)stage3;
+  LK_DECLARE_STAGES(NS, T::STAGE)
   int m0, n0;
   const Work k = work_of<BM, BN>(p, blockIdx.x);
   corner_of<BM, BN>(p, k.tile, m0, n0);
   staged_tile<T, NS, RD, AKM, BKM>(p, m0, n0, k, S);
+}
+
+// Sum over n partial rows of one block of 32 columns (see store_partial8), in order within a
+// thread and then over the 32 threads of a column, 4 columns a thread of 256.
+template <int TY>
+__device__ __forceinline__ void sum_block(const float* part, int n, int block, int cols,
+                                          uint16_t* out) {
+  __shared__ float4v s[32][9];
+  const int t = threadIdx.x, c = t & 7, r = t >> 3;
+  const float* const q = part + (int64_t)block * n * 32 + c * 4;
+  float4v v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int i = r; i < n; i += 32) v += *(const float4v*)(q + i * 32);
+  s[r][c] = v;
+  __syncthreads();
+  if (t < 32 && block * 32 + t < cols) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += s[i][t / 4][t % 4];
+    out[block * 32 + t] = to_16(sum, TY);
+  }
+}
+
+// Both products of a small backward pass and the last step of its bias gradient in one launch:
+// workgroups of da's 64 x 64 tiles, then db's, then blocks of 32 columns of dbias.
+struct PairArgs {
+  LinArgs da, db;
+  const float* part;
+  uint16_t* dbias;
+  int32_t groups, cols;   // of the partial sums
+};
+template <int TY, bool BKM>
+__global__ void __launch_bounds__(256) lin_pair(PairArgs p) {
+  using TA = Tile<TY, 64, 64, 64, true, BKM, 2, 2, 32>;
+  using TB = Tile<TY, 64, 64, 64, false, false, 2, 2, 32>;
+  LK_DECLARE_STAGES(4, TA::STAGE)
+  int h = blockIdx.x, m0, n0;
+  if (h < p.da.num_programs) {
+    corner_of<64, 64>(p.da, h, m0, n0);
+    staged_tile<TA, 4, 3, true, BKM>(p.da, m0, n0, Work{h, -1, nullptr}, S);
+    return;
+  }
+  h -= p.da.num_programs;
+  if (h < p.db.num_programs) {
+    corner_of<64, 64>(p.db, h, m0, n0);
+    staged_tile<TB, 4, 3, false, false>(p.db, m0, n0, Work{h, -1, nullptr}, S);
+    return;
+  }
+  sum_block<TY>(p.part, p.groups, h - p.db.num_programs, p.cols, p.dbias);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -26,6 +26,7 @@ struct GemmPlan {
   int64_t programs, whole;
   int splits, per_split;
   int64_t w_bytes;
+  double cost;            // estimated time in us
   int64_t grid() const { return whole + (programs - whole) * splits; }
 };
 
@@ -93,6 +94,17 @@ hipError_t launch_type(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
     launch_reduce<TY, 128, 128>(g, a, s);
   else
     launch_reduce<TY, 64, 64>(g, a, s);
+  return hipGetLastError();
+}
+
+template <int TY>
+hipError_t launch_pair(const PairArgs& p, bool bkm, hipStream_t s) {
+  const dim3 grid((uint32_t)(p.da.num_programs + p.db.num_programs +
+                             (p.dbias ? (p.cols + 31) / 32 : 0)));
+  if (bkm)
+    hipLaunchKernelGGL((lin_pair<TY, true>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((lin_pair<TY, false>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

@@ -150,6 +150,7 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     int64_t z = 1;
     while (depth >= 64 && z < 16 && g->programs * z * 2 <= kCUs && depth / (z * 2) >= 16) z *= 2;
     set_split(g, 0, depth, z, 16 * g->cols);
+    g->cost = 4.0 + (double)(N * K * 2 / E) / 4.5e6 + (g->splits > 1 ? 3.0 : 0.0);
   } else {
     g->path = lk::kPathTiles;
     double best = 0.0;
@@ -183,6 +184,7 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     }
     if (best == 0.0) return GEMM_F16F32_ERR_TOO_LARGE;
     *g = chosen;
+    g->cost = best;
   }
   if (g->grid() >= kMax) return GEMM_F16F32_ERR_TOO_LARGE;
   return GEMM_F16F32_OK;
@@ -274,7 +276,8 @@ int plan_forward(linear_forward_args& x, ForwardPlan* f) {
 
 // ---- linear_backward ----------------------------------------------------------------------------
 struct BackwardPlan {
-  bool empty, dact;          // nothing at all to do; the element-wise pass runs
+  bool dact;                 // the element-wise pass runs
+  bool pair;                 // the products and dbias's last step go in one launch
   Operand b, a, dt;          // b as da's right operand; a and dpre as db's
   bool db_cols;              // db is column-major: the product is its transpose
   GemmPlan gda, gdb;
@@ -284,13 +287,11 @@ struct BackwardPlan {
 };
 int plan_backward(linear_backward_args& x, BackwardPlan* f) {
   *f = {};
-  f->empty = true;
   if (bad_dim(x.m) || bad_dim(x.n) || bad_dim(x.k)) return GEMM_F16F32_ERR_DIM;
   if (!is16(x.type)) return GEMM_F16F32_ERR_OPTS;
   if (x.activation < LINEAR_ACT_NONE || x.activation > LINEAR_ACT_SILU)
     return GEMM_F16F32_ERR_OPTS;
   const bool act = x.activation != LINEAR_ACT_NONE;
-  f->empty = false;
   int rc = check_rows(x.dc, x.m, x.n, &x.dc_row, 2, true);
   if (rc == 0 && act) rc = check_rows(x.pre, x.m, x.n, &x.pre_row, 2, true);
   if (rc == 0) rc = check_rows(x.da, x.m, x.k, &x.da_row, 2, false);
@@ -338,7 +339,7 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     if (blocks < 1) blocks = 1;
     f->rows_per_block = (int)round_up(cdiv(x.m, blocks), 4);
     f->row_blocks = x.m > 0 ? (int)cdiv(x.m, f->rows_per_block) : 0;
-    if (x.dbias) {
+    if (x.dbias && f->row_blocks != 1) {
       f->part_bytes = round_up(partial_bytes(f->row_blocks, x.n), 256);
     }
   }
@@ -355,6 +356,30 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
                     : plan_gemm(x.type, x.k, x.n, x.m, f->a, f->dt, &f->gdb);
     if (rc != 0) return rc;
     if (f->gdb.w_bytes > f->w_bytes) f->w_bytes = f->gdb.w_bytes;
+  }
+  // One launch for both products, unsplit, where its estimated time is below theirs and that of
+  // the launches saved (about 2 us each).
+  if (f->gda.programs > 0 && f->gdb.programs > 0 && !f->a.km) {
+    const int64_t pa = cdiv(x.m, 64) * cdiv(x.k, 64), pb = cdiv(x.n, 64) * cdiv(x.k, 64);
+    const int64_t deep = cdiv(x.m > x.n ? x.m : x.n, lk::kTileDepth);
+    const int64_t most = 64, lb = f->b.ld > ldd ? f->b.ld : ldd;
+    const bool fits = most * lb < kMax && most * f->a.ld < kMax;
+    const double two = f->gda.cost + f->gdb.cost + 2.0 + (f->part_bytes > 0 ? 2.0 : 0.0);
+    f->pair = fits && pa + pb <= 2 * kCUs && round_cost(kTileCosts[lk::kTile64], pa + pb, deep) < two;
+    if (f->pair) {
+      GemmPlan t = {};
+      t.path = lk::kPathTiles;
+      t.tile = lk::kTile64;
+      t.akm = true;
+      t.bkm = f->b.km;
+      t.programs = t.whole = pa;
+      t.splits = 1;
+      f->gda = t;
+      t.akm = t.bkm = false;
+      t.programs = t.whole = pb;
+      f->gdb = t;
+      f->w_bytes = 0;
+    }
   }
   return GEMM_F16F32_OK;
 }
@@ -498,57 +523,66 @@ int linear_backward(const linear_backward_args* args) {
   char* const ws = (char*)x.workspace;
   const bool act = x.activation != LINEAR_ACT_NONE;
   const void* dpre = x.dc;
-  if (f.dact) {
-    float* const part = x.dbias ? (float*)(ws + f.dpre_bytes) : nullptr;
-    if (f.row_blocks > 0) {
-      nk::DactArgs d = {};
-      d.dc = (const uint16_t*)x.dc;
-      d.dc_row = x.dc_row;
-      if (act) {
-        d.pre = (const uint16_t*)x.pre;
-        d.pre_row = x.pre_row;
-        d.dpre = (uint16_t*)ws;
-        d.dpre_row = f.ldd;
-        dpre = ws;
-      }
-      d.part = part;
-      d.m = (int32_t)x.m;
-      d.n = (int32_t)x.n;
-      d.act = (int32_t)x.activation;
-      d.row_blocks = f.row_blocks;
-      d.rows_per_block = f.rows_per_block;
-      const dim3 grid((uint32_t)(cdiv(x.n, 512) * f.row_blocks));
-      if (bf)
-        hipLaunchKernelGGL((nk::lin_dact<lk::kBF16>), grid, dim3(256), 0, s, d);
-      else
-        hipLaunchKernelGGL((nk::lin_dact<lk::kF16>), grid, dim3(256), 0, s, d);
+  const bool sums = x.dbias != nullptr && f.dact;
+  const bool last = sums && f.row_blocks != 1;   // dbias has a second step
+  float* const part = last ? (float*)(ws + f.dpre_bytes) : nullptr;
+  if (f.dact && f.row_blocks > 0) {
+    nk::DactArgs d = {};
+    d.dc = (const uint16_t*)x.dc;
+    d.dc_row = x.dc_row;
+    if (act) {
+      d.pre = (const uint16_t*)x.pre;
+      d.pre_row = x.pre_row;
+      d.dpre = (uint16_t*)ws;
+      d.dpre_row = f.ldd;
+      dpre = ws;
     }
-    if (x.dbias) {
-      if (bf)
-        launch_sum<lk::kBF16>(part, f.row_blocks, x.n, x.dbias, s);
-      else
-        launch_sum<lk::kF16>(part, f.row_blocks, x.n, x.dbias, s);
-    }
+    d.part = part;
+    d.sum = sums && !last ? (uint16_t*)x.dbias : nullptr;
+    d.m = (int32_t)x.m;
+    d.n = (int32_t)x.n;
+    d.act = (int32_t)x.activation;
+    d.row_blocks = f.row_blocks;
+    d.rows_per_block = f.rows_per_block;
+    const dim3 grid((uint32_t)(cdiv(x.n, 512) * f.row_blocks));
+    if (bf)
+      hipLaunchKernelGGL((nk::lin_dact<lk::kBF16>), grid, dim3(256), 0, s, d);
+    else
+      hipLaunchKernelGGL((nk::lin_dact<lk::kF16>), grid, dim3(256), 0, s, d);
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  if (last && !f.pair) {
+    if (bf)
+      launch_sum<lk::kBF16>(part, f.row_blocks, x.n, x.dbias, s);
+    else
+      launch_sum<lk::kF16>(part, f.row_blocks, x.n, x.dbias, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   void* const W = ws ? ws + f.dpre_bytes + f.part_bytes : nullptr;
+  LinArgs da = {}, db = {};
   if (f.gda.programs > 0) {
     const Operand d = {dpre, act ? f.ldd : x.dc_row, true};
-    LinArgs p = product(x.type, x.m, x.k, x.n, d, f.b, f.gda, W);
-    p.out = (uint16_t*)x.da;
-    p.ldo = x.da_row;
-    rc = launch(x.type, f.gda, p, x.stream);
-    if (rc != GEMM_F16F32_OK) return rc;
+    da = product(x.type, x.m, x.k, x.n, d, f.b, f.gda, W);
+    da.out = (uint16_t*)x.da;
+    da.ldo = x.da_row;
   }
   if (f.gdb.programs > 0) {
     Operand d = f.dt;
     d.p = dpre;
-    LinArgs p = f.db_cols ? product(x.type, x.n, x.k, x.m, d, f.a, f.gdb, W)
-                          : product(x.type, x.k, x.n, x.m, f.a, d, f.gdb, W);
-    p.out = (uint16_t*)x.db;
-    p.ldo = f.db_cols ? x.db_col : x.db_row;
-    rc = launch(x.type, f.gdb, p, x.stream);
+    db = f.db_cols ? product(x.type, x.n, x.k, x.m, d, f.a, f.gdb, W)
+                   : product(x.type, x.k, x.n, x.m, f.a, d, f.gdb, W);
+    db.out = (uint16_t*)x.db;
+    db.ldo = f.db_cols ? x.db_col : x.db_row;
   }
+  if (f.pair) {
+    const lk::PairArgs p = {da, db, part, last ? (uint16_t*)x.dbias : nullptr, f.row_blocks,
+                            (int32_t)x.n};
+    const hipError_t e = bf ? lk::launch_pair<lk::kBF16>(p, f.b.km, s)
+                            : lk::launch_pair<lk::kF16>(p, f.b.km, s);
+    return e == hipSuccess ? GEMM_F16F32_OK : GEMM_F16F32_ERR_HIP;
+  }
+  if (f.gda.programs > 0) rc = launch(x.type, f.gda, da, x.stream);
+  if (rc == GEMM_F16F32_OK && f.gdb.programs > 0) rc = launch(x.type, f.gdb, db, x.stream);
   return rc;
 }
 

@@ -363,26 +363,11 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
   }
 }
 
-// out[j] = the sum of n partial sums, in order within a thread and then over the 32 threads of a
-// column: one block of 32 columns a workgroup, 4 a thread.
+// out[j] = the sum of n partial sums; one block of 32 columns a workgroup.
 template <int TY>
 __global__ void __launch_bounds__(256) sum_partials(const float* part, int n, int cols,
                                                     uint16_t* out) {
-  __shared__ float4v s[32][9];
-  const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
-  const float* const q = part + (int64_t)blockIdx.x * n * 32 + c * 4;
-  float4v v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = r; i < n; i += 32) v += *(const float4v*)(q + i * 32);
-  s[r][c] = v;
-  __syncthreads();
-  const int t = threadIdx.x;
-  if (t < 32 && blockIdx.x * 32 + t < cols) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) sum += s[i][t / 4][t % 4];
-    out[blockIdx.x * 32 + t] = to_16(sum, TY);
-  }
+  sum_block<TY>(part, n, blockIdx.x, cols, out);
 }
 
 struct DactArgs {
@@ -390,6 +375,7 @@ struct DactArgs {
   const uint16_t* pre;   // null: dpre is dc
   uint16_t* dpre;
   float* part;           // partial column sums of every row block, or null
+  uint16_t* sum;         // the column sums themselves (one row block), or null
   int64_t dc_row, pre_row, dpre_row;
   int32_t m, n, act;
   int32_t row_blocks, rows_per_block;
@@ -422,7 +408,7 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
       for (int e = 0; e < 8; ++e) sum[e] += v[e];
     }
   }
-  if (p.part == nullptr) return;
+  if (p.part == nullptr && p.sum == nullptr) return;
   if (g > 0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[g - 1][t * 8 + e] = sum[e];
@@ -433,7 +419,10 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
     for (int i = 0; i < 3; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += s[i][t * 8 + e];
-    store_partial8(p.part, p.row_blocks, rb, col, sum);
+    if (p.sum != nullptr)
+      store8(p.sum + col, sum, n, TY);
+    else
+      store_partial8(p.part, p.row_blocks, rb, col, sum);
   }
 }
 
