@@ -136,17 +136,19 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
   const int64_t panels = cdiv(K, lk::kTileDepth * E);
   if (M <= lk::kSkinnyRows && a.km) {
     g->path = b.km ? lk::kPathSkinnyK : lk::kPathSkinnyN;
+    const int64_t depth = b.km ? panels : cdiv(K, 32);
     // b k-contiguous: a is read once per workgroup, so with many rows the workgroups take more
-    // columns, as long as every CU has one (16 rows, N = 16384, K = 4096: 16 columns 39.8 us, 64
-    // 32.8; one row: 27.3 and 31.4).
+    // columns, as long as the CUs have one each, if need be in two slices of k (e4m3, 16 x 16384
+    // x 4096: 16 columns 18.4 us, 64 columns 13.6; 16 x 8192 x 8192: 18.6, and 16.1 in two
+    // slices; one row, bf16, 16384 x 4096: 23.8 and 25.8).
+    const int64_t wide = cdiv(N, 64);
     g->cols = 64;
-    if (b.km)
-      while (g->cols > 16 && (M <= 8 || cdiv(N, g->cols) < kCUs)) g->cols /= 2;
+    if (b.km && (M <= 8 || (wide < kCUs && (2 * wide < kCUs || depth < 64))))
+      g->cols = M > 8 && 2 * wide >= kCUs ? 32 : 16;
     g->programs = cdiv(N, g->cols);
     // Few columns leave CUs idle: slices of k, of 16 units at least, up to a workgroup a CU.
     // Below 64 units the second launch costs more (512 columns, K = 8192: 7.0 against 12 us; 1024
     // columns in e4m3, K = 4096: 6.5 against 5.5).
-    const int64_t depth = b.km ? panels : cdiv(K, 32);
     int64_t z = 1;
     while (depth >= 64 && z < 16 && g->programs * z * 2 <= kCUs && depth / (z * 2) >= 16) z *= 2;
     set_split(g, 0, depth, z, 16 * g->cols);
@@ -190,20 +192,81 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
   return GEMM_F16F32_OK;
 }
 
+// A product in one piece, or cut at the last whole 256 x 256 tile of one axis or both, with the
+// slivers left of it as products of their own.
+struct Part {
+  GemmPlan g;
+  int64_t m0, n0, M, N;
+};
+constexpr int kParts = 3;
+struct Product {
+  Part part[kParts];
+  int parts;       // 0: nothing to compute
+  int64_t w_bytes; // workspace, shared by the parts
+  double cost;
+};
+int plan_product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a,
+                 const Operand& b, Product* p) {
+  p->part[0] = {{}, 0, 0, M, N};
+  p->parts = 1;
+  const int rc = plan_gemm(type, M, N, K, a, b, &p->part[0].g);
+  if (rc != GEMM_F16F32_OK) return rc;
+  p->cost = p->part[0].g.cost;
+  // In one piece a sliver costs a whole row of tiles, or a second round of workgroups; cut off, a
+  // launch (about 2.5 us) and what its shape takes (4095 x 4097 x 4093: 157 us in one piece, 134
+  // in two).
+  const int64_t rm = M > 256 ? M % 256 : 0, rn = N > 256 ? N % 256 : 0;
+  for (int cut = 1; cut < 4 && p->part[0].g.path == lk::kPathTiles; ++cut) {
+    const int64_t cm = cut & 1 ? rm : 0, cn = cut & 2 ? rn : 0;
+    if (((cut & 1) && cm == 0) || ((cut & 2) && cn == 0)) continue;
+    Product q = {};
+    q.part[q.parts++] = {{}, 0, 0, M - cm, N - cn};
+    if (cn > 0) q.part[q.parts++] = {{}, 0, N - cn, M, cn};
+    if (cm > 0) q.part[q.parts++] = {{}, M - cm, 0, cm, N - cn};
+    bool ok = true;
+    q.cost = 2.5 * (q.parts - 1);
+    for (int i = 0; ok && i < q.parts; ++i) {
+      Part& t = q.part[i];
+      ok = plan_gemm(type, t.M, t.N, K, a, b, &t.g) == GEMM_F16F32_OK;
+      q.cost += t.g.cost;
+    }
+    if (ok && q.cost < p->cost) *p = q;
+  }
+  p->w_bytes = 0;
+  for (int i = 0; i < p->parts; ++i)
+    if (p->part[i].g.w_bytes > p->w_bytes) p->w_bytes = p->part[i].g.w_bytes;
+  return GEMM_F16F32_OK;
+}
+
 // The kernel arguments of a product, epilogue left empty.
-LinArgs product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b,
-                const GemmPlan& g, void* ws) {
+LinArgs product(int64_t type, int64_t K, const Operand& a, const Operand& b) {
   const int64_t E = type == LINEAR_NORM_E4M3 ? 2 : 1;
   LinArgs p = {};
   p.A = (const uint16_t*)a.p;
   p.B = (const uint16_t*)b.p;
   p.lda = a.ld / E;
   p.ldb = b.ld / E;
-  p.M = (int32_t)M;
-  p.N = (int32_t)N;
   p.K = (int32_t)K;
+  p.out_type = (int32_t)type;
+  return p;
+}
+
+// ... those of one part of it.
+LinArgs part_args(const LinArgs& whole, const Part& t, void* ws) {
+  const GemmPlan& g = t.g;
+  LinArgs p = whole;
+  p.A += g.akm ? t.m0 * p.lda : t.m0;
+  p.B += g.bkm ? t.n0 * p.ldb : t.n0;
+  p.out += t.m0 * p.ldo + t.n0;
+  if (p.pre) p.pre += t.m0 * p.ldp + t.n0;
+  if (p.res) p.res += t.m0 * p.ldr + t.n0;
+  if (p.bias) p.bias += t.n0;
+  if (p.scale_a) p.scale_a += t.m0;
+  if (p.scale_b) p.scale_b += t.n0;
+  p.M = (int32_t)t.M;
+  p.N = (int32_t)t.N;
   const bool tiles = g.path == lk::kPathTiles;
-  p.num_pid_m = (int32_t)(tiles ? cdiv(M, lk::kTileShapes[g.tile].bm) : 1);
+  p.num_pid_m = (int32_t)(tiles ? cdiv(t.M, lk::kTileShapes[g.tile].bm) : 1);
   p.num_pid_n = (int32_t)(g.programs / p.num_pid_m);
   const int group = tiles && g.tile == lk::kTile256 ? 8 : 4;
   p.group_m = p.num_pid_m < group ? p.num_pid_m : group;
@@ -211,7 +274,6 @@ LinArgs product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a,
   // b, and neighbours on different XCDs read it faster (1 x 16384 x 4096: 26.3 against 31.9 us).
   p.xcd_remap = p.num_pid_m > 1;
   p.num_programs = (int32_t)g.programs;
-  p.out_type = (int32_t)type;
   p.W = (float*)ws;
   p.first_split = (int32_t)g.whole;
   p.splits = g.splits;
@@ -219,12 +281,17 @@ LinArgs product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a,
   return p;
 }
 
-int launch(int64_t type, const GemmPlan& g, const LinArgs& p, void* stream) {
+int launch(int64_t type, const Product& q, const LinArgs& whole, void* ws, void* stream) {
   const hipStream_t s = (hipStream_t)stream;
-  const hipError_t e = type == LINEAR_NORM_F16    ? lk::launch_type<lk::kF16>(g, p, s)
-                       : type == LINEAR_NORM_BF16 ? lk::launch_type<lk::kBF16>(g, p, s)
-                                                  : lk::launch_type<lk::kE4M3>(g, p, s);
-  return e == hipSuccess ? GEMM_F16F32_OK : GEMM_F16F32_ERR_HIP;
+  for (int i = 0; i < q.parts; ++i) {
+    const LinArgs p = part_args(whole, q.part[i], ws);
+    const GemmPlan& g = q.part[i].g;
+    const hipError_t e = type == LINEAR_NORM_F16    ? lk::launch_type<lk::kF16>(g, p, s)
+                         : type == LINEAR_NORM_BF16 ? lk::launch_type<lk::kBF16>(g, p, s)
+                                                    : lk::launch_type<lk::kE4M3>(g, p, s);
+    if (e != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  return GEMM_F16F32_OK;
 }
 
 int check_workspace(const void* ws, int64_t have, int64_t need) {
@@ -241,12 +308,10 @@ bool bad_dim(int64_t d) { return d < 0 || d >= kMax; }
 // ---- linear_forward ----------------------------------------------------------------------------
 struct ForwardPlan {
   Operand a, b;
-  GemmPlan g;
-  bool empty;
+  Product q;   // no parts: an empty result
 };
 int plan_forward(linear_forward_args& x, ForwardPlan* f) {
-  f->empty = true;
-  f->g = {};
+  *f = {};
   if (bad_dim(x.m) || bad_dim(x.n) || bad_dim(x.k)) return GEMM_F16F32_ERR_DIM;
   if (!is16(x.type) && x.type != LINEAR_NORM_E4M3) return GEMM_F16F32_ERR_OPTS;
   if (!is16(x.out_type) || (is16(x.type) && x.out_type != x.type)) return GEMM_F16F32_ERR_OPTS;
@@ -254,7 +319,6 @@ int plan_forward(linear_forward_args& x, ForwardPlan* f) {
     return GEMM_F16F32_ERR_OPTS;
   if (is16(x.type) && (x.scale_a || x.scale_b)) return GEMM_F16F32_ERR_OPTS;
   if (x.m == 0 || x.n == 0) return GEMM_F16F32_OK;
-  f->empty = false;
   int rc = operand(x.a, x.m, x.k, x.a_row, x.a_col, x.type, &f->a);
   if (rc == 0) rc = operand(x.b, x.n, x.k, x.b_col, x.b_row, x.type, &f->b);
   if (rc == 0) rc = check_rows(x.out, x.m, x.n, &x.out_row, 2, true);
@@ -271,7 +335,7 @@ int plan_forward(linear_forward_args& x, ForwardPlan* f) {
   const Region res = region(x.residual, x.m, x.n, x.residual_row, 2);
   const bool in_place = x.residual == x.out && x.residual_row == x.out_row;
   if (overlap(w[1], res) || (!in_place && overlap(w[0], res))) return GEMM_F16F32_ERR_OVERLAP;
-  return plan_gemm(x.type, x.m, x.n, x.k, f->a, f->b, &f->g);
+  return plan_product(x.type, x.m, x.n, x.k, f->a, f->b, &f->q);
 }
 
 // ---- linear_backward ----------------------------------------------------------------------------
@@ -280,7 +344,7 @@ struct BackwardPlan {
   bool pair;                 // the products and dbias's last step go in one launch
   Operand b, a, dt;          // b as da's right operand; a and dpre as db's
   bool db_cols;              // db is column-major: the product is its transpose
-  GemmPlan gda, gdb;
+  Product qa, qb;            // da's and db's products
   int64_t ldd;               // dpre's row stride
   int row_blocks, rows_per_block;
   int64_t dpre_bytes, part_bytes, w_bytes;
@@ -346,25 +410,25 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
   const int64_t ldd = act ? f->ldd : (x.dc_row > 0 ? x.dc_row : 1);
   if (x.da && x.m > 0 && x.k > 0) {
     const Operand d = {x.dc, ldd, true};
-    rc = plan_gemm(x.type, x.m, x.k, x.n, d, f->b, &f->gda);
+    rc = plan_product(x.type, x.m, x.k, x.n, d, f->b, &f->qa);
     if (rc != 0) return rc;
-    if (f->gda.w_bytes > f->w_bytes) f->w_bytes = f->gda.w_bytes;
+    if (f->qa.w_bytes > f->w_bytes) f->w_bytes = f->qa.w_bytes;
   }
   if (x.db && x.k > 0 && x.n > 0) {
     f->dt = {x.dc, ldd, false};
-    rc = f->db_cols ? plan_gemm(x.type, x.n, x.k, x.m, f->dt, f->a, &f->gdb)
-                    : plan_gemm(x.type, x.k, x.n, x.m, f->a, f->dt, &f->gdb);
+    rc = f->db_cols ? plan_product(x.type, x.n, x.k, x.m, f->dt, f->a, &f->qb)
+                    : plan_product(x.type, x.k, x.n, x.m, f->a, f->dt, &f->qb);
     if (rc != 0) return rc;
-    if (f->gdb.w_bytes > f->w_bytes) f->w_bytes = f->gdb.w_bytes;
+    if (f->qb.w_bytes > f->w_bytes) f->w_bytes = f->qb.w_bytes;
   }
   // One launch for both products, unsplit, where its estimated time is below theirs and that of
   // the launches saved (about 2 us each).
-  if (f->gda.programs > 0 && f->gdb.programs > 0 && !f->a.km) {
+  if (f->qa.parts > 0 && f->qb.parts > 0 && !f->a.km) {
     const int64_t pa = cdiv(x.m, 64) * cdiv(x.k, 64), pb = cdiv(x.n, 64) * cdiv(x.k, 64);
     const int64_t deep = cdiv(x.m > x.n ? x.m : x.n, lk::kTileDepth);
     const int64_t most = 64, lb = f->b.ld > ldd ? f->b.ld : ldd;
     const bool fits = most * lb < kMax && most * f->a.ld < kMax;
-    const double two = f->gda.cost + f->gdb.cost + 2.0 + (f->part_bytes > 0 ? 2.0 : 0.0);
+    const double two = f->qa.cost + f->qb.cost + 2.0 + (f->part_bytes > 0 ? 2.0 : 0.0);
     f->pair = fits && pa + pb <= 2 * kCUs && round_cost(kTileCosts[lk::kTile64], pa + pb, deep) < two;
     if (f->pair) {
       GemmPlan t = {};
@@ -374,10 +438,10 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
       t.bkm = f->b.km;
       t.programs = t.whole = pa;
       t.splits = 1;
-      f->gda = t;
+      f->qa.part[0] = {t, 0, 0, x.m, x.k};
       t.akm = t.bkm = false;
       t.programs = t.whole = pb;
-      f->gdb = t;
+      f->qb.part[0] = {t, 0, 0, f->db_cols ? x.n : x.k, f->db_cols ? x.k : x.n};
       f->w_bytes = 0;
     }
   }
@@ -457,7 +521,7 @@ int64_t linear_forward_workspace(const linear_forward_args* args) {
   linear_forward_args x = *args;
   ForwardPlan f;
   const int rc = plan_forward(x, &f);
-  return rc != GEMM_F16F32_OK ? rc : f.g.w_bytes;
+  return rc != GEMM_F16F32_OK ? rc : f.q.w_bytes;
 }
 
 int linear_forward(const linear_forward_args* args) {
@@ -465,11 +529,11 @@ int linear_forward(const linear_forward_args* args) {
   linear_forward_args x = *args;
   ForwardPlan f;
   int rc = plan_forward(x, &f);
-  if (rc != GEMM_F16F32_OK || f.empty) return rc;
-  rc = check_workspace(x.workspace, x.workspace_bytes, f.g.w_bytes);
+  if (rc != GEMM_F16F32_OK || f.q.parts == 0) return rc;
+  rc = check_workspace(x.workspace, x.workspace_bytes, f.q.w_bytes);
   if (rc != GEMM_F16F32_OK) return rc;
-  if (f.g.w_bytes > 0) {
-    const Region w = {x.workspace, (uint64_t)f.g.w_bytes};
+  if (f.q.w_bytes > 0) {
+    const Region w = {x.workspace, (uint64_t)f.q.w_bytes};
     const Region o[] = {region(x.out, x.m, x.n, x.out_row, 2), region(x.pre, x.m, x.n, x.pre_row, 2),
                         region(x.residual, x.m, x.n, x.residual_row, 2),
                         operand_region(f.a, x.m, x.k, x.type), operand_region(f.b, x.n, x.k, x.type),
@@ -477,7 +541,7 @@ int linear_forward(const linear_forward_args* args) {
                         region(x.scale_b, 1, x.n, x.n, 4)};
     if (conflict(&w, 1, o, 8)) return GEMM_F16F32_ERR_OVERLAP;
   }
-  LinArgs p = product(x.type, x.m, x.n, x.k, f.a, f.b, f.g, x.workspace);
+  LinArgs p = product(x.type, x.k, f.a, f.b);
   p.out = (uint16_t*)x.out;
   p.ldo = x.out_row;
   p.pre = (uint16_t*)x.pre;
@@ -489,7 +553,7 @@ int linear_forward(const linear_forward_args* args) {
   p.scale_b = x.scale_b;
   p.act = (int32_t)x.activation;
   p.out_type = (int32_t)x.out_type;
-  return launch(x.type, f.g, p, x.stream);
+  return launch(x.type, f.q, p, x.workspace, x.stream);
 }
 
 int64_t linear_backward_workspace(const linear_backward_args* args) {
@@ -560,29 +624,27 @@ int linear_backward(const linear_backward_args* args) {
   }
   void* const W = ws ? ws + f.dpre_bytes + f.part_bytes : nullptr;
   LinArgs da = {}, db = {};
-  if (f.gda.programs > 0) {
-    const Operand d = {dpre, act ? f.ldd : x.dc_row, true};
-    da = product(x.type, x.m, x.k, x.n, d, f.b, f.gda, W);
+  if (f.qa.parts > 0) {
+    da = product(x.type, x.n, {dpre, act ? f.ldd : x.dc_row, true}, f.b);
     da.out = (uint16_t*)x.da;
     da.ldo = x.da_row;
   }
-  if (f.gdb.programs > 0) {
+  if (f.qb.parts > 0) {
     Operand d = f.dt;
     d.p = dpre;
-    db = f.db_cols ? product(x.type, x.n, x.k, x.m, d, f.a, f.gdb, W)
-                   : product(x.type, x.k, x.n, x.m, f.a, d, f.gdb, W);
+    db = f.db_cols ? product(x.type, x.m, d, f.a) : product(x.type, x.m, f.a, d);
     db.out = (uint16_t*)x.db;
     db.ldo = f.db_cols ? x.db_col : x.db_row;
   }
   if (f.pair) {
-    const lk::PairArgs p = {da, db, part, last ? (uint16_t*)x.dbias : nullptr, f.row_blocks,
-                            (int32_t)x.n};
+    const lk::PairArgs p = {part_args(da, f.qa.part[0], W), part_args(db, f.qb.part[0], W), part,
+                            last ? (uint16_t*)x.dbias : nullptr, f.row_blocks, (int32_t)x.n};
     const hipError_t e = bf ? lk::launch_pair<lk::kBF16>(p, f.b.km, s)
                             : lk::launch_pair<lk::kF16>(p, f.b.km, s);
     return e == hipSuccess ? GEMM_F16F32_OK : GEMM_F16F32_ERR_HIP;
   }
-  if (f.gda.programs > 0) rc = launch(x.type, f.gda, da, x.stream);
-  if (rc == GEMM_F16F32_OK && f.gdb.programs > 0) rc = launch(x.type, f.gdb, db, x.stream);
+  if (f.qa.parts > 0) rc = launch(x.type, f.qa, da, W, x.stream);
+  if (rc == GEMM_F16F32_OK && f.qb.parts > 0) rc = launch(x.type, f.qb, db, W, x.stream);
   return rc;
 }
 

@@ -10,6 +10,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/hip/HIPContext.h>
 
 #include "linear_norm.h"
@@ -94,7 +95,7 @@ float* fptr(const Tensor& t) { return (float*)ptr(t); }
 int64_t row(const Tensor& t) { return t.defined() ? t.stride(0) : 0; }
 
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device& device) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+  return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
 // Raises GemmError(code, name).

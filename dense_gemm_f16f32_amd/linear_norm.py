@@ -63,16 +63,12 @@ def native():
     return _native
 
 
-def _call(stream, name, t, *args):
-    """The binding's function on torch's current stream, or on `stream`."""
-    f = getattr(_native or native(), name)
-    if stream is None:
-        return f(t, *args)
+def _on(stream, t):
+    """Context of a call on `stream` instead of torch's current one."""
     import torch
     if t.is_cuda and stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the operands on {t.device}")
-    with torch.cuda.stream(stream):
-        return f(t, *args)
+    return torch.cuda.stream(stream)
 
 
 class RMSNormResult(NamedTuple):
@@ -95,8 +91,11 @@ def linear(a, b, bias=None, residual=None, *, activation="none", scale_a=None, s
     (result, pre) with `with_pre`, where pre is the value before the activation, which
     linear_backward needs.  `out` may be the residual's own tensor.
     """
-    return _call(stream, "linear", a, b, bias, residual, activation, scale_a, scale_b, out_dtype,
-                 with_pre, out)
+    f = (_native or native()).linear
+    if stream is None:
+        return f(a, b, bias, residual, activation, scale_a, scale_b, out_dtype, with_pre, out)
+    with _on(stream, a):
+        return f(a, b, bias, residual, activation, scale_a, scale_b, out_dtype, with_pre, out)
 
 
 def linear_backward(dc, a, b, pre=None, *, activation="none", bias_grad=False, a_grad=True,
@@ -107,7 +106,11 @@ def linear_backward(dc, a, b, pre=None, *, activation="none", bias_grad=False, a
     is linear's value before the activation (not needed for "none").  All of one 16-bit type;
     dc and pre contiguous along n, a and b as in linear.  db has b's storage order.
     """
-    return _call(stream, "linear_backward", dc, a, b, pre, activation, bias_grad, a_grad, b_grad)
+    f = (_native or native()).linear_backward
+    if stream is None:
+        return f(dc, a, b, pre, activation, bias_grad, a_grad, b_grad)
+    with _on(stream, dc):
+        return f(dc, a, b, pre, activation, bias_grad, a_grad, b_grad)
 
 
 def rms_norm(x, weight, residual=None, *, eps=1e-5, out_dtype=None, with_rstd=False,
@@ -120,8 +123,11 @@ def rms_norm(x, weight, residual=None, *, eps=1e-5, out_dtype=None, with_rstd=Fa
     is taken of the unrounded sum.  `with_rstd` also returns 1 / sqrt(mean(h^2) + eps), which
     rms_norm_backward needs.
     """
-    return RMSNormResult._make(_call(stream, "rms_norm", x, weight, residual, eps, out_dtype,
-                                     with_rstd))
+    f = (_native or native()).rms_norm
+    if stream is None:
+        return RMSNormResult._make(f(x, weight, residual, eps, out_dtype, with_rstd))
+    with _on(stream, x):
+        return RMSNormResult._make(f(x, weight, residual, eps, out_dtype, with_rstd))
 
 
 def rms_norm_backward(dy, h, weight, rstd, *, dh=None, weight_grad=True, stream=None):
@@ -130,4 +136,8 @@ def rms_norm_backward(dy, h, weight, rstd, *, dh=None, weight_grad=True, stream=
     dy (rows, dim): gradient of y; h and rstd as rms_norm returned them; dh: the gradient that
     reaches h by another way (the residual stream), added to dx.
     """
-    return _call(stream, "rms_norm_backward", dy, h, weight, rstd, dh, weight_grad)
+    f = (_native or native()).rms_norm_backward
+    if stream is None:
+        return f(dy, h, weight, rstd, dh, weight_grad)
+    with _on(stream, dy):
+        return f(dy, h, weight, rstd, dh, weight_grad)
