@@ -104,24 +104,28 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8], int type) {
 // and not read.  p is n values before its row's end.  `back`: the row has 8 values at least;
 // then a lane at its end reads the row's last 8 and shifts, one load like every other lane's
 // (value by value, the lanes at a row's end cost a norm of 4092 columns half as much again).
-__device__ __forceinline__ u32x4 raw8(const uint16_t* p, int n, bool back) {
-  if (back) {
-    const int s = n >= 8 ? 0 : 8 - n;
-    u32x4 v = *(const u32x4_any*)(p - s);
-    if (s > 0) {
-      const uint64_t lo = (uint64_t)v[0] | ((uint64_t)v[1] << 32);
-      const uint64_t hi = (uint64_t)v[2] | ((uint64_t)v[3] << 32);
-      const uint64_t l = s >= 8 ? 0 : s >= 4 ? hi >> (16 * (s - 4)) : (lo >> (16 * s)) | (hi << (64 - 16 * s));
-      const uint64_t h = s >= 4 ? 0 : hi >> (16 * s);
-      v = u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
-    }
-    return v;
-  }
+// In two steps, so that a load can be in flight before its lane's shift has to wait for it.
+__device__ __forceinline__ u32x4 raw8_load(const uint16_t* p, int n, bool back) {
+  if (back) return *(const u32x4_any*)(p - (n >= 8 ? 0 : 8 - n));
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (e < n) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
   return v;
+}
+__device__ __forceinline__ u32x4 raw8_shift(u32x4 v, int n, bool back) {
+  if (n >= 8 || !back) return v;
+  const int s = 8 - n;
+  const uint64_t lo = (uint64_t)v[0] | ((uint64_t)v[1] << 32);
+  const uint64_t hi = (uint64_t)v[2] | ((uint64_t)v[3] << 32);
+  const uint64_t l = s >= 8   ? 0
+                     : s >= 4 ? hi >> (16 * (s - 4))
+                              : (lo >> (16 * s)) | (hi << (64 - 16 * s));
+  const uint64_t h = s >= 4 ? 0 : hi >> (16 * s);
+  return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+}
+__device__ __forceinline__ u32x4 raw8(const uint16_t* p, int n, bool back) {
+  return raw8_shift(raw8_load(p, n, back), n, back);
 }
 __device__ __forceinline__ void load8(float (&f)[8], const uint16_t* p, int n, int type,
                                       bool back) {
@@ -764,6 +768,163 @@ __global__ void __launch_bounds__(256) lin_pair(PairArgs p) {
     return;
   }
   sum_block<TY>(p.part, p.groups, h - p.db.num_programs, p.cols, p.dbias);
+}
+
+// ---------------------------------------------------------------------------------------
+// A small backward pass in one launch: both products on 64 x 64 tiles, with dpre = dc act'(pre)
+// made on the way into LDS by every workgroup that needs it (a few times over, which costs less
+// than a pass of its own and its launch), and its column sums by the workgroups of db's first
+// tiles along k.  Panels go through registers, three ahead, and two LDS stages.
+// ---------------------------------------------------------------------------------------
+struct SmallArgs {
+  LinArgs da, db;   // dc in the place of dpre
+  const uint16_t* pre;   // without an activation dc again (loaded, not used)
+  int64_t ldpre;
+  uint16_t* dbias;
+  int32_t act;
+};
+
+// One operand's panel on its way through registers.  Rows have at least 8 values (see
+// raw8_load), and the loads are free of branches: after one, the compiler waits for them.
+template <class O, bool DPRE>
+struct RegPanel {
+  u32x4 v[O::LD], u[DPRE ? O::LD : 1];
+  // Loads the panel from k0 on.  Rows past the matrix repeat its last one.
+  __device__ __forceinline__ void fetch(const uint16_t* p, int64_t ld, const uint16_t* pre,
+                                        int64_t ldpre, int x0, int k0, int X, int K, int t) {
+#pragma unroll
+    for (int i = 0; i < O::LD; ++i) {
+      const int q = i * O::NW * 64 + t, row = q / O::CH, c = (q % O::CH) * 8;
+      const int e = (O::KM ? k0 : x0) + c, n = (O::KM ? K : X) - e;
+      const int r = (O::KM ? x0 : k0) + row, R = O::KM ? X : K;
+      const int64_t at = r < R ? r : R - 1;
+      v[i] = raw8_load(p + at * ld + e, n, true);
+      if constexpr (DPRE) u[i] = raw8_load(pre + at * ldpre + e, n, true);
+    }
+  }
+  // What lies outside the matrix along k becomes 0 (along x it feeds only results that are not
+  // stored).
+  __device__ __forceinline__ void settle(int i, int x0, int k0, int X, int K, int t) {
+    const int q = i * O::NW * 64 + t, row = q / O::CH, c = (q % O::CH) * 8;
+    const int n = O::KM ? K - k0 - c : X - x0 - c;
+    v[i] = raw8_shift(v[i], n, true);
+    if constexpr (DPRE) u[i] = raw8_shift(u[i], n, true);
+    if (!O::KM && k0 + row >= K) v[i] = u32x4{0u, 0u, 0u, 0u};
+  }
+};
+
+template <class T, bool AKM, bool BKM, int DP, bool SUM>
+__device__ __forceinline__ void small_tile(const LinArgs& p, const SmallArgs& a, int tile,
+                                           char GK_LDS* smem) {
+  using OA = typename T::OA;
+  using OB = typename T::OB;
+  constexpr int TY = T::TY;
+  const int t = threadIdx.x, lane = t & 63;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = w / T::WN, wn = w % T::WN;
+  int m0, n0;
+  corner_of<64, 64>(p, tile, m0, n0);
+  const bool sums = SUM && a.dbias != nullptr && (DP == 1 ? n0 : m0) == 0;
+  const int np = (p.K + 63) / 64;
+  RegPanel<OA, DP == 1> ra[3];
+  RegPanel<OB, DP == 2> rb[3];
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  auto fetch = [&](int j, int s) __attribute__((always_inline)) {
+    const int k0 = (s < np ? s : np - 1) * 64;   // past the end: loaded again, not used
+    ra[j].fetch(p.A, p.lda, a.pre, a.ldpre, m0, k0, p.M, p.K, t);
+    rb[j].fetch(p.B, p.ldb, a.pre, a.ldpre, n0, k0, p.N, p.K, t);
+  };
+  auto put = [&](auto& r, auto is_dpre, int i, char GK_LDS* at) __attribute__((always_inline)) {
+    if constexpr (is_dpre.value) {
+      if (a.act != LINEAR_ACT_NONE || (SUM && sums)) {
+        float v[8], u[8];
+        unpack8(v, r.v[i], TY);
+        unpack8(u, r.u[i], TY);
+        slope8(v, u, a.act);
+        if (SUM && sums) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        }
+        r.v[i] = pack8(v, TY);
+      }
+    }
+    *(u32x4 GK_LDS*)at = r.v[i];
+  };
+  auto deposit = [&](int j, int s) __attribute__((always_inline)) {
+    if (s >= np) return;
+    char GK_LDS* const st = smem + (s & 1) * T::STAGE;
+#pragma unroll
+    for (int i = 0; i < OA::LD; ++i) {
+      const int q = i * 256 + t;
+      ra[j].settle(i, m0, s * 64, p.M, p.K, t);
+      put(ra[j], std::integral_constant<bool, DP == 1>{}, i,
+          st + gk::lds_chunk<OA>(q / OA::CH, q % OA::CH));
+    }
+#pragma unroll
+    for (int i = 0; i < OB::LD; ++i) {
+      const int q = i * 256 + t;
+      rb[j].settle(i, n0, s * 64, p.N, p.K, t);
+      put(rb[j], std::integral_constant<bool, DP == 2>{}, i,
+          st + T::A_BYTES + gk::lds_chunk<OB>(q / OB::CH, q % OB::CH));
+    }
+  };
+  int oa[OA::NOFF], ob[OB::NOFF];
+  gk::operand_offsets<OA>(oa, wm, lane, 0);
+  gk::operand_offsets<OB>(ob, wn, lane, T::A_BYTES);
+  typename T::Acc acc[1][1];
+  static_assert(T::TM == 1 && T::TN == 1, "one block a wave");
+  acc[0][0] = typename T::Acc{};
+#pragma unroll
+  for (int j = 0; j < 3; ++j) fetch(j, j);
+  deposit(0, 0);
+  for (int s = 0; s < np; s += 3) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      if (s + j < np) {
+        __syncthreads();           // panel s + j is in LDS, panel s + j - 1 has been read
+        fetch(j, s + j + 3);
+        const char GK_LDS* const st = smem + ((s + j) & 1) * T::STAGE;
+#pragma unroll
+        for (int kk = 0; kk < T::KS; ++kk)
+          mma<T>(acc[0][0], read_frag<T, OA>(st, oa, 0, kk), read_frag<T, OB>(st, ob, 0, kk));
+        deposit((j + 1) % 3, s + j + 1);
+      }
+    }
+  }
+  __syncthreads();
+  if (SUM && sums) {
+    // a thread's chunks all lie in the 8 columns from 8 (t % 8) on
+    float GK_LDS* const f = (float GK_LDS*)smem;
+    const int X = DP == 1 ? p.M : p.N, x0 = DP == 1 ? m0 : n0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[(t >> 3) * 68 + (t & 7) * 8 + e] = sum[e];
+    __syncthreads();
+    if (t < 64 && x0 + t < X) {
+      float v = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) v += f[i * 68 + t];
+      a.dbias[x0 + t] = to_16(v, TY);
+    }
+    __syncthreads();
+  }
+  epilogue<T>(p, acc, m0, n0, wm, wn, lane, smem + w * Slab<T>::BYTES, nullptr);
+}
+
+// BKM: b as da's operand is k-contiguous.  COLS: db is column-major (its transpose computed).
+template <int TY, bool BKM, bool COLS>
+__global__ void __launch_bounds__(256) lin_small_bwd(SmallArgs p) {
+  using TA = Tile<TY, 64, 64, 64, true, BKM, 2, 2, 32>;
+  using TB = Tile<TY, 64, 64, 64, false, false, 2, 2, 32>;
+  static_assert(4 * Slab<TA>::BYTES <= 2 * TA::STAGE && 32 * 68 * 4 <= 2 * TA::STAGE, "LDS");
+  __shared__ __attribute__((aligned(16))) char smem[2 * TA::STAGE];
+  const int h = blockIdx.x;
+  if (h < p.da.num_programs)
+    small_tile<TA, true, BKM, 1, false>(p.da, p, h, (char GK_LDS*)smem);
+  else
+    small_tile<TB, false, false, COLS ? 1 : 2, true>(p.db, p, h - p.da.num_programs,
+                                                     (char GK_LDS*)smem);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -108,4 +108,18 @@ hipError_t launch_pair(const PairArgs& p, bool bkm, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int TY>
+hipError_t launch_small(const SmallArgs& p, bool bkm, bool cols, hipStream_t s) {
+  const dim3 grid((uint32_t)(p.da.num_programs + p.db.num_programs));
+  if (bkm && cols)
+    hipLaunchKernelGGL((lin_small_bwd<TY, true, true>), grid, dim3(256), 0, s, p);
+  else if (bkm)
+    hipLaunchKernelGGL((lin_small_bwd<TY, true, false>), grid, dim3(256), 0, s, p);
+  else if (cols)
+    hipLaunchKernelGGL((lin_small_bwd<TY, false, true>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((lin_small_bwd<TY, false, false>), grid, dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
 }  // namespace lk

@@ -342,6 +342,7 @@ int plan_forward(linear_forward_args& x, ForwardPlan* f) {
 struct BackwardPlan {
   bool dact;                 // the element-wise pass runs
   bool pair;                 // the products and dbias's last step go in one launch
+  bool small;                // ... and the element-wise pass as well
   Operand b, a, dt;          // b as da's right operand; a and dpre as db's
   bool db_cols;              // db is column-major: the product is its transpose
   Product qa, qb;            // da's and db's products
@@ -430,6 +431,10 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     const bool fits = most * lb < kMax && most * f->a.ld < kMax;
     const double two = f->qa.cost + f->qb.cost + 2.0 + (f->part_bytes > 0 ? 2.0 : 0.0);
     f->pair = fits && pa + pb <= 2 * kCUs && round_cost(kTileCosts[lk::kTile64], pa + pb, deep) < two;
+    // The element-wise pass as well while a tile's panels are few: its loads go through
+    // registers, three panels ahead, and a panel costs 1.1 - 1.8 us instead of 0.3 (f16, silu: 64^3
+    // 4.8 against 13.7 us in two launches, 300^3 11.8 and 12.1, 512^3 13.0 and 10.8).
+    f->small = f->pair && deep <= 4 && x.n >= 8 && x.k >= 8;
     if (f->pair) {
       GemmPlan t = {};
       t.path = lk::kPathTiles;
@@ -443,6 +448,10 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
       t.programs = t.whole = pb;
       f->qb.part[0] = {t, 0, 0, f->db_cols ? x.n : x.k, f->db_cols ? x.k : x.n};
       f->w_bytes = 0;
+      if (f->small) {
+        f->dact = false;
+        f->dpre_bytes = f->part_bytes = 0;
+      }
     }
   }
   return GEMM_F16F32_OK;
@@ -624,17 +633,26 @@ int linear_backward(const linear_backward_args* args) {
   }
   void* const W = ws ? ws + f.dpre_bytes + f.part_bytes : nullptr;
   LinArgs da = {}, db = {};
+  const int64_t ldd = act && !f.small ? f.ldd : x.dc_row;
   if (f.qa.parts > 0) {
-    da = product(x.type, x.n, {dpre, act ? f.ldd : x.dc_row, true}, f.b);
+    da = product(x.type, x.n, {dpre, ldd, true}, f.b);
     da.out = (uint16_t*)x.da;
     da.ldo = x.da_row;
   }
   if (f.qb.parts > 0) {
-    Operand d = f.dt;
-    d.p = dpre;
+    const Operand d = {dpre, ldd, false};
     db = f.db_cols ? product(x.type, x.m, d, f.a) : product(x.type, x.m, f.a, d);
     db.out = (uint16_t*)x.db;
     db.ldo = f.db_cols ? x.db_col : x.db_row;
+  }
+  if (f.small) {
+    const lk::SmallArgs p = {part_args(da, f.qa.part[0], nullptr),
+                             part_args(db, f.qb.part[0], nullptr),
+                             (const uint16_t*)(act ? x.pre : x.dc), act ? x.pre_row : x.dc_row,
+                             (uint16_t*)x.dbias, (int32_t)x.activation};
+    const hipError_t e = bf ? lk::launch_small<lk::kBF16>(p, f.b.km, f.db_cols, s)
+                            : lk::launch_small<lk::kF16>(p, f.b.km, f.db_cols, s);
+    return e == hipSuccess ? GEMM_F16F32_OK : GEMM_F16F32_ERR_HIP;
   }
   if (f.pair) {
     const lk::PairArgs p = {part_args(da, f.qa.part[0], W), part_args(db, f.qb.part[0], W), part,

@@ -243,9 +243,9 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = c0 + i * STEP, n = p.dim - col;
-      q.d[i] = raw8(p.dy + row * p.dy_row + col, n, back);
-      q.h[i] = raw8(p.h + row * p.h_row + col, n, back);
-      q.r[i] = p.dh ? raw8(p.dh + row * p.dh_row + col, n, back) : u32x4{0u, 0u, 0u, 0u};
+      q.d[i] = raw8_load(p.dy + row * p.dy_row + col, n, back);
+      q.h[i] = raw8_load(p.h + row * p.h_row + col, n, back);
+      q.r[i] = p.dh ? raw8_load(p.dh + row * p.dh_row + col, n, back) : u32x4{0u, 0u, 0u, 0u};
     }
   };
   constexpr bool kAhead = C <= 2;
@@ -262,6 +262,10 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float d[8], x[8];
+      const int n = p.dim - c0 - i * STEP;
+      cur.d[i] = raw8_shift(cur.d[i], n, back);
+      cur.h[i] = raw8_shift(cur.h[i], n, back);
+      cur.r[i] = raw8_shift(cur.r[i], n, back);
       unpack8(d, cur.d[i], TY);
       unpack8(x, cur.h[i], TY);
 #pragma unroll

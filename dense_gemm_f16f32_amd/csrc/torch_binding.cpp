@@ -135,12 +135,17 @@ PyObject* wrap(const Tensor& t) {
   Py_RETURN_NONE;
 }
 template <class... T>
-PyObject* tuple(const T&... t) {
-  PyObject* r = PyTuple_New(sizeof...(T));
+PyObject* tuple_of(PyTypeObject* type, const T&... t) {   // a tuple type without other fields
+  PyObject* r = type->tp_alloc(type, sizeof...(T));
   if (r == nullptr) throw python_error();
   Py_ssize_t i = 0;
   (PyTuple_SET_ITEM(r, i++, wrap(t)), ...);
   return r;
+}
+
+template <class... T>
+PyObject* tuple(const T&... t) {
+  return tuple_of(&PyTuple_Type, t...);
 }
 
 bool arity(Py_ssize_t n, Py_ssize_t want) {
@@ -272,10 +277,10 @@ PyObject* linear_bwd(PyObject*, PyObject* const* v, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// rms_norm(x, weight, residual, eps, out_dtype, with_rstd)
+// rms_norm(x, weight, residual, eps, out_dtype, with_rstd, type of the result)
 PyObject* norm(PyObject*, PyObject* const* v, Py_ssize_t count) {
   HANDLE_TH_ERRORS
-  if (!arity(count, 6)) return nullptr;
+  if (!arity(count, 7)) return nullptr;
   const Args a{v};
   const Tensor x = a.needed(0, "x"), w = a.needed(1, "weight"), res = a.tensor(2, "residual");
   on_gpu(x, "x");
@@ -323,7 +328,9 @@ PyObject* norm(PyObject*, PyObject* const* v, Py_ssize_t count) {
   p.eps = eps;
   p.stream = current_stream(device);
   check(rms_norm_forward(&p), "rms_norm_forward");
-  return tuple(y, h.defined() ? h : x, rstd, scale);
+  TORCH_CHECK_TYPE(PyType_Check(v[6]) && PyType_IsSubtype((PyTypeObject*)v[6], &PyTuple_Type),
+                   "the result's type must be a tuple");
+  return tuple_of((PyTypeObject*)v[6], y, h.defined() ? h : x, rstd, scale);
   END_HANDLE_TH_ERRORS
 }
 

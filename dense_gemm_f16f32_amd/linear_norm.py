@@ -125,9 +125,9 @@ def rms_norm(x, weight, residual=None, *, eps=1e-5, out_dtype=None, with_rstd=Fa
     """
     f = (_native or native()).rms_norm
     if stream is None:
-        return RMSNormResult._make(f(x, weight, residual, eps, out_dtype, with_rstd))
+        return f(x, weight, residual, eps, out_dtype, with_rstd, RMSNormResult)
     with _on(stream, x):
-        return RMSNormResult._make(f(x, weight, residual, eps, out_dtype, with_rstd))
+        return f(x, weight, residual, eps, out_dtype, with_rstd, RMSNormResult)
 
 
 def rms_norm_backward(dy, h, weight, rstd, *, dh=None, weight_grad=True, stream=None):

@@ -319,3 +319,29 @@ def test_graph_replays():
         torch.cuda.synchronize()
         for x, y in zip(held, want):
             assert torch.equal(x, y), i
+
+
+@pytest.mark.parametrize("ty", DT)
+@pytest.mark.parametrize("bo", "rc")
+@pytest.mark.parametrize("m,n,k", [(1, 8, 8), (3, 9, 200), (64, 64, 64), (65, 127, 8), (200, 250, 70),
+                                   (256, 256, 300), (255, 249, 61), (7, 200, 1000)])
+def test_backward_in_one_launch(m, n, k, bo, ty):
+    """Passes small enough for the kernel that makes dpre on the way (few panels, n and k of at
+    least 8), every activation, with and without a bias gradient."""
+    for i, activation in enumerate(ACTS):
+        check_backward(m, n, k, ty, "r", bo, activation, bias=i % 3 != 1, pad=i % 3, seed=m + i)
+
+
+def test_backward_in_one_launch_keeps_nan_in_its_row_and_column():
+    """NaN in dc[i, j] reaches row i of da and column j of db and dbias, and nothing else."""
+    q = gen(31)
+    for bo in "rc":
+        a = normal(q, (90, 40), torch.bfloat16)
+        b = operand(q, 40, 70, torch.bfloat16, bo, 0, 0)
+        dc, pre = normal(q, (90, 70), torch.bfloat16), normal(q, (90, 70), torch.bfloat16)
+        dc[89, 3] = float("nan")
+        da, db, dbias = g.linear_backward(dc, a, b, pre, activation="silu", bias_grad=True)
+        rows, cols = da.isnan(), db.isnan()
+        assert bool(rows[89].all()) and int(rows.sum()) == 40
+        assert bool(cols[:, 3].all()) and int(cols.sum()) == 40
+        assert bool(dbias[3].isnan()) and int(dbias.isnan().sum()) == 1

@@ -131,11 +131,20 @@ def test_split_k_workspace():
     (dict(a_row=2, a_col=2), g.ERR_LD), (dict(db_row=2, db_col=2), g.ERR_LD),
     (dict(db_row=1, db_col=127), g.ERR_LD), (dict(dbias=7 * G + 1), g.ERR_OPTS),
     (dict(da=G), g.ERR_OVERLAP), (dict(db=3 * G), g.ERR_OVERLAP), (dict(dbias=4 * G), g.ERR_OVERLAP),
-    (dict(da=6 * G + 64), g.ERR_OVERLAP), (dict(workspace=0), g.ERR_WORKSPACE),
-    (dict(workspace_bytes=100), g.ERR_WORKSPACE), (dict(workspace=8 * G + 4), g.ERR_WORKSPACE),
-    (dict(workspace=2 * G), g.ERR_OVERLAP)])
+    (dict(da=6 * G + 64), g.ERR_OVERLAP)])
 def test_backward_refusals(change, code):
     assert backward(**change) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(workspace=0), g.ERR_WORKSPACE), (dict(workspace_bytes=100), g.ERR_WORKSPACE),
+    (dict(workspace=8 * G + 4), g.ERR_WORKSPACE), (dict(workspace=2 * G), g.ERR_OVERLAP)])
+def test_backward_workspace_refusals(change, code):
+    """A large pass keeps dpre and partial sums in its workspace."""
+    large = dict(m=4096, n=4096, k=4096, dc_row=4096, a_row=4096, b_col=4096, pre_row=4096,
+                 da_row=4096, db_col=4096)
+    assert backward("linear_backward_workspace", **large) >= 4096 * 4096 * 2
+    assert backward(**large, **change) == code
 
 
 def test_backward_with_nothing_to_do():
