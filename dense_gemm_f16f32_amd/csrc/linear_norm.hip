@@ -48,12 +48,12 @@ bool conflict(const Region* w, int nw, const Region* r, int nr) {
   return false;
 }
 
-// A row-major matrix: row stride (of no meaning for one row) and alignment.
+// A row-major matrix: row stride (of no meaning without a second row) and alignment.
 int check_rows(const void* p, int64_t rows, int64_t cols, int64_t* ld, int64_t elem, bool needed) {
+  if (rows <= 1 || cols == 0) *ld = cols > 0 ? cols : 1;
   if (rows == 0 || cols == 0) return GEMM_F16F32_OK;
   if (p == nullptr) return needed ? GEMM_F16F32_ERR_NULL : GEMM_F16F32_OK;
   if ((uintptr_t)p % elem) return GEMM_F16F32_ERR_OPTS;
-  if (rows == 1) *ld = cols;
   if (*ld < cols) return GEMM_F16F32_ERR_LD;
   // byte offsets inside the matrix stay below 2^62
   if (*ld > ((int64_t)1 << 60) / rows) return GEMM_F16F32_ERR_TOO_LARGE;
@@ -213,8 +213,8 @@ int plan_product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a
   if (rc != GEMM_F16F32_OK) return rc;
   p->cost = p->part[0].g.cost;
   // In one piece a sliver costs a whole row of tiles, or a second round of workgroups; cut off, a
-  // launch (about 2.5 us) and what its shape takes (4095 x 4097 x 4093: 157 us in one piece, 134
-  // in two).
+  // launch (about 2.5 us) and what its shape takes (4095 x 4097 x 4093: 145 us in one piece, 135
+  // in two; 4097 x 4096 x 4096: 132 and 116).
   const int64_t rm = M > 256 ? M % 256 : 0, rn = N > 256 ? N % 256 : 0;
   for (int cut = 1; cut < 4 && p->part[0].g.path == lk::kPathTiles; ++cut) {
     const int64_t cm = cut & 1 ? rm : 0, cn = cut & 2 ? rn : 0;
@@ -255,8 +255,10 @@ LinArgs product(int64_t type, int64_t K, const Operand& a, const Operand& b) {
 LinArgs part_args(const LinArgs& whole, const Part& t, void* ws) {
   const GemmPlan& g = t.g;
   LinArgs p = whole;
-  p.A += g.akm ? t.m0 * p.lda : t.m0;
-  p.B += g.bkm ? t.n0 * p.ldb : t.n0;
+  if (p.K > 0) {   // else there are no operands
+    p.A += g.akm ? t.m0 * p.lda : t.m0;
+    p.B += g.bkm ? t.n0 * p.ldb : t.n0;
+  }
   p.out += t.m0 * p.ldo + t.n0;
   if (p.pre) p.pre += t.m0 * p.ldp + t.n0;
   if (p.res) p.res += t.m0 * p.ldr + t.n0;
@@ -408,7 +410,7 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
       f->part_bytes = round_up(partial_bytes(f->row_blocks, x.n), 256);
     }
   }
-  const int64_t ldd = act ? f->ldd : (x.dc_row > 0 ? x.dc_row : 1);
+  const int64_t ldd = act ? f->ldd : x.dc_row;
   if (x.da && x.m > 0 && x.k > 0) {
     const Operand d = {x.dc, ldd, true};
     rc = plan_product(x.type, x.m, x.k, x.n, d, f->b, &f->qa);
