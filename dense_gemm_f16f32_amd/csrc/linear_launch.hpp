@@ -59,12 +59,14 @@ template <int TY>
 hipError_t launch_type(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
   const dim3 grid((uint32_t)g.grid());
   if (g.path == kPathSkinnyK) {
-    if (g.cols == 16)
-      hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8>), grid, dim3(512), 0, s, a);
+    if (a.K < (TY == kE4M3 ? 16 : 8))   // such rows need no more than one wave
+      hipLaunchKernelGGL((lin_skinny_k<TY, 1, 1, true>), grid, dim3(64), 0, s, a);
+    else if (g.cols == 16)
+      hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8, false>), grid, dim3(512), 0, s, a);
     else if (g.cols == 32)
-      hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8>), grid, dim3(512), 0, s, a);
+      hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8, false>), grid, dim3(512), 0, s, a);
     else
-      hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8>), grid, dim3(512), 0, s, a);
+      hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8, false>), grid, dim3(512), 0, s, a);
   } else if (g.path == kPathSkinnyN) {
     if constexpr (TY != kE4M3) {
       hipLaunchKernelGGL((lin_skinny_n<TY, 4, 8>), grid, dim3(512), 0, s, a);

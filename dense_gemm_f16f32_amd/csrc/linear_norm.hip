@@ -134,7 +134,8 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
   g->akm = a.km;
   g->bkm = b.km;
   const int64_t panels = cdiv(K, lk::kTileDepth * E);
-  if (M <= lk::kSkinnyRows && a.km) {
+  // few rows (and where b is row-major, rows that its loads fit into)
+  if (M <= lk::kSkinnyRows && a.km && (b.km || (N >= 4 && K >= 8))) {
     g->path = b.km ? lk::kPathSkinnyK : lk::kPathSkinnyN;
     const int64_t depth = b.km ? panels : cdiv(K, 32);
     // b k-contiguous: a is read once per workgroup, so with many rows the workgroups take more
@@ -143,8 +144,8 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     // slices; one row, bf16, 16384 x 4096: 23.8 and 25.8).
     const int64_t wide = cdiv(N, 64);
     g->cols = 64;
-    if (b.km && (M <= 8 || (wide < kCUs && (2 * wide < kCUs || depth < 64))))
-      g->cols = M > 8 && 2 * wide >= kCUs ? 32 : 16;
+    if (b.km && (M <= 8 || K < 16 || (wide < kCUs && (2 * wide < kCUs || depth < 64))))
+      g->cols = M > 8 && K >= 16 && 2 * wide >= kCUs ? 32 : 16;
     g->programs = cdiv(N, g->cols);
     // Few columns leave CUs idle: slices of k, of 16 units at least, up to a workgroup a CU.
     // Below 64 units the second launch costs more (512 columns, K = 8192: 7.0 against 12 us; 1024

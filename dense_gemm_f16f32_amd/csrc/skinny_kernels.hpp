@@ -7,6 +7,18 @@
 
 namespace lk {
 
+// 8 e4m3 values as f16, which holds them exactly.  The 8-bit matrix instruction rounds inside:
+// its sums are off by up to 2^-13 of the products' magnitudes for K = 7 and 2^-18 for K = 1000
+// (f16: 2^-22).  Here, where memory bounds the product, the f16 instruction costs no time.
+__device__ __forceinline__ int4v halves(int lo, int hi) {
+  int4v v;
+  v[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false));
+  v[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true));
+  v[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false));
+  v[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true));
+  return v;
+}
+
 template <int TY>
 __device__ __forceinline__ void mma16x16(float4v& acc, const int4v& a, const int4v& b) {
   if constexpr (TY == kF16)
@@ -20,14 +32,21 @@ __device__ __forceinline__ void mma16x16(float4v& acc, const int4v& a, const int
 __device__ __forceinline__ int4v load16(const uint16_t* p) {
   return __builtin_bit_cast(int4v, *(const u32x4_any*)p);
 }
-// 16 bytes of a k-contiguous row from k element k on; elements past K are 0 and not read.
-template <int TY>
-__device__ __forceinline__ int4v load16_tail(const uint16_t* row, int k, int K) {
-  constexpr int E = TY == kE4M3 ? 16 : 8;
-  if (k + E <= K) return load16(row + (TY == kE4M3 ? k / 2 : k));
+// 16 bytes of a k-contiguous row of K elements, from element k on; past the row's end they are 0
+// and not read.  chunk_load takes the row's last 16 bytes there, and chunk_shift moves them.  No
+// branch stands before a load or between loads: after one, the compiler waits for them.  Rows
+// below 16 bytes (SHORT) are read element by element.
+template <int TY, bool SHORT>
+__device__ __forceinline__ u32x4 chunk_load(const uint16_t* row, int k, int K) {
+  constexpr int E = TY == kE4M3 ? 16 : 8, B = 16 / E;
+  if constexpr (!SHORT) {
+    typedef u32x4 any __attribute__((aligned(1)));
+    const int s = k + E <= K ? 0 : k + E - K;
+    return *(const any*)((const char*)row + (int64_t)(k - s) * B);
+  }
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
+  for (int e = 0; e < E - 1; ++e) {
     if (k + e < K) {
       if (TY == kE4M3)
         v[e / 4] |= (uint32_t)((const uint8_t*)row)[k + e] << (8 * (e % 4));
@@ -35,6 +54,14 @@ __device__ __forceinline__ int4v load16_tail(const uint16_t* row, int k, int K) 
         v[e / 2] |= (uint32_t)row[k + e] << (16 * (e % 2));
     }
   }
+  return v;
+}
+// `live`: whether the chunk counts at all (else 0).
+template <int TY, bool SHORT>
+__device__ __forceinline__ int4v chunk_shift(u32x4 v, int k, int K, bool live) {
+  constexpr int E = TY == kE4M3 ? 16 : 8, B = 16 / E;
+  if (!live) v = u32x4{0u, 0u, 0u, 0u};
+  if (!SHORT && k + E > K) v = shift_down(v, 8 * B * (k + E - K));
   return __builtin_bit_cast(int4v, v);
 }
 
@@ -76,10 +103,10 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
 // every row: lane l takes the 16-byte chunks l / 16 and 4 + l / 16 of row l % 16, of a and of b
 // alike, so the order of k inside the unit is the same for both.  The loads of U units are in
 // flight at once.
-template <int TY, int NB, int NW>
+template <int TY, int NB, int NW, bool SHORT>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   constexpr int UE = TY == kE4M3 ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk
-  constexpr int NC = 16 * NB, U = NB == 1 ? 4 : 2;
+  constexpr int NC = 16 * NB, U = 4;
   __shared__ float s[NW * 16 * (NC + 4)];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -99,9 +126,11 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   }
   auto mul = [&](int c, const int4v (&a)[2], const int4v (&b)[2]) __attribute__((always_inline)) {
     if constexpr (TY == kE4M3) {
-      acc[c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7),
-          __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7), acc[c], 0, 0, 0, 0, 0, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = 0; d < 4; d += 2)
+          mma16x16<kF16>(acc[c], halves(a[h][d], a[h][d + 1]), halves(b[h][d], b[h][d + 1]));
     } else {
       mma16x16<TY>(acc[c], a[0], b[0]);
       mma16x16<TY>(acc[c], a[1], b[1]);
@@ -123,22 +152,34 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
         for (int c = 0; c < NB; ++c) b[i][c][h] = load16(pb[c] + k);
         a[i][h] = load16(pa + k);
       }
+    // Every load is on its way before the first is used.  With one block of 16-bit columns the
+    // waves are many and small, and do without (16 rows of e4m3, 8192 x 8192: 18.9 -> 16.7 us; one
+    // of bf16, 16384 x 4096: 23.1 without, 24.0 with).
+    if constexpr (NB > 1 || TY == kE4M3) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
       for (int c = 0; c < NB; ++c) mul(c, a[i], b[i][c]);
   }
-  for (; u < u1; u += NW) {
-    int4v a[2], b[NB][2];
+  for (; u < u1; u += NW) {   // this wave's last units, the matrix's ragged one among them
+    u32x4 a[2], b[NB][2];
+    int k[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = u * UE + (h * 4 + g) * CE;
+      k[h] = u * UE + (h * 4 + g) * CE;
 #pragma unroll
-      for (int c = 0; c < NB; ++c) b[c][h] = load16_tail<TY>(pb[c], k, p.K);
-      a[h] = load16_tail<TY>(pa, k, p.K);
+      for (int c = 0; c < NB; ++c) b[c][h] = chunk_load<TY, SHORT>(pb[c], k[h], p.K);
+      a[h] = chunk_load<TY, SHORT>(pa, k[h], p.K);
     }
+    int4v av[2], bv[2];
 #pragma unroll
-    for (int c = 0; c < NB; ++c) mul(c, a, b[c]);
+    for (int h = 0; h < 2; ++h) av[h] = chunk_shift<TY, SHORT>(a[h], k[h], p.K, true);
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) bv[h] = chunk_shift<TY, SHORT>(b[c][h], k[h], p.K, true);
+      mul(c, av, bv);
+    }
   }
   join_waves<TY, NW, NC>(p, acc, (float GK_LDS*)s, n0, wk.w,
                          [](int c, int i) { return c * 16 + i; });
@@ -162,18 +203,21 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
   const uint16_t* const pa = p.A + (int64_t)(x < p.M ? x : p.M - 1) * p.lda + 8 * g;
   const int col = n0 + x * CP;
   const int have = p.N - col;          // this lane's columns that exist
-  // a lane without whole columns reads whole ones further left and shifts; see `row`
-  const uint16_t* const pb = p.B + (int64_t)(8 * g) * p.ldb + col;
+  // a lane without CP columns reads the row's last CP and shifts (rows have at least CP)
+  const int over = have >= CP ? 0 : CP - have;
+  const uint16_t* const pb = p.B + (int64_t)(8 * g) * p.ldb + col - over;
   float4v acc[CP];
 #pragma unroll
   for (int c = 0; c < CP; ++c) acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
   auto row = [&](const uint16_t* q) __attribute__((always_inline)) {
-    if (have >= CP) return (vec)*(const vec_any*)q;
-    vec v;
-#pragma unroll
-    for (int d = 0; d < CP / 2; ++d)
-      v[d] = (2 * d < have ? (uint32_t)q[2 * d] : 0u) |
-             (2 * d + 1 < have ? (uint32_t)q[2 * d + 1] << 16 : 0u);
+    return (vec)*(const vec_any*)q;
+  };
+  auto shift = [&](vec v) __attribute__((always_inline)) {
+    static_assert(CP == 4, "64 bits");
+    if (over > 0) {
+      const uint64_t b = over >= 4 ? 0 : __builtin_bit_cast(uint64_t, v) >> (16 * over);
+      v = __builtin_bit_cast(vec, b);
+    }
     return v;
   };
   auto mul = [&](const int4v& a, const vec (&b)[8]) __attribute__((always_inline)) {
@@ -205,15 +249,33 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
       a[i] = load16(pa + k);
     }
 #pragma unroll
-    for (int i = 0; i < U; ++i) mul(a[i], b[i]);
-  }
-  for (; u < u1; u += NW) {
-    const int k = u * 32;
-    vec b[8];
+    for (int i = 0; i < U; ++i) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      b[r] = k + 8 * g + r < p.K ? row(pb + ((int64_t)k + r) * p.ldb) : vec(0u);
-    mul(load16_tail<TY>(pa - 8 * g, k + 8 * g, p.K), b);
+      for (int r = 0; r < 8; ++r) b[i][r] = shift(b[i][r]);
+      mul(a[i], b[i]);
+    }
+  }
+  if (u < u1) {   // this wave's last units, at most U, the matrix's ragged one among them
+    u32x4 a[U];
+    vec b[U][8];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = (u + i * NW < u1 ? u + i * NW : u1 - 1) * 32 + 8 * g;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {   // k rows past the last: the last one, not counted
+        const int kr = k + r < p.K ? k + r : p.K - 1;
+        b[i][r] = row(pb + (int64_t)(kr - 8 * g) * p.ldb);
+      }
+      a[i] = chunk_load<TY, false>(pa - 8 * g, k, p.K);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const bool live = u + i * NW < u1;
+      const int k = (live ? u + i * NW : u1 - 1) * 32 + 8 * g;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) b[i][r] = live && k + r < p.K ? shift(b[i][r]) : vec(0u);
+      mul(chunk_shift<TY, false>(a[i], k, p.K, live), b[i]);
+    }
   }
   join_waves<TY, NW, NC>(p, acc, (float GK_LDS*)s, n0, wk.w,
                          [](int c, int i) { return i * CP + c; });

@@ -345,3 +345,20 @@ def test_backward_in_one_launch_keeps_nan_in_its_row_and_column():
         assert bool(rows[89].all()) and int(rows.sum()) == 40
         assert bool(cols[:, 3].all()) and int(cols.sum()) == 40
         assert bool(dbias[3].isnan()) and int(dbias.isnan().sum()) == 1
+
+
+@pytest.mark.parametrize("ty", DT)
+@pytest.mark.parametrize("bo", "rc")
+@pytest.mark.parametrize("n", [1, 3, 4, 5, 7, 61, 67, 130])
+@pytest.mark.parametrize("k", [1, 5, 7, 8, 9, 33, 63, 449, 519, 1025, 2047])
+def test_few_rows_at_every_edge(n, k, bo, ty):
+    """Row ends inside a chunk, a unit and a batch of units; NaN lies right after every row."""
+    for m in (1, 6, 16):
+        check(m, n, k, ty, "r", bo, "relu", bias=True, pad=1 + m % 2, offset=k % 2, seed=n + k)
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 70])
+@pytest.mark.parametrize("k", [1, 7, 15, 16, 17, 31, 100, 129, 1000, 1039, 4097])
+def test_few_rows_in_8_bits_at_every_edge(n, k):
+    for m in (1, 9):
+        check8(m, n, k, "f16", bias=True, seed=n + k)
