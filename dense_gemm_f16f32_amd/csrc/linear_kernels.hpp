@@ -8,9 +8,7 @@
 //    e4m3 operand of K values is a k-major matrix of K/2 slots, and one 64-byte piece of a row
 //    feeds v_mfma_f32_32x32x64_f8f6f4, twice the work of the 16-bit instruction on the same
 //    bytes (the unscaled form: scales are applied to the sum, in the epilogue).  Its inner sums
-//    are rounded to fewer bits than fp32 (measured: off by up to 2^-13 of the products'
-//    magnitudes for K = 7, 2^-17 for K = 1000); taking the values as f16 would be exact, at half
-//    the rate.
+//    are rounded to fewer bits than fp32 (see kHalvesK).
 //  * the ragged panel: when the panel depth does not divide K, the panel that holds the last
 //    K mod BK values is multiplied first, so that every other panel starts at a multiple of BK
 //    and keeps the alignment of its rows.
@@ -305,8 +303,10 @@ __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, floa
 // ---- tiles -----------------------------------------------------------------------------------
 // A BM x BN tile by WM x WN waves, panels of BK slots.  XB is the MFMA block: 32, or 16 (16-bit
 // types only).  One k step covers KD slots of both operands.
-template <int TY_, int BM_, int BN_, int BK_, bool AKM, bool BKM, int WM_, int WN_, int XB_>
+template <int TY_, int BM_, int BN_, int BK_, bool AKM, bool BKM, int WM_, int WN_, int XB_,
+          bool HALVES_ = false>
 struct Tile {
+  static constexpr bool HALVES = HALVES_;   // e4m3 values multiplied as f16 (see kHalvesK)
   static constexpr int TY = TY_, BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, XB = XB_;
   static constexpr int NW = WM * WN;
   using OA = gk::Opnd<BM, BK, AKM, WM, NW, XB>;
@@ -334,6 +334,20 @@ __device__ __forceinline__ typename T::Frag read_frag(const char GK_LDS* st,
   }
 }
 
+// 8 e4m3 values as f16, which holds them exactly.  The 8-bit matrix instruction rounds inside:
+// its sums are off by up to 2^-13 of the products' magnitudes for K = 7 and 2^-17 for K = 1000
+// (f16: 2^-22).  Where the product is bound by memory or by latency -- few rows, or K up to
+// kHalvesK -- the f16 instruction, of half the rate, costs little or nothing.
+constexpr int kHalvesK = 512;
+__device__ __forceinline__ int4v halves(int lo, int hi) {
+  int4v v;
+  v[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false));
+  v[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true));
+  v[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false));
+  v[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true));
+  return v;
+}
+
 // The blocks are computed transposed (b's columns as the rows of the product): a lane then holds
 // 4 consecutive columns of one row of the result -- with XB = 16, row l % 16, columns 4 (l / 16)
 // + v; with XB = 32, row l % 32, columns 8 (v / 4) + 4 (l / 32) + v % 4.
@@ -346,6 +360,12 @@ __device__ __forceinline__ void mma(typename T::Acc& acc, const typename T::Frag
   else if constexpr (T::TY == kBF16)
     acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
                                                   __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
+  else if constexpr (T::HALVES)
+#pragma unroll
+    for (int d = 0; d < 8; d += 2)
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          __builtin_bit_cast(half8, halves(b[d], b[d + 1])),
+          __builtin_bit_cast(half8, halves(a[d], a[d + 1])), acc, 0, 0, 0);
   else
     acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, 0, 0, 0, 0, 0, 0);
 }
@@ -716,9 +736,10 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, co
     S[3] = (char GK_LDS*)stage3;                                                 \
   }
 
-template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM>
+template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM,
+          bool HALVES>
 __global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
-  using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32>;
+  using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32, HALVES>;
   LK_DECLARE_STAGES(NS, T::STAGE)
   int m0, n0;
   const Work k = work_of<BM, BN>(p, blockIdx.x);

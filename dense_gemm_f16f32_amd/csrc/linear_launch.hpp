@@ -30,22 +30,26 @@ struct GemmPlan {
   int64_t grid() const { return whole + (programs - whole) * splits; }
 };
 
-template <int TY, bool AKM, bool BKM>
-void launch_tile(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
+template <int TY, bool AKM, bool BKM, bool HALVES>
+void launch_staged(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
   // operands of a panel are read as many k steps ahead as a panel of the type has, less one
   constexpr int RD = TY == kE4M3 ? 1 : 3;
-  switch (g.tile) {
-    case kTile256:
-      hipLaunchKernelGGL((lin_ring<TY, AKM, BKM>), grid, dim3(256), 0, s, a);
-      break;
-    case kTile128:
-      hipLaunchKernelGGL((lin_staged<TY, 128, 128, 64, 2, RD, 2, 2, AKM, BKM>), grid, dim3(256), 0,
-                         s, a);
-      break;
-    default:
-      hipLaunchKernelGGL((lin_staged<TY, 64, 64, 64, 4, RD, 2, 2, AKM, BKM>), grid, dim3(256), 0, s,
-                         a);
-  }
+  if (g.tile == kTile128)
+    hipLaunchKernelGGL((lin_staged<TY, 128, 128, 64, 2, RD, 2, 2, AKM, BKM, HALVES>), grid,
+                       dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((lin_staged<TY, 64, 64, 64, 4, RD, 2, 2, AKM, BKM, HALVES>), grid,
+                       dim3(256), 0, s, a);
+}
+
+template <int TY, bool AKM, bool BKM>
+void launch_tile(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
+  if (g.tile == kTile256)
+    hipLaunchKernelGGL((lin_ring<TY, AKM, BKM>), grid, dim3(256), 0, s, a);
+  else if (TY == kE4M3 && a.K <= kHalvesK)
+    launch_staged<TY, AKM, BKM, TY == kE4M3>(g, a, grid, s);
+  else
+    launch_staged<TY, AKM, BKM, false>(g, a, grid, s);
 }
 
 template <int TY, int BM, int BN>

@@ -161,6 +161,8 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     for (int t = 0; t < lk::kTiles; ++t) {
       const lk::TileShape& s = lk::kTileShapes[t];
       const TileCost& c = kTileCosts[t];
+      // short 8-bit sums are taken as f16, which the largest tile does not do
+      if (t == lk::kTile256 && type == LINEAR_NORM_E4M3 && K <= lk::kHalvesK) continue;
       // panels' 32-bit offsets
       const int64_t ra = a.km ? s.bm : lk::kTileDepth, rb = b.km ? s.bn : lk::kTileDepth;
       if (ra * (a.ld / E) >= kMax || rb * (b.ld / E) >= kMax) continue;

@@ -7,18 +7,6 @@
 
 namespace lk {
 
-// 8 e4m3 values as f16, which holds them exactly.  The 8-bit matrix instruction rounds inside:
-// its sums are off by up to 2^-13 of the products' magnitudes for K = 7 and 2^-18 for K = 1000
-// (f16: 2^-22).  Here, where memory bounds the product, the f16 instruction costs no time.
-__device__ __forceinline__ int4v halves(int lo, int hi) {
-  int4v v;
-  v[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false));
-  v[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true));
-  v[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false));
-  v[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true));
-  return v;
-}
-
 template <int TY>
 __device__ __forceinline__ void mma16x16(float4v& acc, const int4v& a, const int4v& b) {
   if constexpr (TY == kF16)

@@ -17,10 +17,10 @@
  * ties to even), with one exception: dpre is rounded to the operands' type before it enters
  * the matrix products (their operands are 16 bits wide).  dbias sums the unrounded values.
  *
- * 8-bit operands: up to 16 rows (m) are multiplied as f16, exactly.  More rows go through the
- * 8-bit matrix instruction, which rounds inside: measured over random operands, a sum is off by
- * up to 2^-13 of the sum of its products' magnitudes for k = 7, 2^-15 for k = 128 and 2^-17 for
- * k = 1000.
+ * 8-bit operands: with up to 16 rows (m) or k up to 512 the values are multiplied as f16,
+ * exactly.  Beyond, they go through the 8-bit matrix instruction, which rounds inside: measured
+ * over random operands, a sum is off by up to 2^-17 of the sum of its products' magnitudes at k
+ * = 1000.
  *
  * Activations: none, relu, gelu (0.5 v (1 + erf(v / sqrt 2))), gelu_tanh (the tanh form of it),
  * silu (v / (1 + exp(-v))).  relu's slope at 0 is 0.

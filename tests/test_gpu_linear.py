@@ -362,3 +362,20 @@ def test_few_rows_at_every_edge(n, k, bo, ty):
 def test_few_rows_in_8_bits_at_every_edge(n, k):
     for m in (1, 9):
         check8(m, n, k, "f16", bias=True, seed=n + k)
+
+
+@pytest.mark.parametrize("m,n", [(17, 70), (200, 130), (2100, 2050)])
+@pytest.mark.parametrize("k", [1, 16, 40, 130, 512])
+def test_short_8_bit_sums_are_exact_to_fp32(m, n, k):
+    """The residual takes the rounded result away, so that the sum's own error shows: (k + 8)
+    2^-23 of the products' magnitudes, and 2^-11 of what is left."""
+    q = gen(k)
+    a, sa = e4m3_rows(torch.randn((m, k), generator=q, device="cuda"))
+    w, sb = e4m3_rows(torch.randn((n, k), generator=q, device="cuda"))
+    kw = dict(scale_a=sa, scale_b=sb, out_dtype=torch.float16)
+    first = g.linear(a, w.t(), **kw)
+    rest = g.linear(a, w.t(), residual=-first, **kw)
+    _, v, err, _ = linear64(a, w.t(), None, None, "none", sa, sb)
+    left = rest.double() - (v - first.double())
+    bound = err + 6 * F32 * v.abs() + half_step(torch.float16) * rest.double().abs() + 2.0 ** -25
+    assert bool((left.abs() <= bound).all())
