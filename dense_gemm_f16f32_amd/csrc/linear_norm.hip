@@ -140,16 +140,16 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     const int64_t depth = b.km ? panels : cdiv(K, 32);
     // b k-contiguous: a is read once per workgroup, so with many rows the workgroups take more
     // columns, as long as the CUs have one each, if need be in two slices of k (e4m3, 16 x 16384
-    // x 4096: 16 columns 18.4 us, 64 columns 13.6; 16 x 8192 x 8192: 18.6, and 16.1 in two
-    // slices; one row, bf16, 16384 x 4096: 23.8 and 25.8).
+    // x 4096: 16 columns 19.5 us, 64 columns 14.1; 16 x 8192 x 8192: 18.8, and 16.4 in two
+    // slices; one row, bf16, 16384 x 4096: 24.1 and 25.0).
     const int64_t wide = cdiv(N, 64);
     g->cols = 64;
     if (b.km && (M <= 8 || K < 16 || (wide < kCUs && (2 * wide < kCUs || depth < 64))))
       g->cols = M > 8 && K >= 16 && 2 * wide >= kCUs ? 32 : 16;
     g->programs = cdiv(N, g->cols);
     // Few columns leave CUs idle: slices of k, of 16 units at least, up to a workgroup a CU.
-    // Below 64 units the second launch costs more (512 columns, K = 8192: 7.0 against 12 us; 1024
-    // columns in e4m3, K = 4096: 6.5 against 5.5).
+    // Below 64 units the second launch costs more (4 rows, 512 columns, K = 8192 in bf16: 6.8 us
+    // in 8 slices, 13.0 in one; 1024 columns, K = 4096 in e4m3: 6.2 in 4, 5.9 in one).
     int64_t z = 1;
     while (depth >= 64 && z < 16 && g->programs * z * 2 <= kCUs && depth / (z * 2) >= 16) z *= 2;
     set_split(g, 0, depth, z, 16 * g->cols);

