@@ -403,7 +403,8 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
   }
   if (f->dact) {
     const int64_t cols = cdiv(x.n, 512);
-    int64_t blocks = cdiv(x.m, 16);
+    // a row a thread, up to 4 workgroups a CU (512^3 f16 with silu: 9.0 us in all; 4 rows: 10.7)
+    int64_t blocks = cdiv(x.m, 4);
     const int64_t most = cdiv(4 * kCUs, cols);
     if (blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;
@@ -437,8 +438,9 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     const double two = f->qa.cost + f->qb.cost + 2.0 + (f->part_bytes > 0 ? 2.0 : 0.0);
     f->pair = fits && pa + pb <= 2 * kCUs && round_cost(kTileCosts[lk::kTile64], pa + pb, deep) < two;
     // The element-wise pass as well while a tile's panels are few: its loads go through
-    // registers, three panels ahead, and a panel costs 1.1 - 1.8 us instead of 0.3 (f16, silu: 64^3
-    // 4.8 against 13.7 us in two launches, 300^3 11.8 and 12.1, 512^3 13.0 and 10.8).
+    // registers, three panels ahead, and a panel costs about 1.2 us instead of 0.3, for a launch
+    // less (3 us of host time; f16, silu: 64^3 4.6 us against 8.2 in two launches, 128^3 5.8 and
+    // 7.6, 256^3 8.1 and 7.5, 300^3 11.8 and 9.6).
     f->small = f->pair && deep <= 4 && x.n >= 8 && x.k >= 8;
     if (f->pair) {
       GemmPlan t = {};
