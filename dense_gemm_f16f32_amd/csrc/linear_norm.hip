@@ -435,8 +435,15 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     const int64_t deep = cdiv(x.m > x.n ? x.m : x.n, lk::kTileDepth);
     const int64_t most = 64, lb = f->b.ld > ldd ? f->b.ld : ldd;
     const bool fits = most * lb < kMax && most * f->a.ld < kMax;
+    // as long as its deepest tile, or as all its tiles' work takes
+    const TileCost& c = kTileCosts[lk::kTile64];
+    const int64_t slots = (int64_t)kCUs * c.per_cu, P = pa + pb;
+    const double work = pa * (double)cdiv(x.n, 64) + pb * (double)cdiv(x.m, 64);
+    double one = round_cost(c, P < kCUs ? P : kCUs, deep);
+    const double all = (c.fixed * P + c.panel * work) / slots;
+    if (all > one) one = all;
     const double two = f->qa.cost + f->qb.cost + 2.0 + (f->part_bytes > 0 ? 2.0 : 0.0);
-    f->pair = fits && pa + pb <= 2 * kCUs && round_cost(kTileCosts[lk::kTile64], pa + pb, deep) < two;
+    f->pair = fits && P <= 4 * kCUs && one < two;
     // The element-wise pass as well while a tile's panels are few: its loads go through
     // registers, three panels ahead, and a panel costs about 1.2 us instead of 0.3, for a launch
     // less (3 us of host time; f16, silu: 64^3 4.6 us against 8.2 in two launches, 128^3 5.8 and
@@ -513,13 +520,24 @@ void norm_backward(const nk::NormBwdArgs& p, int grid, hipStream_t s) {
 
 // Workgroups of the norm's backward pass, each with partial dweight sums: two a CU keep enough
 // loads in flight (8192 x 4096: 45.5 us; four a CU 52.7, their sums being written and read).
+// Few rows, 2 for each that a workgroup works on at once, take one workgroup, which writes dweight
+// itself: a launch less (1 x 4096: 3.6 us against 5.8, and 3 us of host time; with 8 for each the
+// kernel took longer than the launch, 8 x 4096 11.8 us against 6.0).
 int backward_groups(int64_t rows, int64_t dim) {
-  const int64_t n = dim <= kShortRow ? cdiv(rows, 4) : rows;
+  const int64_t at_once = dim <= kShortRow ? 4 : 1;
+  if (dim <= kLongRow && rows <= 2 * at_once) return rows > 0;
+  const int64_t n = cdiv(rows, at_once);
   return (int)(n < 2 * kCUs ? n : 2 * kCUs);
+}
+// Whether dweight needs a second step.
+bool backward_sums(int64_t rows, int64_t dim) {
+  return dim > kLongRow || backward_groups(rows, dim) != 1;
 }
 
 int64_t norm_backward_bytes(const rms_norm_backward_args& x) {
-  return x.dweight ? partial_bytes(backward_groups(x.rows, x.dim), x.dim) : 0;
+  return x.dweight && backward_sums(x.rows, x.dim)
+             ? partial_bytes(backward_groups(x.rows, x.dim), x.dim)
+             : 0;
 }
 
 template <int TY>
@@ -776,14 +794,16 @@ int rms_norm_backward(const rms_norm_backward_args* args) {
     p.dh_row = x.dh_row;
     p.dx = (uint16_t*)x.dx;
     p.dx_row = x.dx_row;
-    p.part = x.dweight ? (float*)x.workspace : nullptr;
+    const bool sums = backward_sums(x.rows, x.dim);
+    p.part = x.dweight && sums ? (float*)x.workspace : nullptr;
+    p.dweight = sums ? nullptr : (uint16_t*)x.dweight;
       p.rows = (int32_t)x.rows;
     p.dim = (int32_t)x.dim;
     p.inv_dim = (float)(1.0 / (double)x.dim);
     bf ? norm_backward<lk::kBF16>(p, groups, s) : norm_backward<lk::kF16>(p, groups, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
-  if (x.dweight) {
+  if (x.dweight && backward_sums(x.rows, x.dim)) {
     bf ? launch_sum<lk::kBF16>((const float*)x.workspace, groups, x.dim, x.dweight, s)
        : launch_sum<lk::kF16>((const float*)x.workspace, groups, x.dim, x.dweight, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;

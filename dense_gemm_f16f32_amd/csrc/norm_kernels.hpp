@@ -198,7 +198,7 @@ struct NormBwdArgs {
   const uint16_t* dh;
   uint16_t* dx;
   uint16_t* dweight;
-  float* part;   // partial dweight sums of every workgroup, or null
+  float* part;   // partial dweight sums of every workgroup; null: dweight itself, or nothing
   int64_t dy_row, h_row, dh_row, dx_row;
   int32_t rows, dim;
   float inv_dim;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
     }
     cur = nxt;
   }
-  if (p.part == nullptr) return;
+  if (p.part == nullptr && p.dweight == nullptr) return;
   if constexpr (RW > 1) {   // the other rows' sums, in their order
     __shared__ float sdw[RW - 1][C * 512];
     if (rw > 0) {
@@ -316,7 +316,11 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int col = c0 + i * STEP;
-    if (col < p.dim) store_partial8(p.part, gridDim.x, blockIdx.x, col, dw[i]);
+    if (col >= p.dim) continue;
+    if (p.part != nullptr)
+      store_partial8(p.part, gridDim.x, blockIdx.x, col, dw[i]);
+    else   // the only workgroup
+      store8(p.dweight + col, dw[i], p.dim - col, TY);
   }
 }
 

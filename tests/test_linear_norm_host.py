@@ -65,7 +65,7 @@ def norm(**change):
 
 
 def norm_backward(call="rms_norm_backward", **change):
-    base = dict(rows=4, dim=64, type=F16, dy=G, dy_row=64, h=2 * G, h_row=64, weight=3 * G,
+    base = dict(rows=400, dim=64, type=F16, dy=G, dy_row=64, h=2 * G, h_row=64, weight=3 * G,
                 rstd=4 * G, dh=5 * G, dh_row=64, dx=6 * G, dx_row=64, dweight=7 * G,
                 workspace=8 * G, workspace_bytes=G)
     return getattr(ln.lib(), call)(args(NORM_BACKWARD, NORM_BACKWARD_STRUCT, base, **change))
@@ -184,6 +184,9 @@ def test_norm_without_rows():
     assert norm(rows=0, x=0, residual=0, weight=0, y=0, h=0, rstd=0) == g.OK
     assert norm_backward("rms_norm_backward_workspace", rows=0) == 0
     assert norm_backward("rms_norm_backward_workspace", dweight=0) == 0
+    # few rows: one workgroup, which needs none
+    assert norm_backward("rms_norm_backward_workspace") > 0
+    assert norm_backward("rms_norm_backward_workspace", rows=4) == 0
 
 
 def test_structures_match_the_header():
