@@ -62,14 +62,32 @@ __device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
 __device__ __forceinline__ uint32_t abs_bits(float v) {
   return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
 }
-// 8 values to e4m3, nearest, ties to even (|v| <= 448 up to the rounding of 1 / scale)
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], float inv) {
+// A row's 8-bit scale, with what a division by it takes: the rounded reciprocal, and the scale
+// again for the remainder (0 for an infinite scale, whose quotients are 0, or NaN).
+struct Divisor {
+  float inv, scale;
+};
+__device__ __forceinline__ Divisor divisor(float scale) {
+  return {1.f / scale, scale <= 3.40282347e38f ? scale : 0.f};
+}
+// v / scale: the product with the rounded reciprocal, and the remainder that it leaves (exact in
+// one fma) divided the same way.  Without that step the quotient is off by up to 2^-23 of itself
+// and crosses a tie of the 8-bit rounding once in about 2^20 values.
+__device__ __forceinline__ float quotient(float v, Divisor d) {
+  const float q = v * d.inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, d.scale, v), d.inv, q);
+}
+// 8 quotients to e4m3, nearest, ties to even (at most 448 up to the rounding of the scale)
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], Divisor d) {
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = quotient(v[e], d);
   uint2 o;
   int lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, hi, true);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
   o.x = (uint32_t)lo;
   o.y = (uint32_t)hi;
   return o;
@@ -77,8 +95,8 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], float inv) {
 struct __attribute__((packed)) Bytes8 {
   uint32_t x, y;
 };
-__device__ __forceinline__ void store_e4m3x8(uint8_t* p, const float (&v)[8], float inv, int n) {
-  const uint2 q = to_e4m3x8(v, inv);
+__device__ __forceinline__ void store_e4m3x8(uint8_t* p, const float (&v)[8], Divisor d, int n) {
+  const uint2 q = to_e4m3x8(v, d);
   if (n >= 8) {
     *(Bytes8*)p = Bytes8{q.x, q.y};
   } else {
@@ -153,7 +171,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
         v[e] = v[e] * rstd * w[e];
     }
   };
-  float inv = 1.f;
+  Divisor by = {1.f, 1.f};
   if constexpr (Q8) {
     uint32_t m = 0u;
 #pragma unroll CR
@@ -168,7 +186,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
     }
     const float scale = e4m3_scale(group_max<NW>(m, smax));
     if (threadIdx.x == 0) p.scale[row] = scale;
-    inv = 1.f / scale;
+    by = divisor(scale);
   }
 #pragma unroll CR
   for (int i = 0; i < steps; ++i) {
@@ -177,7 +195,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
     float v[8];
     norm(i, v);
     if constexpr (Q8)
-      store_e4m3x8((uint8_t*)p.y + row * p.y_row + col, v, inv, p.dim - col);
+      store_e4m3x8((uint8_t*)p.y + row * p.y_row + col, v, by, p.dim - col);
     else
       store8((uint16_t*)p.y + row * p.y_row + col, v, p.dim - col, TY);
     // h may be x's or the residual's memory: without registers it is written last
