@@ -282,9 +282,10 @@ __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, floa
                                         const Columns& c) {
   const int ot = TY == kE4M3 ? p.out_type : TY;
   if (TY == kE4M3) {
+    // one scale after the other: their product can leave fp32's range where the result does not
     const float sa = p.scale_a ? p.scale_a[row] : 1.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * (sa * c.sb[e]) + c.bias[e];
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * sa * c.sb[e] + c.bias[e];
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += c.bias[e];
@@ -539,7 +540,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float v = e < 4 ? lo[e & 3] : hi[e & 3];
-          f[u * 8 + e] = T::TY == kE4M3 ? v * (sa[u] * c.sb[e]) + c.bias[e] : v + c.bias[e];
+          f[u * 8 + e] = T::TY == kE4M3 ? v * sa[u] * c.sb[e] + c.bias[e] : v + c.bias[e];
         }
       }
       auto put = [&](uint16_t* base, int64_t ld) __attribute__((always_inline)) {
