@@ -207,9 +207,11 @@ __device__ __forceinline__ float act_slope(float v, int act) {
       return c + v * e * 0.39894228040143268f;   // 1 / sqrt(2 pi)
     }
     case LINEAR_ACT_GELU_TANH: {
-      // v p(2u): p + v p (1 - p) 2u'.  p (1 - p) is 0 long before v^2 overflows.
+      // v p(2u): p + v p (1 - p) 2u'.  p (1 - p) is 0 long before v^2 overflows, and then the
+      // slope is p: the product would be 0 times infinity from |v| = 1.8e19 on.
       const float p = sigmoid(2.f * kTanhC * (v + 0.044715f * v * v * v));
-      return p + v * p * (1.f - p) * (2.f * kTanhC) * (1.f + 0.134145f * v * v);
+      const float d = p * (1.f - p);
+      return d == 0.f ? p : p + v * d * (2.f * kTanhC) * (1.f + 0.134145f * v * v);
     }
     case LINEAR_ACT_SILU: {
       const float p = sigmoid(v);
