@@ -153,7 +153,25 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
       for (int e = 0; e < 8; ++e) sum += hv[0][e] * hv[0][e];
     }
   }
-  const float rstd = 1.f / sqrtf(group_sum<NW>(sum, ssum) * p.inv_dim + p.eps);
+  float square = group_sum<NW>(sum, ssum) * p.inv_dim + p.eps, unit = 1.f;
+  // Squares outside fp32's range (bf16 rows above 1e19, or below 1e-9 with a tiny eps) are summed
+  // again in units that bring them into it; every thread of the row holds the same sum.
+  if (square < 0x1p-60f || square == __builtin_inff()) {
+    unit = square < 1.f ? 0x1p64f : 0x1p-96f;
+    if constexpr (NW > 1) __syncthreads();   // the first sum has been read
+    sum = 0.f;
+#pragma unroll CR
+    for (int i = 0; i < steps; ++i) {
+      if constexpr (C == 0) load_h(c0 + i * STEP, hv[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = hv[C > 0 ? i : 0][e] * unit;
+        sum += v * v;
+      }
+    }
+    square = group_sum<NW>(sum, ssum) * p.inv_dim + p.eps * unit * unit;
+  }
+  const float rstd = unit / sqrtf(square);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
   // y of step i
   auto norm = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
