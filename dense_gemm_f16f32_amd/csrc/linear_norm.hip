@@ -14,6 +14,7 @@ using lk::GemmPlan;
 using lk::LinArgs;
 
 constexpr int64_t kMax = (int64_t)1 << 31;
+constexpr int64_t kThreads = (int64_t)1 << 32;   // a launch has fewer
 constexpr int kCUs = 256;
 
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
@@ -134,8 +135,9 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
   g->akm = a.km;
   g->bkm = b.km;
   const int64_t panels = cdiv(K, lk::kTileDepth * E);
-  // few rows (and where b is row-major, rows that its loads fit into)
-  if (M <= lk::kSkinnyRows && a.km && (b.km || (N >= 4 && K >= 8))) {
+  // few rows (and where b is row-major, rows that its loads fit into), in a launch's threads
+  if (M <= lk::kSkinnyRows && a.km && (b.km || (N >= 4 && K >= 8)) &&
+      cdiv(N, 64) * 512 < kThreads) {
     g->path = b.km ? lk::kPathSkinnyK : lk::kPathSkinnyN;
     const int64_t depth = b.km ? panels : cdiv(K, 32);
     // b k-contiguous: a is read once per workgroup, so with many rows the workgroups take more
@@ -146,6 +148,7 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     g->cols = 64;
     if (b.km && (M <= 8 || K < 16 || (wide < kCUs && (2 * wide < kCUs || depth < 64))))
       g->cols = M > 8 && K >= 16 && 2 * wide >= kCUs ? 32 : 16;
+    if (K >= 8 * E && cdiv(N, g->cols) * 512 >= kThreads) g->cols = 64;
     g->programs = cdiv(N, g->cols);
     // Few columns leave CUs idle: slices of k, of 16 units at least, up to a workgroup a CU.
     // Below 64 units the second launch costs more (4 rows, 512 columns, K = 8192 in bf16: 6.8 us
@@ -172,6 +175,7 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
         // full rounds, then the rest in slices; the second launch and the sums' way through
         // memory (mostly through the caches) for a split
         const int64_t per = cdiv(panels, splits), tail = P - whole;
+        if ((whole + tail * splits) * 256 >= kThreads) return;
         double cost = (double)(whole / slots) * round_cost(c, slots, panels);
         cost += round_cost(c, tail * splits, per);
         if (splits > 1) cost += 3.0 + (double)(tail * splits) * s.bm * s.bn * 8 / 8.0e6;
@@ -191,7 +195,6 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     *g = chosen;
     g->cost = best;
   }
-  if (g->grid() >= kMax) return GEMM_F16F32_ERR_TOO_LARGE;
   return GEMM_F16F32_OK;
 }
 
@@ -542,8 +545,12 @@ int64_t norm_backward_bytes(const rms_norm_backward_args& x) {
 
 template <int TY>
 void launch_sum(const float* part, int n, int64_t cols, void* out, hipStream_t s) {
-  hipLaunchKernelGGL((nk::sum_partials<TY>), dim3((uint32_t)cdiv(cols, 32)), dim3(256), 0, s, part, n,
-                     (int)cols, (uint16_t*)out);
+  const int64_t blocks = cdiv(cols, 32), most = kThreads / 256 - 1;
+  for (int64_t first = 0; first < blocks; first += most) {
+    const int64_t grid = blocks - first < most ? blocks - first : most;
+    hipLaunchKernelGGL((nk::sum_partials<TY>), dim3((uint32_t)grid), dim3(256), 0, s, part, n,
+                       (int)first, (int)cols, (uint16_t*)out);
+  }
 }
 
 }  // namespace

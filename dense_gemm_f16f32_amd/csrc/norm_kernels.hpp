@@ -411,11 +411,11 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
   }
 }
 
-// out[j] = the sum of n partial sums; one block of 32 columns a workgroup.
+// out[j] = the sum of n partial sums; one block of 32 columns a workgroup, from block `first` on.
 template <int TY>
-__global__ void __launch_bounds__(256) sum_partials(const float* part, int n, int cols,
+__global__ void __launch_bounds__(256) sum_partials(const float* part, int n, int first, int cols,
                                                     uint16_t* out) {
-  sum_block<TY>(part, n, blockIdx.x, cols, out);
+  sum_block<TY>(part, n, first + blockIdx.x, cols, out);
 }
 
 struct DactArgs {

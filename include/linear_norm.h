@@ -32,6 +32,11 @@
  * row-major with any row stride of at least their row length.  Stride arguments of an axis of
  * extent 1 are ignored.
  *
+ * Extents are below 2^31.  A product is refused with GEMM_F16F32_ERR_TOO_LARGE where the rows of
+ * a stored panel (64 if k is not the unit-stride axis, else a tile's 64 to 256) times the leading
+ * dimension reach 2^31 16-bit elements and it has more rows than the kernels for up to 16 take,
+ * or where its tiles need 2^32 threads.
+ *
  * Ownership and execution as in gemm_f16f32.h: every pointer is the caller's, nothing is
  * allocated, no state is kept, calls only enqueue kernels on `stream` (a hipStream_t) and may
  * be captured in a HIP graph.  Workspaces are sized by the *_workspace functions; they need no
