@@ -492,7 +492,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
   const int rr = lane / S::LANES, cc = (lane % S::LANES) * 8;
   const int col = n0 + wn * T::WTN + cc;
   const int row0 = m0 + wm * T::WTM + rr;
-  const bool whole = m0 + T::BM <= p.M && n0 + T::BN <= p.N;
+  const bool whole = T::BM <= p.M - m0 && T::BN <= p.N - n0;
   const int ot = T::TY == kE4M3 ? p.out_type : T::TY;
   const Columns c = load_columns<T::TY>(p, col);
   const float GK_LDS* const sr = s + rr * S::LDW + cc;
@@ -589,7 +589,7 @@ template <int TY, int BK>
 __device__ __forceinline__ Panels panels_of(int K) {
   constexpr int E = TY == kE4M3 ? 2 : 1;   // elements per slot
   Panels q;
-  q.k2 = (K + E - 1) / E;
+  q.k2 = K / E + K % E;   // E is 1 or 2; K + 1 need not fit
   q.rem = K % (BK * E);
   q.np = K / (BK * E) + (q.rem ? 1 : 0);
   q.first = K / (BK * E) * BK;

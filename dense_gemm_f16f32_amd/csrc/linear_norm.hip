@@ -410,6 +410,7 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     int64_t blocks = cdiv(x.m, 4);
     const int64_t most = cdiv(4 * kCUs, cols);
     if (blocks > most) blocks = most;
+    if (blocks < cdiv(x.m, 1 << 30)) blocks = cdiv(x.m, 1 << 30);   // the kernel's row counter
     if (blocks < 1) blocks = 1;
     f->rows_per_block = (int)round_up(cdiv(x.m, blocks), 4);
     f->row_blocks = x.m > 0 ? (int)cdiv(x.m, f->rows_per_block) : 0;

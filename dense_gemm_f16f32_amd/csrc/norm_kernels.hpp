@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
   const uint16_t* const res = p.res ? p.res + row * p.res_row : nullptr;
   uint16_t* const h = p.h ? p.h + row * p.h_row : nullptr;
   const int c0 = threadIdx.x * 8;
-  const int steps = C > 0 ? C : (p.dim + STEP - 1) / STEP;
+  const int steps = C > 0 ? C : (p.dim - 1) / STEP + 1;   // dim > 0; dim + STEP need not fit
   float hv[CR][8], wv[CR][8];
   auto load_h = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
     load8(v, x + col, p.dim - col, TY, back);
@@ -385,13 +385,13 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
       }
     };
     float g[8], x[8], d[8], sum = 0.f;
-    for (int col = c0; col < p.dim; col += STEP) {
+    for (uint32_t col = c0; col < (uint32_t)p.dim; col += STEP) {
       load(col, g, x, d);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += g[e] * x[e];
     }
     const float mean = group_sum<NW>(sum, ssum[turn]) * p.inv_dim;
-    for (int col = c0; col < p.dim; col += STEP) {
+    for (uint32_t col = c0; col < (uint32_t)p.dim; col += STEP) {
       float v[8];
       load(col, g, x, d);
       if (p.dh)
@@ -426,7 +426,7 @@ struct DactArgs {
   uint16_t* sum;         // the column sums themselves (one row block), or null
   int64_t dc_row, pre_row, dpre_row;
   int32_t m, n, act;
-  int32_t row_blocks, rows_per_block;
+  int32_t row_blocks, rows_per_block;   // at most 2^30
 };
 
 // dpre = dc act'(pre) and its column sums over a block of rows: 512 columns a workgroup, 4 rows
@@ -437,20 +437,25 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
   const int cb = blockIdx.x / p.row_blocks, rb = blockIdx.x - cb * p.row_blocks;
   const int t = threadIdx.x & 63, g = threadIdx.x >> 6;
   const int col = cb * 512 + t * 8, n = p.n - col;
-  const int r1 = (rb + 1) * p.rows_per_block < p.m ? (rb + 1) * p.rows_per_block : p.m;
+  // rows counted from the block's first: numbers past the last row need not fit 31 bits
+  const int64_t r0 = (int64_t)rb * p.rows_per_block;
+  const int rows = p.m - r0 < p.rows_per_block ? (int)(p.m - r0) : p.rows_per_block;
+  const uint16_t* const dc = p.dc + r0 * p.dc_row + col;
+  const uint16_t* const pre = p.pre + r0 * p.pre_row + col;
+  uint16_t* const dpre = p.dpre + r0 * p.dpre_row + col;
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
   if (n > 0) {
 #pragma unroll 4
-    for (int row = rb * p.rows_per_block + g; row < r1; row += 4) {
+    for (int row = g; row < rows; row += 4) {
       float v[8];
-      load8(v, p.dc + row * p.dc_row + col, n, TY, p.n >= 8);
+      load8(v, dc + row * p.dc_row, n, TY, p.n >= 8);
       if (p.pre) {
         float u[8];
-        load8(u, p.pre + row * p.pre_row + col, n, TY, p.n >= 8);
+        load8(u, pre + row * p.pre_row, n, TY, p.n >= 8);
         slope8(v, u, p.act);
-        store8(p.dpre + row * p.dpre_row + col, v, n, TY);
+        store8(dpre + row * p.dpre_row, v, n, TY);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += v[e];

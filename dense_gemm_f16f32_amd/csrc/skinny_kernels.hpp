@@ -23,14 +23,15 @@ __device__ __forceinline__ int4v load16(const uint16_t* p) {
 // 16 bytes of a k-contiguous row of K elements, from element k on; past the row's end they are 0
 // and not read.  chunk_load takes the row's last 16 bytes there, and chunk_shift moves them.  No
 // branch stands before a load or between loads: after one, the compiler waits for them.  Rows
-// below 16 bytes (SHORT) are read element by element.
+// below 16 bytes (SHORT) are read element by element.  k is unsigned: past the end of the longest
+// row it does not fit 31 bits.
 template <int TY, bool SHORT>
-__device__ __forceinline__ u32x4 chunk_load(const uint16_t* row, int k, int K) {
+__device__ __forceinline__ u32x4 chunk_load(const uint16_t* row, uint32_t k, uint32_t K) {
   constexpr int E = TY == kE4M3 ? 16 : 8, B = 16 / E;
   if constexpr (!SHORT) {
     typedef u32x4 any __attribute__((aligned(1)));
-    const int s = k + E <= K ? 0 : k + E - K;
-    return *(const any*)((const char*)row + (int64_t)(k - s) * B);
+    const uint32_t at = k + E <= K ? k : K - E;
+    return *(const any*)((const char*)row + (int64_t)at * B);
   }
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -46,10 +47,10 @@ __device__ __forceinline__ u32x4 chunk_load(const uint16_t* row, int k, int K) {
 }
 // `live`: whether the chunk counts at all (else 0).
 template <int TY, bool SHORT>
-__device__ __forceinline__ int4v chunk_shift(u32x4 v, int k, int K, bool live) {
+__device__ __forceinline__ int4v chunk_shift(u32x4 v, uint32_t k, uint32_t K, bool live) {
   constexpr int E = TY == kE4M3 ? 16 : 8, B = 16 / E;
   if (!live) v = u32x4{0u, 0u, 0u, 0u};
-  if (!SHORT && k + E > K) v = shift_down(v, 8 * B * (k + E - K));
+  if (!SHORT && k + E > K) v = shift_down(v, (int)(8 * B * (k + E - K)));
   return __builtin_bit_cast(int4v, v);
 }
 
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
       mma16x16<TY>(acc[c], a[1], b[1]);
     }
   };
-  const int units = (p.K + UE - 1) / UE, whole = p.K / UE;
+  const int whole = p.K / UE, units = whole + (p.K % UE != 0);
   const int u0 = wk.z < 0 ? 0 : wk.z * p.per_split;
   const int u1 = wk.z >= 0 && u0 + p.per_split < units ? u0 + p.per_split : units;
   const int uw = u1 < whole ? u1 : whole;
@@ -152,10 +153,10 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   }
   for (; u < u1; u += NW) {   // this wave's last units, the matrix's ragged one among them
     u32x4 a[2], b[NB][2];
-    int k[2];
+    uint32_t k[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      k[h] = u * UE + (h * 4 + g) * CE;
+      k[h] = (uint32_t)u * UE + (h * 4 + g) * CE;
 #pragma unroll
       for (int c = 0; c < NB; ++c) b[c][h] = chunk_load<TY, SHORT>(pb[c], k[h], p.K);
       a[h] = chunk_load<TY, SHORT>(pa, k[h], p.K);
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
       mma16x16<TY>(acc[c], a, __builtin_bit_cast(int4v, o));
     }
   };
-  const int units = (p.K + 31) / 32, whole = p.K / 32;
+  const int whole = p.K / 32, units = whole + (p.K % 32 != 0);
   const int u0 = wk.z < 0 ? 0 : wk.z * p.per_split;
   const int u1 = wk.z >= 0 && u0 + p.per_split < units ? u0 + p.per_split : units;
   const int uw = u1 < whole ? u1 : whole;
