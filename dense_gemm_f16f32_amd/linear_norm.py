@@ -4,8 +4,10 @@ torch tensors (see include/linear_norm.h for the formulas and contracts).
 Every step of the computation runs in the HIP kernels of liblinear_norm.so.  The functions here
 go through the compiled binding csrc/torch_binding.cpp, which checks the tensors, allocates
 results and workspace with torch on the stream the kernels run on, and calls the library.
-Errors found by the library raise `GemmError` with its code; what it cannot see (dtypes,
-devices, shapes) raises ValueError.  The functions keep no state and take no part in autograd
+With `stream` a call runs on that stream; the caller orders it after the work that makes its
+operands, and the work that uses its results after it, as with any torch stream.  Operands may be
+temporaries.  Errors found by the library raise `GemmError` with its code; what it cannot see
+(dtypes, devices, shapes) raises ValueError.  The functions keep no state and take no part in autograd
 (the *_backward functions are the gradients).
 """
 from __future__ import annotations
@@ -63,12 +65,20 @@ def native():
     return _native
 
 
-def _on(stream, t):
-    """Context of a call on `stream` instead of torch's current one."""
+def _on(stream, f, args, tensors):
+    """f(*args) on `stream` instead of torch's current one.  The tensors among args stay
+    untouched until `stream` has passed the call: torch gives memory that is freed before that
+    to no other work."""
     import torch
+    t = tensors[0]
     if t.is_cuda and stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the operands on {t.device}")
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        result = f(*args)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return result
 
 
 class RMSNormResult(NamedTuple):
@@ -94,8 +104,8 @@ def linear(a, b, bias=None, residual=None, *, activation="none", scale_a=None, s
     f = (_native or native()).linear
     if stream is None:
         return f(a, b, bias, residual, activation, scale_a, scale_b, out_dtype, with_pre, out)
-    with _on(stream, a):
-        return f(a, b, bias, residual, activation, scale_a, scale_b, out_dtype, with_pre, out)
+    args = (a, b, bias, residual, activation, scale_a, scale_b, out_dtype, with_pre, out)
+    return _on(stream, f, args, (a, b, bias, residual, scale_a, scale_b, out))
 
 
 def linear_backward(dc, a, b, pre=None, *, activation="none", bias_grad=False, a_grad=True,
@@ -109,8 +119,8 @@ def linear_backward(dc, a, b, pre=None, *, activation="none", bias_grad=False, a
     f = (_native or native()).linear_backward
     if stream is None:
         return f(dc, a, b, pre, activation, bias_grad, a_grad, b_grad)
-    with _on(stream, dc):
-        return f(dc, a, b, pre, activation, bias_grad, a_grad, b_grad)
+    return _on(stream, f, (dc, a, b, pre, activation, bias_grad, a_grad, b_grad),
+               (dc, a, b, pre))
 
 
 def rms_norm(x, weight, residual=None, *, eps=1e-5, out_dtype=None, with_rstd=False,
@@ -126,8 +136,8 @@ def rms_norm(x, weight, residual=None, *, eps=1e-5, out_dtype=None, with_rstd=Fa
     f = (_native or native()).rms_norm
     if stream is None:
         return f(x, weight, residual, eps, out_dtype, with_rstd, RMSNormResult)
-    with _on(stream, x):
-        return f(x, weight, residual, eps, out_dtype, with_rstd, RMSNormResult)
+    return _on(stream, f, (x, weight, residual, eps, out_dtype, with_rstd, RMSNormResult),
+               (x, weight, residual))
 
 
 def rms_norm_backward(dy, h, weight, rstd, *, dh=None, weight_grad=True, stream=None):
@@ -139,5 +149,4 @@ def rms_norm_backward(dy, h, weight, rstd, *, dh=None, weight_grad=True, stream=
     f = (_native or native()).rms_norm_backward
     if stream is None:
         return f(dy, h, weight, rstd, dh, weight_grad)
-    with _on(stream, dy):
-        return f(dy, h, weight, rstd, dh, weight_grad)
+    return _on(stream, f, (dy, h, weight, rstd, dh, weight_grad), (dy, h, weight, rstd, dh))
