@@ -5,6 +5,7 @@
 // Python, the checks and allocations of one call took 12-14 us, several times the kernel.
 // Positional arguments only (the Python functions give them in order); None stands for absent.
 #include <Python.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -21,13 +22,24 @@ using at::Tensor;
 
 const char* const kActivations[] = {"none", "relu", "gelu", "gelu_tanh", "silu"};
 
+// The results carry no history, so an operand whose gradient (or tangent) would be lost is refused.
+void untracked(const Tensor& t, const char* what) {
+  const c10::AutogradState& mode = c10::AutogradState::get_tls_state();
+  TORCH_CHECK_VALUE(!(mode.get_grad_mode() && t.requires_grad()) &&
+                        !(mode.get_fw_grad_mode() && t._fw_grad(0).defined()),
+                    what, " requires grad, and this function takes no part in autograd: call it "
+                    "under torch.no_grad(), or in a torch.autograd.Function with its backward");
+}
+
 struct Args {
   PyObject* const* v;
   // a tensor, or an undefined one for None
   Tensor tensor(int i, const char* what) const {
     if (v[i] == Py_None) return Tensor();
     TORCH_CHECK_TYPE(THPVariable_Check(v[i]), what, " must be a tensor");
-    return THPVariable_Unpack(v[i]);
+    const Tensor& t = THPVariable_Unpack(v[i]);
+    untracked(t, what);
+    return t;
   }
   Tensor needed(int i, const char* what) const {
     TORCH_CHECK_TYPE(v[i] != Py_None, what, " must be a tensor");

@@ -8,7 +8,8 @@ With `stream` a call runs on that stream; the caller orders it after the work th
 operands, and the work that uses its results after it, as with any torch stream.  Operands may be
 temporaries.  Errors found by the library raise `GemmError` with its code; what it cannot see
 (dtypes, devices, shapes) raises ValueError.  The functions keep no state and take no part in autograd
-(the *_backward functions are the gradients).
+(the *_backward functions are the gradients): an operand that requires grad is refused, outside
+torch.no_grad() and the forward and backward of a torch.autograd.Function.
 """
 from __future__ import annotations
 
