@@ -45,7 +45,11 @@ struct Args {
     TORCH_CHECK_TYPE(v[i] != Py_None, what, " must be a tensor");
     return tensor(i, what);
   }
-  bool flag(int i) const { return PyObject_IsTrue(v[i]) > 0; }
+  bool flag(int i) const {
+    const int f = PyObject_IsTrue(v[i]);
+    if (f < 0) throw python_error();
+    return f > 0;
+  }
   bool has_dtype(int i) const {
     if (v[i] == Py_None) return false;
     TORCH_CHECK_TYPE(THPDtype_Check(v[i]), "out_dtype must be a torch.dtype");
