@@ -72,7 +72,7 @@ def _on(stream, f, args, tensors):
     to no other work."""
     import torch
     t = tensors[0]
-    if t.is_cuda and stream.device != t.device:
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the operands on {t.device}")
     with torch.cuda.stream(stream):
         result = f(*args)
