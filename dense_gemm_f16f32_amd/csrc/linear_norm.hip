@@ -612,12 +612,14 @@ int linear_backward(const linear_backward_args* args) {
   BackwardPlan f;
   int rc = plan_backward(x, &f);
   if (rc != GEMM_F16F32_OK) return rc;
+  const bool act = x.activation != LINEAR_ACT_NONE;
   const int64_t need = f.dpre_bytes + f.part_bytes + f.w_bytes;
   rc = check_workspace(x.workspace, x.workspace_bytes, need);
   if (rc != GEMM_F16F32_OK) return rc;
   if (need > 0) {
     const Region w = {x.workspace, (uint64_t)need};
-    const Region o[] = {region(x.dc, x.m, x.n, x.dc_row, 2), region(x.pre, x.m, x.n, x.pre_row, 2),
+    const Region o[] = {region(x.dc, x.m, x.n, x.dc_row, 2),
+                        region(act ? x.pre : nullptr, x.m, x.n, x.pre_row, 2),
                         region(x.da, x.m, x.k, x.da_row, 2), region(x.dbias, 1, x.n, x.n, 2),
                         operand_region(f.a, x.k, x.m, x.type), operand_region(f.b, x.k, x.n, x.type),
                         f.db_cols ? region(x.db, x.n, x.k, x.db_col, 2)
@@ -627,7 +629,6 @@ int linear_backward(const linear_backward_args* args) {
   const bool bf = x.type == LINEAR_NORM_BF16;
   const hipStream_t s = (hipStream_t)x.stream;
   char* const ws = (char*)x.workspace;
-  const bool act = x.activation != LINEAR_ACT_NONE;
   const void* dpre = x.dc;
   const bool sums = x.dbias != nullptr && f.dact;
   const bool last = sums && f.row_blocks != 1;   // dbias has a second step
@@ -805,7 +806,7 @@ int rms_norm_backward(const rms_norm_backward_args* args) {
     const bool sums = backward_sums(x.rows, x.dim);
     p.part = x.dweight && sums ? (float*)x.workspace : nullptr;
     p.dweight = sums ? nullptr : (uint16_t*)x.dweight;
-      p.rows = (int32_t)x.rows;
+    p.rows = (int32_t)x.rows;
     p.dim = (int32_t)x.dim;
     p.inv_dim = (float)(1.0 / (double)x.dim);
     bf ? norm_backward<lk::kBF16>(p, groups, s) : norm_backward<lk::kF16>(p, groups, s);
