@@ -145,9 +145,10 @@ def kernels_with_private_arrays(so_path: str) -> list:
     return found
 
 
-def _compile(src: str, so: str, extra=()) -> int:
-    """Compiles one library, checks it and moves it in place; returns the number of its kernels
-    whose asm-MFMA wait states were checked."""
+def _compile(src: str, so: str, extra=(), check=None) -> int:
+    """Compiles one library, checks it (with `check`, which raises, as well) and moves it in place;
+    returns the number of its kernels whose asm-MFMA wait states were checked.  A library that
+    fails leaves the one in place alone."""
     tmp = so + ".tmp"
     cmd = [HIPCC, *FLAGS, *extra, "-I", os.path.join(ROOT, "include"),
            "-I", os.path.join(PKG, "csrc"), src, "-o", tmp]
@@ -158,27 +159,35 @@ def _compile(src: str, so: str, extra=()) -> int:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if msgs:
         print("\n".join(msgs))
-    # Every kernel must have its host launch stub; an undefined one means the host pass
-    # dropped a kernel and the library would fail to load.
-    nm = subprocess.run(["nm", "-D", "--undefined-only", tmp], capture_output=True, text=True)
-    missing = [ln.split()[-1] for ln in nm.stdout.splitlines() if "__device_stub__" in ln]
-    if nm.returncode != 0 or missing:
+    try:
+        # Every kernel must have its host launch stub; an undefined one means the host pass
+        # dropped a kernel and the library would fail to load.
+        nm = subprocess.run(["nm", "-D", "--undefined-only", tmp], capture_output=True, text=True)
+        missing = [ln.split()[-1] for ln in nm.stdout.splitlines() if "__device_stub__" in ln]
+        if nm.returncode != 0 or missing:
+            raise RuntimeError("undefined kernel stubs in the built library: "
+                               + ", ".join(missing))
+        n = check_mfma_waits(tmp)
+        if n == 0:
+            raise RuntimeError("no asm-MFMA kernel found to check in the built library")
+        if check is not None:
+            check(tmp)
+    except BaseException:
         os.remove(tmp)
-        raise RuntimeError("undefined kernel stubs in the built library: " + ", ".join(missing))
-    n = check_mfma_waits(tmp)
-    if n == 0:
-        os.remove(tmp)
-        raise RuntimeError("no asm-MFMA kernel found to check in the built library")
+        raise
     os.replace(tmp, so)
     return n
 
 
-def build_linear_norm(extra=()) -> str:
-    """Compiles the linear layer and the norm (liblinear_norm.so)."""
-    _compile(LN_SRC, LN_SO, extra)
-    found = kernels_with_private_arrays(LN_SO)
+def _refuse_private_arrays(so_path: str) -> None:
+    found = kernels_with_private_arrays(so_path)
     if found:
         raise RuntimeError("kernels with arrays in memory: " + ", ".join(found))
+
+
+def build_linear_norm(extra=()) -> str:
+    """Compiles the linear layer and the norm (liblinear_norm.so)."""
+    _compile(LN_SRC, LN_SO, extra, _refuse_private_arrays)
     return LN_SO
 
 
