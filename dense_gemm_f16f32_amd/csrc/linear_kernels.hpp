@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(256) lin_pair(PairArgs p) {
 // ---------------------------------------------------------------------------------------
 // A small backward pass in one launch: both products on 64 x 64 tiles, with dpre = dc act'(pre)
 // made on the way into LDS by every workgroup that needs it (a few times over, which costs less
-// than a pass of its own and its launch), and its column sums by the workgroups of db's first
+// than a pass of its own and its launch) and rounded there to the operands' type (see lin_dact), and its column sums by the workgroups of db's first
 // tiles along k.  Panels go through registers, three ahead, and two LDS stages.
 // ---------------------------------------------------------------------------------------
 struct SmallArgs {

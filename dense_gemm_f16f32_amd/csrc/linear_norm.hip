@@ -141,9 +141,12 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     g->path = b.km ? lk::kPathSkinnyK : lk::kPathSkinnyN;
     const int64_t depth = b.km ? panels : cdiv(K, 32);
     // b k-contiguous: a is read once per workgroup, so with many rows the workgroups take more
-    // columns, as long as the CUs have one each, if need be in two slices of k (e4m3, 16 x 16384
-    // x 4096: 16 columns 19.5 us, 64 columns 14.1; 16 x 8192 x 8192: 18.8, and 16.4 in two
-    // slices; one row, bf16, 16384 x 4096: 24.1 and 25.0).
+    // columns, as long as the CUs have one each, if need be in two slices of k.  In us, with the
+    // weights partly in the last-level cache / with other weights in between: e4m3, 16 x 16384 x
+    // 4096: 16 columns 19.5 / 22.3, 64 columns 14.1 / 17.7; 16 x 8192 x 8192: 16 columns 18.8 /
+    // 21.5, 64 in two slices 16.4 / 20.3 (32 columns in one piece, which this rule does not
+    // take, 18.2 / 18.7); one row, bf16, 16384 x 4096: 16 columns 24.1 / 28.1, 64 columns 25.0 /
+    // 29.7.
     const int64_t wide = cdiv(N, 64);
     g->cols = 64;
     if (b.km && (M <= 8 || K < 16 || (wide < kCUs && (2 * wide < kCUs || depth < 64))))
@@ -450,8 +453,10 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     f->pair = fits && P <= 4 * kCUs && one < two;
     // The element-wise pass as well while a tile's panels are few: its loads go through
     // registers, three panels ahead, and a panel costs about 1.2 us instead of 0.3, for a launch
-    // less (3 us of host time; f16, silu: 64^3 4.6 us against 8.2 in two launches, 128^3 5.8 and
-    // 7.6, 256^3 8.1 and 7.5, 300^3 11.8 and 9.6).
+    // less (f16, silu: 64^3 4.6 us against 8.2 in two launches, 128^3 5.8 and 7.6, 256^3 8.1 and
+    // 7.5, 4 x 200 x 300 8.9 and 7.9, 64 x 256 x 3000 8.2 and 7.9, 300^3, past the rule, 11.8 and
+    // 9.6).  At four panels only the launch's 3 us of host time speak for it, which a captured
+    // graph does not pay.
     f->small = f->pair && deep <= 4 && x.n >= 8 && x.k >= 8;
     if (f->pair) {
       GemmPlan t = {};

@@ -107,7 +107,8 @@ __device__ __forceinline__ void store_e4m3x8(uint8_t* p, const float (&v)[8], Di
 }
 
 // One pass: the sum of squares, the 8-bit scale and y come from the row in registers.  HBM bounds
-// it: 8192 x 8192 bf16 with residual to e4m3 88 us (5.3 TB/s), 4095 x 4093 f16 25 us (5.4 TB/s).
+// it: 8192 x 8192 bf16 with residual to e4m3 88 us (5.3 TB/s), 4095 x 4093 f16 29 us (4.6 TB/s; 24.5
+// where the rows are partly in the last-level cache).
 // One row a workgroup of 64 NW threads, 8 columns a thread at a time.  C > 0: rows of at most
 // 512 NW C columns, held in registers.  C == 0: longer rows, read again for each step that
 // needs them.
@@ -257,8 +258,8 @@ __device__ __forceinline__ void store_partial8(float* part, int groups, int grou
 // (b + grid) RW .., ...; where registers allow, the next row's values are loaded before the
 // current row is worked on.  Each thread keeps its columns' dweight sums in registers; the
 // workgroup adds and writes them once.  Short rows (one wave each) go four to a workgroup.  HBM
-// bounds it: 8192 x 4096 bf16 41 us (6.7 TB/s of dy, h, dh and dx), and 5 for sum_partials; without
-// the loads ahead 70 us.
+// bounds it: 8192 x 4096 bf16 50 us (5.4 TB/s of dy, h, dh and dx), and 5 for sum_partials; with the
+// rows partly in the last-level cache 41 us, and there without the loads ahead 70.
 template <int TY, int NW, int C, int RW>
 __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
   static_assert(NW == 1 || RW == 1, "rows of several waves share the workgroup's barrier");
@@ -430,7 +431,14 @@ struct DactArgs {
 };
 
 // dpre = dc act'(pre) and its column sums over a block of rows: 512 columns a workgroup, 4 rows
-// at a time.  HBM bounds it: 4096 x 4096 bf16 21.4 us (4.7 TB/s).
+// at a time.  HBM bounds it: 4096 x 4096 bf16 with gelu_tanh 27 us (3.7 TB/s), 24.5 where dc and pre
+// are partly in the last-level cache.
+//
+// dpre is rounded to the operands' type, once: the matrix instructions take both operands in one
+// 16-bit type.  In fp32 it would have to go through the products as two 16-bit halves, which
+// doubles their work (at 4096^3 from 216 us to 432) to take a gradient's error, relative in the
+// norm, from 0.0023 to the 0.0017 of its own rounding in bf16 (f16: from 0.00029 to 0.00021).  The
+// column sums take the unrounded values.
 template <int TY>
 __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
   __shared__ float s[3][512];

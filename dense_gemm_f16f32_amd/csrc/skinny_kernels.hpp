@@ -91,8 +91,10 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
 // b stored k-contiguous (column-major): 16 NB columns a workgroup.  One unit is 128 bytes of
 // every row: lane l takes the 16-byte chunks l / 16 and 4 + l / 16 of row l % 16, of a and of b
 // alike, so the order of k inside the unit is the same for both.  The loads of U units are in
-// flight at once.  HBM bounds it: 1 x 16384 x 4096 bf16 24.2 us (5.5 TB/s), 16 x 16384 x 4096 23.7
-// us (5.7 TB/s), 16 x 8192 x 8192 e4m3 13.1 us (5.2 TB/s) and 3.5 for its two slices' join.
+// flight at once.  HBM bounds it.  With other weights in between (2 GiB of them in turn): 1 x 16384
+// x 4096 bf16 26.9 us (5.0 TB/s), 16 x 16384 x 4096 30.1 us (4.5 TB/s), 16 x 8192 x 8192 e4m3 17.0
+// us (3.9 TB/s) and 4.3 for its two slices' join.  The same weights again and again stay partly in
+// the last-level cache: 24.7, 23.4 and 13.7 us.
 template <int TY, int NB, int NW, bool SHORT>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   constexpr int UE = TY == kE4M3 ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk
@@ -143,8 +145,8 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
         a[i][h] = load16(pa + k);
       }
     // Every load is on its way before the first is used.  With one block of 16-bit columns the
-    // waves are many and small, and do without (16 rows of e4m3, 8192 x 8192: 18.9 -> 16.7 us; one
-    // of bf16, 16384 x 4096: 23.1 without, 24.0 with).
+    // waves are many and small, and do without (weights partly in the last-level cache: 16 rows of
+    // e4m3, 8192 x 8192: 18.9 -> 16.7 us; one of bf16, 16384 x 4096: 23.1 without, 24.0 with).
     if constexpr (NB > 1 || TY == kE4M3) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < U; ++i)
@@ -179,7 +181,9 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
 // columns, from CP (l % 16) on, of the 8 k rows 8 (l / 16) .. + 7 of a 32-deep unit; pairs of
 // rows are interleaved by byte permutes into k-runs, one MFMA operand per column.  64 columns a
 // workgroup: a wave's load covers 128 bytes of four k rows.  HBM bounds it: 1 x 16384 x 4096 bf16
-// 22.3 us (6.0 TB/s, the weights partly in the last cache).
+// 25.7 us (5.2 TB/s) with other weights in between, 21.5 with these partly in the last-level cache.
+// Rows of b at any 2-byte address: a k row's 128 bytes touch two lines, 1 x 8191 x 8191 38.8 us
+// (3.5 TB/s) either way.
 template <int TY, int CP, int NW>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
   constexpr int NC = 16 * CP;

@@ -15,7 +15,12 @@
  *
  * Sums, statistics and gradients are held in fp32; every output is rounded once (to nearest,
  * ties to even), with one exception: dpre is rounded to the operands' type before it enters
- * the matrix products (their operands are 16 bits wide).  dbias sums the unrounded values.
+ * the matrix products (their operands are 16 bits wide; beyond f16's range it is infinite).
+ * dbias sums the unrounded values.
+ *
+ * Activations, their lower tails included, and the terms of their slopes are off by a few 2^-23 of
+ * their own values around 0, and by up to 2^-15 where exp leaves fp32's range.
+ * The norm's squares may leave fp32's range; rstd may not.
  *
  * 8-bit operands: with up to 16 rows (m) or k up to 512 the values are multiplied as f16,
  * exactly.  Beyond, they go through the 8-bit matrix instruction, which rounds inside: measured
