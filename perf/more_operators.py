@@ -133,7 +133,8 @@ def _pack(v, lowest):
     """(integers, scales) of v in 32 bits: the largest of each 32 neighbours lies in [64, 128)
     scales, and at most 127 are stored."""
     b = _blocks(v)
-    e = (torch.frexp(b.abs().amax(2)).exponent - 7).clamp(min=lowest)
+    top = b.abs().amax(2)
+    e = torch.where(top > 0, torch.frexp(top).exponent - 7, lowest).clamp(min=lowest)
     scale = torch.ldexp(torch.ones_like(b[:, :, 0]), e)
     q = torch.round(b / scale[:, :, None]).clamp(-127, 127)
     return q.view(v.shape[0], -1)[:, :v.shape[1]], scale
