@@ -288,7 +288,9 @@ def _plain(s):
         a = s["a"].float()
         if s["quantize"]:
             amax = a.abs().amax(1)
-            scale_a = torch.where(amax > 0, amax / 127, torch.ones_like(amax))
+            # (torch divides by a number with its rounded reciprocal)
+            scale_a = torch.where(amax > 0, amax / torch.full_like(amax, 127),
+                                  torch.ones_like(amax))
             a = torch.round(a / scale_a[:, None])
         else:
             scale_a = s["scale_a"]
@@ -385,7 +387,8 @@ def exact(case, seed):
         a = d["a"]
         if case["quantize"]:   # the scale is a 32-bit number, and the integers go by it
             top = torch.linalg.vector_norm(s["a"].float(), ord=math.inf, dim=1)
-            unit = torch.where(top == 0, torch.ones_like(top), top / 127).to(torch.float64)
+            unit = torch.where(top == 0, torch.ones_like(top), (top.to(torch.float64) / 127).float())
+            unit = unit.to(torch.float64)
             a = torch.round(a / unit.unsqueeze(1)) * unit.unsqueeze(1)
         else:
             a = a * d["scale_a"].unsqueeze(1)
