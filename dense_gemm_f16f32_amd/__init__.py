@@ -8,8 +8,9 @@ passes their device pointers, element strides (row- or column-major, any leading
 and torch's current HIP stream, and for split K a workspace tensor.  PyTorch is used for
 device memory and streams only.
 
-linear, linear_backward, rms_norm and rms_norm_backward (linear_norm.py) are the operators of a
-transformer block around the product, in a library of their own.
+linear, linear_backward, rms_norm, layer_norm, their backward passes, quantize_rows, pack8 and unpack8
+(linear_norm.py) are the operators of a transformer block around the product, in a library of their
+own.
 
 The library is loaded on first use; if it has not been built the call raises at once
 (there is no fallback of any kind).
@@ -281,5 +282,7 @@ def tile_map(num_pid_m, num_pid_n, group_m, xcd_remap, stream=None):
     return out
 
 
-from .linear_norm import (ACTIVATIONS, RMSNormResult, linear, linear_backward,  # noqa: E402,F401
-                          rms_norm, rms_norm_backward)
+from .linear_norm import (ACTIVATIONS, LayerNormResult, Packed8, QuantizedRows,  # noqa: E402,F401
+                          RMSNormResult, layer_norm, layer_norm_backward, linear,
+                          linear_backward, pack8, quantize_rows, rms_norm, rms_norm_backward,
+                          unpack8)

@@ -65,8 +65,12 @@ ASM_MFMA_KERNELS = ("mfma_ceiling",                         # the rate probe (bo
                     "gemm_genericILi256ELi256ELb")          # gemm_generic, 256 x 256 tiles
 
 
-def _asm_mfma_kernel(name: str) -> bool:
-    return any(k in name for k in ASM_MFMA_KERNELS) and (
+# The linear layer's 256 x 256 tile on int8 operands.
+ASM_INT_MFMA_KERNELS = ("lin_i8_ring",)
+
+
+def _asm_mfma_kernel(name: str, kernels=ASM_MFMA_KERNELS) -> bool:
+    return any(k in name for k in kernels) and (
         "gemm_generic" not in name or "ELi2ELi2ELb" in name)
 
 
@@ -86,7 +90,7 @@ def disassemble(so_path: str, *options: str) -> str:
                               check=True, capture_output=True, text=True).stdout
 
 
-def scan_mfma_waits(asm: str):
+def scan_mfma_waits(asm: str, kernels=ASM_MFMA_KERNELS):
     """Scans the asm-MFMA kernels of a disassembly, in program order: after an MFMA that
     writes accumulator registers, no v_accvgpr_read/mov may come before the drain (four
     `s_nop 7`, 32 wait states); after a v_accvgpr_write/mov, no MFMA may come before an
@@ -95,7 +99,7 @@ def scan_mfma_waits(asm: str):
     checked, bad = 0, []
     for block in re.split(r"\n(?=[0-9a-f]+ <)", asm):
         m = re.match(r"[0-9a-f]+ <([^>]+)>:", block)
-        if not m or not _asm_mfma_kernel(m.group(1)):
+        if not m or not _asm_mfma_kernel(m.group(1), kernels):
             continue
         checked += 1
         mfma_pending = write_pending = False
@@ -122,10 +126,10 @@ def scan_mfma_waits(asm: str):
     return checked, bad
 
 
-def check_mfma_waits(so_path: str) -> int:
+def check_mfma_waits(so_path: str, kernels=ASM_MFMA_KERNELS) -> int:
     """scan_mfma_waits on a built library; raises on a violation (which would mean the compiler
     moved accumulators around the asm MFMAs) and returns the number of kernels checked."""
-    checked, bad = scan_mfma_waits(disassemble(so_path))
+    checked, bad = scan_mfma_waits(disassemble(so_path), kernels)
     if bad:
         raise RuntimeError("asm MFMA wait states not met:\n" + "\n".join(bad[:20]))
     return checked
@@ -185,9 +189,15 @@ def _refuse_private_arrays(so_path: str) -> None:
         raise RuntimeError("kernels with arrays in memory: " + ", ".join(found))
 
 
+def _check_linear_norm(so_path: str) -> None:
+    _refuse_private_arrays(so_path)
+    if check_mfma_waits(so_path, ASM_INT_MFMA_KERNELS) != 1:
+        raise RuntimeError("the int8 tile's asm-MFMA kernel was not found to check")
+
+
 def build_linear_norm(extra=()) -> str:
-    """Compiles the linear layer and the norm (liblinear_norm.so)."""
-    _compile(LN_SRC, LN_SO, extra, _refuse_private_arrays)
+    """Compiles the linear layer and the norms (liblinear_norm.so)."""
+    _compile(LN_SRC, LN_SO, extra, _check_linear_norm)
     return LN_SO
 
 

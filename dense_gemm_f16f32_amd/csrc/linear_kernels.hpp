@@ -1,14 +1,17 @@
-// Device code of the linear layer on gfx950: tiled matrix products on 16-bit or e4m3 operands
+// Device code of the linear layer on gfx950: tiled matrix products on 16-bit, e4m3 or int8 operands
 // with the layer's epilogue, out = act(a b scale + bias) + residual.
 //
 // The operand side (panels in LDS, swizzles, buffer->LDS loads, transposing reads, the program
 // map) is the fp16 product's, from gemm_kernels.hpp; it moves 16-byte chunks and does not look
 // inside them.  What differs here:
-//  * the element type: fp16, bf16 or e4m3.  Two e4m3 values ride in each 16-bit slot, so an
-//    e4m3 operand of K values is a k-major matrix of K/2 slots, and one 64-byte piece of a row
-//    feeds v_mfma_f32_32x32x64_f8f6f4, twice the work of the 16-bit instruction on the same
+//  * the element type: fp16, bf16, e4m3 or int8.  Two 8-bit values ride in each 16-bit slot, so an
+//    8-bit operand of K values is a k-major matrix of K/2 slots, and one 64-byte piece of an e4m3
+//    row feeds v_mfma_f32_32x32x64_f8f6f4, twice the work of the 16-bit instruction on the same
 //    bytes (the unscaled form: scales are applied to the sum, in the epilogue).  Its inner sums
-//    are rounded to fewer bits than fp32 (see kHalvesK).
+//    are rounded to fewer bits than fp32 (see kHalvesK).  The int8 instructions
+//    (v_mfma_i32_16x16x64_i8, 32x32x32) take and leave their registers as the 16-bit ones do; the
+//    accumulators hold 32-bit integers, exact up to K = 131071 (2^31 / 128^2), which travel as the
+//    bits of floats to the epilogue and are converted there.
 //  * the ragged panel: when the panel depth does not divide K, the panel that holds the last
 //    K mod BK values is multiplied first, so that every other panel starts at a multiple of BK
 //    and keeps the alignment of its rows.
@@ -37,13 +40,17 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float2v __attribute__((ext_vector_type(2)));
 typedef int int8v __attribute__((ext_vector_type(8)));
+typedef int int16v __attribute__((ext_vector_type(16)));
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));   // 16 bytes at any 16-bit element
 
 constexpr int kF16 = LINEAR_NORM_F16, kBF16 = LINEAR_NORM_BF16, kE4M3 = LINEAR_NORM_E4M3;
+constexpr int kI8 = LINEAR_NORM_I8;
+template <int TY>
+constexpr bool kBytes = TY == kE4M3 || TY == kI8;   // 8-bit operands
 
 struct LinArgs {
-  const uint16_t* A;      // 16-bit slots: elements, or pairs of e4m3 values
+  const uint16_t* A;      // 16-bit slots: elements, or pairs of 8-bit values
   const uint16_t* B;
   int64_t lda, ldb;       // slots
   int32_t M, N, K;        // K in elements
@@ -57,6 +64,10 @@ struct LinArgs {
   const float* scale_b;
   int64_t ldo, ldp, ldr;
   int32_t act, out_type;
+  // the value before the activation in 8 bits (see pack_block8), or null; not with `pre`
+  uint8_t* pre8;
+  uint8_t* pre8_scale;
+  int64_t ldp8, ldps;
   // Split K: the tiles from `first_split` on (all, some or none) are computed in `splits` slices
   // of k, `per_split` panels each, the last one the rest.  Slice z of the i-th of them leaves
   // its sums in W, a BM x BN block at (i splits + z) BM BN; lin_reduce adds the slices.
@@ -158,6 +169,107 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8], int n, 
     }
     if (n & 1) *p = (uint16_t)v[0];
   }
+}
+
+// ---- checkpoints in 8 bits ---------------------------------------------------------------
+// 32 neighbouring values of a row share a scale, a power of two 2^(b - 127) held as the byte b: the
+// largest magnitude lies in [64, 128) scales.  Values are integers, rounded to nearest (ties to
+// even) and at most 127.  Not below 2^-24 (f16) or 2^-120 (bf16), a scale times an integer is a
+// value of its 16-bit type, so what is restored enters the matrix instructions unrounded; with the
+// largest magnitude divided by 127 instead (a step of up to half the size) it would be rounded
+// again there.  A block that holds an infinity or a NaN has scale NaN (b = 255), and so do all its
+// values.
+__device__ __forceinline__ int lowest_scale(int type) { return type == kF16 ? 127 - 24 : 127 - 120; }
+
+// Largest of the 4 lanes of a quad, all of which are active.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);   // 1 0 3 2
+  v = v > o ? v : o;
+  o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);            // 2 3 0 1
+  return v > o ? v : o;
+}
+struct Block8 {
+  uint32_t lo, hi;   // 8 integers
+  uint32_t scale;    // the block's byte
+};
+// 8 values of a block, whose others the quad's other lanes hold (0 where there are none).
+__device__ __forceinline__ Block8 pack_block8(const float (&v)[8], int type) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu;
+    m = m > b ? m : b;
+  }
+  const int exponent = (int)(quad_max(m) >> 23), low = lowest_scale(type);
+  const int b = exponent - 6 < low ? low : exponent - 6;
+  const float inv = __builtin_bit_cast(float, (uint32_t)(254 - b) << 23);   // 2^(127 - b)
+  uint32_t q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)   // the addition rounds, and leaves the integer in the low bits
+    q[e] = __builtin_bit_cast(
+        uint32_t, __builtin_amdgcn_fmed3f(v[e] * inv, -127.f, 127.f) + 12582912.f);
+  auto bytes = [&](int i) __attribute__((always_inline)) {
+    const uint32_t x = __builtin_amdgcn_perm(q[i + 1], q[i], 0x0C0C0400u);
+    const uint32_t y = __builtin_amdgcn_perm(q[i + 3], q[i + 2], 0x0C0C0400u);
+    return x | (y << 16);
+  };
+  if (exponent == 255) return {0u, 0u, 255u};
+  return {bytes(0), bytes(4), (uint32_t)b};
+}
+// 8 values back, exact: bytes as (128 + q) - 128, times the scale.
+__device__ __forceinline__ void unpack_block8(float (&v)[8], uint32_t lo, uint32_t hi,
+                                              uint32_t b) {
+  // byte 0 is 2^-127, below the normal numbers, and 255 NaN
+  const float scale = b == 255u ? __builtin_nanf("")
+                                : __builtin_bit_cast(float, b == 0u ? 0x400000u : b << 23);
+  const uint32_t w[2] = {lo ^ 0x80808080u, hi ^ 0x80808080u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = ((float)((w[e / 4] >> (8 * (e & 3))) & 0xFFu) - 128.f) * scale;
+}
+struct __attribute__((packed)) Bytes8 {
+  uint32_t x, y;
+};
+struct __attribute__((packed)) Bytes4 {
+  uint32_t x;
+};
+struct __attribute__((packed)) Bytes2 {
+  uint16_t x;
+};
+// 8 bytes to p, of which the first n > 0 exist, in pieces of 8, 4, 2 and 1.
+__device__ __forceinline__ void store_bytes8(uint8_t* p, uint32_t lo, uint32_t hi, int n) {
+  if (n >= 8) {
+    *(Bytes8*)p = Bytes8{lo, hi};
+    return;
+  }
+  if (n & 4) {
+    *(Bytes4*)p = Bytes4{lo};
+    p += 4;
+    lo = hi;
+  }
+  if (n & 2) {
+    *(Bytes2*)p = Bytes2{(uint16_t)lo};
+    p += 2;
+    lo >>= 16;
+  }
+  if (n & 1) *p = (uint8_t)lo;
+}
+// 8 bytes from p, of which the first n exist (n >= 8: all, n <= 0: none); the others are 0 and not
+// read.  p is n bytes before its row's end; `back`: the row has 8 bytes at least (see raw8_load).
+__device__ __forceinline__ uint2 load_bytes8(const uint8_t* p, int n, bool back) {
+  uint2 v = {0u, 0u};
+  if (back) {
+    const Bytes8 q = *(const Bytes8*)(p - (n >= 8 ? 0 : 8 - n));
+    uint64_t w = (uint64_t)q.x | ((uint64_t)q.y << 32);
+    w = n >= 8 ? w : n <= 0 ? 0u : w >> (8 * (8 - n));
+    v.x = (uint32_t)w;
+    v.y = (uint32_t)(w >> 32);
+    return v;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < n) (e < 4 ? v.x : v.y) |= (uint32_t)p[e] << (8 * (e & 3));
+  return v;
 }
 
 // ---- activations -------------------------------------------------------------------------
@@ -270,7 +382,7 @@ struct Columns {
 };
 template <int TY>
 __device__ __forceinline__ Columns load_columns(const LinArgs& p, int col) {
-  const int ot = TY == kE4M3 ? p.out_type : TY;
+  const int ot = kBytes<TY> ? p.out_type : TY;
   Columns c;
   c.n = p.N - col;
 #pragma unroll
@@ -280,7 +392,7 @@ __device__ __forceinline__ Columns load_columns(const LinArgs& p, int col) {
   }
   if (c.n > 0) {
     if (p.bias) load8(c.bias, p.bias + col, c.n, ot, p.N >= 8);
-    if (TY == kE4M3 && p.scale_b) {
+    if (kBytes<TY> && p.scale_b) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (e < c.n) c.sb[e] = p.scale_b[col + e];
@@ -288,11 +400,41 @@ __device__ __forceinline__ Columns load_columns(const LinArgs& p, int col) {
   }
   return c;
 }
+// A sum as the matrix instructions leave it.
+template <int TY>
+__device__ __forceinline__ float sum_value(float v) {
+  return TY == kI8 ? (float)__builtin_bit_cast(int, v) : v;
+}
+// Partial sums added.
+template <int TY>
+__device__ __forceinline__ float sum_add(float v, float w) {
+  if constexpr (TY == kI8)
+    return __builtin_bit_cast(float, __builtin_bit_cast(int, v) + __builtin_bit_cast(int, w));
+  else
+    return v + w;
+}
+// Whether a lane takes part in what finish8 does: columns that do not exist still belong to a
+// block of the checkpoint.
+__device__ __forceinline__ bool takes_part(const LinArgs& p, int row, int col) {
+  return row < p.M && (col < p.N || p.pre8 != nullptr);
+}
+__device__ __forceinline__ void put_pre8(const LinArgs& p, int64_t row, int col, const float (&v)[8],
+                                         int n, int ot) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = e < n ? v[e] : 0.f;
+  const Block8 b = pack_block8(x, ot);
+  if (n <= 0) return;
+  store_bytes8(p.pre8 + row * p.ldp8 + col, b.lo, b.hi, n);
+  if ((col & 31) == 0) p.pre8_scale[row * p.ldps + (col >> 5)] = (uint8_t)b.scale;
+}
 template <int TY>
 __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, float (&v)[8],
                                         const Columns& c) {
-  const int ot = TY == kE4M3 ? p.out_type : TY;
-  if (TY == kE4M3) {
+  const int ot = kBytes<TY> ? p.out_type : TY;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = sum_value<TY>(v[e]);
+  if (kBytes<TY>) {
     // one scale after the other: their product can leave fp32's range where the result does not
     const float sa = p.scale_a ? p.scale_a[row] : 1.f;
 #pragma unroll
@@ -302,6 +444,10 @@ __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, floa
     for (int e = 0; e < 8; ++e) v[e] += c.bias[e];
   }
   if (p.pre) store8(p.pre + (int64_t)row * p.ldp + col, v, c.n, ot);
+  if (p.pre8) {
+    put_pre8(p, row, col, v, c.n, ot);
+    if (c.n <= 0) return;
+  }
   act_n(v, p.act);
   if (p.res) {
     float r[8];
@@ -330,7 +476,8 @@ struct Tile {
   static constexpr int A_BYTES = OA::BYTES, STAGE = OA::BYTES + OB::BYTES;
   using Acc = std::conditional_t<XB == 16, float4v, float16v>;
   using Frag = std::conditional_t<TY == kE4M3, int8v, int4v>;
-  static_assert(TY != kE4M3 || (AKM && BKM && XB == 32), "e4m3 operands are k-major");
+  static_assert(!kBytes<TY> || (AKM && BKM), "8-bit operands are k-major");
+  static_assert(TY != kE4M3 || XB == 32, "MFMA block of e4m3 operands");
 };
 
 template <class T, class O>
@@ -372,6 +519,10 @@ __device__ __forceinline__ void mma(typename T::Acc& acc, const typename T::Frag
   else if constexpr (T::TY == kBF16)
     acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
                                                   __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
+  else if constexpr (T::TY == kI8)
+    acc = __builtin_bit_cast(
+        float16v, __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, __builtin_bit_cast(int16v, acc), 0,
+                                                        0, 0));
   else if constexpr (T::HALVES)
 #pragma unroll
     for (int d = 0; d < 8; d += 2)
@@ -392,6 +543,8 @@ __device__ __forceinline__ void mma_inplace(typename T::Acc& acc, const typename
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
   else if constexpr (T::TY == kBF16)
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+  else if constexpr (T::TY == kI8)
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
   else
     asm volatile("v_mfma_f32_32x32x64_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 #else
@@ -456,7 +609,7 @@ struct Loader {
       u32x4 v = gk::load_chunk<true>(r, off[i] + lead);
       if constexpr (!O::KM) {
         if (row >= rem) v = u32x4{0u, 0u, 0u, 0u};
-      } else if constexpr (TY == kE4M3) {
+      } else if constexpr (kBytes<TY>) {
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           const int have = rem - (c * 16 + 4 * d);   // bytes of this dword that exist
@@ -493,7 +646,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
   const int col = n0 + wn * T::WTN + cc;
   const int row0 = m0 + wm * T::WTM + rr;
   const bool whole = T::BM <= p.M - m0 && T::BN <= p.N - n0;
-  const int ot = T::TY == kE4M3 ? p.out_type : T::TY;
+  const int ot = kBytes<T::TY> ? p.out_type : T::TY;
   const Columns c = load_columns<T::TY>(p, col);
   const float GK_LDS* const sr = s + rr * S::LDW + cc;
 #pragma unroll
@@ -528,7 +681,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
         const int row = row_t + i * S::ROWS;
         const float4v lo = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW);
         const float4v hi = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW + 4);
-        if (row < p.M && col < p.N) {
+        if (takes_part(p, row, col)) {
           float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
           finish8<T::TY>(p, row, col, f, c);
         }
@@ -544,14 +697,14 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
       const int64_t row = row_t + i * S::ROWS;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (T::TY == kE4M3) sa[u] = p.scale_a ? p.scale_a[row + u * S::ROWS] : 1.f;
+        if (kBytes<T::TY>) sa[u] = p.scale_a ? p.scale_a[row + u * S::ROWS] : 1.f;
         if (p.res) res[u] = *(const u32x4_any*)(p.res + (row + u * S::ROWS) * p.ldr + col);
         const float GK_LDS* const q = sr + (i + u) * S::ROWS * S::LDW;
         const float4v lo = *(const float4v GK_LDS*)q, hi = *(const float4v GK_LDS*)(q + 4);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = e < 4 ? lo[e & 3] : hi[e & 3];
-          f[u * 8 + e] = T::TY == kE4M3 ? v * sa[u] * c.sb[e] + c.bias[e] : v + c.bias[e];
+          const float v = sum_value<T::TY>(e < 4 ? lo[e & 3] : hi[e & 3]);
+          f[u * 8 + e] = kBytes<T::TY> ? v * sa[u] * c.sb[e] + c.bias[e] : v + c.bias[e];
         }
       }
       auto put = [&](uint16_t* base, int64_t ld) __attribute__((always_inline)) {
@@ -564,6 +717,15 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
         }
       };
       if (p.pre) put(p.pre, p.ldp);
+      if (p.pre8) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = f[u * 8 + e];
+          put_pre8(p, row + u * S::ROWS, col, v, 8, ot);
+        }
+      }
       act_n(f, p.act);
       if (p.res) {
 #pragma unroll
@@ -587,7 +749,7 @@ struct Panels {
 };
 template <int TY, int BK>
 __device__ __forceinline__ Panels panels_of(int K) {
-  constexpr int E = TY == kE4M3 ? 2 : 1;   // elements per slot
+  constexpr int E = kBytes<TY> ? 2 : 1;   // elements per slot
   Panels q;
   q.k2 = K / E + K % E;   // E is 1 or 2; K + 1 need not fit
   q.rem = K % (BK * E);
@@ -639,7 +801,7 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, co
   // check can cut them off (see last_element_slot): their owners write them again.
   uint16_t va = 0, vb = 0;
   int pa = -1, pb = -1;
-  if (T::TY != kE4M3 && q.rem == 0 && s1 == q.np) {
+  if (!kBytes<T::TY> && q.rem == 0 && s1 == q.np) {
     pa = gk::last_element_slot<OA>(m0, p.M, p.K, p.A, la.ext, tid, va);
     pb = gk::last_element_slot<OB>(n0, p.N, p.K, p.B, lb.ext, tid, vb);
   }
@@ -973,7 +1135,7 @@ __global__ void __launch_bounds__(256) lin_small_bwd(SmallArgs p) {
 // The 256 x 256 tile (64 slots deep, 4 waves of 128 x 128): the panels in five 32 KiB LDS slots,
 // B's in a ring of three and A's in a ring of two, two k steps per panel, each scheduled by
 // hand -- see ring_tile in gemm_kernels.hpp, whose order of loads, reads and barriers this is.
-// 16-bit types: 64 MFMAs of 16x16x32 a step; e4m3: 16 of 32x32x64, the same cycles.  Bound by the
+// 16-bit types: 64 MFMAs of 16x16x32 a step (int8: of 16x16x64); e4m3: 16 of 32x32x64, the same cycles.  Bound by the
 // matrix cores at the chip's power limit: 8192^3 bf16 with bias, gelu and pre-activation 764 - 809
 // us (1.36 - 1.44 PFLOP/s, MFMA busy 72 %), e4m3 with bias and silu 398 - 423 us (2.6 - 2.76), no
 // LDS bank conflicts.
@@ -1003,7 +1165,7 @@ __device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, cons
   lb.init(p.B, p.ldb, p.N, q.k2, n0, w, lane);
   uint16_t va = 0, vb = 0;
   int pa = -1, pb = -1;
-  if (TY != kE4M3 && q.rem == 0 && s1 == q.np) {
+  if (!kBytes<TY> && q.rem == 0 && s1 == q.np) {
     pa = gk::last_element_slot<OA>(m0, p.M, p.K, p.A, la.ext, tid, va);
     pb = gk::last_element_slot<OB>(n0, p.N, p.K, p.B, lb.ext, tid, vb);
   }
@@ -1116,6 +1278,14 @@ __global__ void __launch_bounds__(256) lin_ring(LinArgs p) {
   corner_of<256, 256>(p, k.tile, m0, n0);
   ring_tile<TY, AKM, BKM>(p, m0, n0, k, SA, SB);
 }
+// The same on int8 operands.
+__global__ void __launch_bounds__(256) lin_i8_ring(LinArgs p) {
+  GK_DECLARE_RING()
+  int m0, n0;
+  const Work k = work_of<256, 256>(p, blockIdx.x);
+  corner_of<256, 256>(p, k.tile, m0, n0);
+  ring_tile<kI8, true, true>(p, m0, n0, k, SA, SB);
+}
 
 // The k slices of the split tiles added in order, then the epilogue; a thread per 8 columns, 256
 // threads a workgroup, PER workgroups a BM x BN tile (the last one not always full).  Latency
@@ -1128,13 +1298,18 @@ __global__ void __launch_bounds__(256) lin_reduce(LinArgs p) {
   int m0, n0;
   corner_of<BM, BN>(p, p.first_split + i, m0, n0);
   const int r = t / Q, c = (t - r * Q) * 8, row = m0 + r, col = n0 + c;
-  if (row >= p.M || col >= p.N) return;
+  if (!takes_part(p, row, col)) return;
   const float* w = p.W + (int64_t)i * p.splits * (BM * BN) + r * BN + c;
   float4v lo = *(const float4v*)w, hi = *(const float4v*)(w + 4);
 #pragma unroll 4
   for (int z = 1; z < p.splits; ++z) {
-    lo += *(const float4v*)(w + (int64_t)z * (BM * BN));
-    hi += *(const float4v*)(w + (int64_t)z * (BM * BN) + 4);
+    const float4v l = *(const float4v*)(w + (int64_t)z * (BM * BN));
+    const float4v h = *(const float4v*)(w + (int64_t)z * (BM * BN) + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[e] = sum_add<TY>(lo[e], l[e]);
+      hi[e] = sum_add<TY>(hi[e], h[e]);
+    }
   }
   float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   finish8<TY>(p, row, col, f, load_columns<TY>(p, col));

@@ -44,9 +44,12 @@ void launch_staged(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s
 
 template <int TY, bool AKM, bool BKM>
 void launch_tile(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
-  if (g.tile == kTile256)
-    hipLaunchKernelGGL((lin_ring<TY, AKM, BKM>), grid, dim3(256), 0, s, a);
-  else if (TY == kE4M3 && a.K <= kHalvesK)
+  if (g.tile == kTile256) {
+    if constexpr (TY == kI8)
+      hipLaunchKernelGGL(lin_i8_ring, grid, dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((lin_ring<TY, AKM, BKM>), grid, dim3(256), 0, s, a);
+  } else if (TY == kE4M3 && a.K <= kHalvesK)
     launch_staged<TY, AKM, BKM, TY == kE4M3>(g, a, grid, s);
   else
     launch_staged<TY, AKM, BKM, false>(g, a, grid, s);
@@ -63,19 +66,22 @@ template <int TY>
 hipError_t launch_type(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
   const dim3 grid((uint32_t)g.grid());
   if (g.path == kPathSkinnyK) {
-    if (a.K < (TY == kE4M3 ? 16 : 8))   // such rows need no more than one wave
-      hipLaunchKernelGGL((lin_skinny_k<TY, 1, 1, true>), grid, dim3(64), 0, s, a);
-    else if (g.cols == 16)
+    if (a.K < (kBytes<TY> ? 16 : 8)) {   // such rows need no more than one wave
+      if (g.cols == 16)
+        hipLaunchKernelGGL((lin_skinny_k<TY, 1, 1, true>), grid, dim3(64), 0, s, a);
+      else
+        hipLaunchKernelGGL((lin_skinny_k<TY, 2, 1, true>), grid, dim3(64), 0, s, a);
+    } else if (g.cols == 16)
       hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8, false>), grid, dim3(512), 0, s, a);
     else if (g.cols == 32)
       hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8, false>), grid, dim3(512), 0, s, a);
     else
       hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8, false>), grid, dim3(512), 0, s, a);
   } else if (g.path == kPathSkinnyN) {
-    if constexpr (TY != kE4M3) {
+    if constexpr (!kBytes<TY>) {
       hipLaunchKernelGGL((lin_skinny_n<TY, 4, 8>), grid, dim3(512), 0, s, a);
     }
-  } else if constexpr (TY == kE4M3) {
+  } else if constexpr (kBytes<TY>) {
     launch_tile<TY, true, true>(g, a, grid, s);
   } else if (g.akm) {
     if (g.bkm)

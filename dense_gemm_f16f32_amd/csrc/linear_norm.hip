@@ -1,4 +1,4 @@
-// C-ABI of the linear layer and the root-mean-square norm: argument checks, kernel choice,
+// C-ABI of the linear layer, the norms and rows in 8 bits: argument checks, kernel choice,
 // launches.  The declarations and their contracts are in include/linear_norm.h.
 #include "linear_norm.h"
 
@@ -21,6 +21,7 @@ int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t round_up(int64_t x, int64_t y) { return cdiv(x, y) * y; }
 
 bool is16(int64_t type) { return type == LINEAR_NORM_F16 || type == LINEAR_NORM_BF16; }
+bool is8(int64_t type) { return type == LINEAR_NORM_E4M3 || type == LINEAR_NORM_I8; }
 
 // ---- matrices ------------------------------------------------------------------------------
 // Bytes from a matrix's first element to one past its last (rows ld apart); saturating.
@@ -70,7 +71,7 @@ struct Operand {
 };
 int operand(const void* p, int64_t X, int64_t K, int64_t sx, int64_t sk, int64_t type,
             Operand* o) {
-  const int64_t elem = type == LINEAR_NORM_E4M3 ? 1 : 2;
+  const int64_t elem = is8(type) ? 1 : 2;
   *o = {p, K > 1 ? K : 1, true};
   if (X == 0 || K == 0) return GEMM_F16F32_OK;
   if (p == nullptr) return GEMM_F16F32_ERR_NULL;
@@ -91,7 +92,7 @@ int operand(const void* p, int64_t X, int64_t K, int64_t sx, int64_t sk, int64_t
   return GEMM_F16F32_OK;
 }
 Region operand_region(const Operand& o, int64_t X, int64_t K, int64_t type) {
-  const int64_t e = type == LINEAR_NORM_E4M3 ? 1 : 2;
+  const int64_t e = is8(type) ? 1 : 2;
   return o.km ? region(o.p, X, K, o.ld, e) : region(o.p, K, X, o.ld, e);
 }
 
@@ -127,10 +128,11 @@ double round_cost(const TileCost& c, int64_t workgroups, int64_t panels) {
   return workgroups <= kCUs ? c.fixed1 + panels * c.panel1 : c.fixed + panels * c.panel;
 }
 
-// The path, tile and split of an M x N x K product (M, N > 0).
+// The path, tile and split of an M x N x K product (M, N > 0).  `blocks`: the epilogue packs blocks
+// of 32 columns, which one workgroup has to hold.
 int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b,
-              GemmPlan* g) {
-  const int64_t E = type == LINEAR_NORM_E4M3 ? 2 : 1;
+              bool blocks, GemmPlan* g) {
+  const int64_t E = is8(type) ? 2 : 1;
   *g = {};
   g->akm = a.km;
   g->bkm = b.km;
@@ -152,6 +154,7 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     if (b.km && (M <= 8 || K < 16 || (wide < kCUs && (2 * wide < kCUs || depth < 64))))
       g->cols = M > 8 && K >= 16 && 2 * wide >= kCUs ? 32 : 16;
     if (K >= 8 * E && cdiv(N, g->cols) * 512 >= kThreads) g->cols = 64;
+    if (blocks && g->cols == 16) g->cols = 32;
     g->programs = cdiv(N, g->cols);
     // Few columns leave CUs idle: slices of k, of 16 units at least, up to a workgroup a CU.
     // Below 64 units the second launch costs more (4 rows, 512 columns, K = 8192 in bf16: 6.8 us
@@ -215,10 +218,10 @@ struct Product {
   double cost;
 };
 int plan_product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a,
-                 const Operand& b, Product* p) {
+                 const Operand& b, bool blocks, Product* p) {
   p->part[0] = {{}, 0, 0, M, N};
   p->parts = 1;
-  const int rc = plan_gemm(type, M, N, K, a, b, &p->part[0].g);
+  const int rc = plan_gemm(type, M, N, K, a, b, blocks, &p->part[0].g);
   if (rc != GEMM_F16F32_OK) return rc;
   p->cost = p->part[0].g.cost;
   // In one piece a sliver costs a whole row of tiles, or a second round of workgroups; cut off, a
@@ -236,7 +239,7 @@ int plan_product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a
     q.cost = 2.5 * (q.parts - 1);
     for (int i = 0; ok && i < q.parts; ++i) {
       Part& t = q.part[i];
-      ok = plan_gemm(type, t.M, t.N, K, a, b, &t.g) == GEMM_F16F32_OK;
+      ok = plan_gemm(type, t.M, t.N, K, a, b, blocks, &t.g) == GEMM_F16F32_OK;
       q.cost += t.g.cost;
     }
     if (ok && q.cost < p->cost) *p = q;
@@ -249,7 +252,7 @@ int plan_product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a
 
 // The kernel arguments of a product, epilogue left empty.
 LinArgs product(int64_t type, int64_t K, const Operand& a, const Operand& b) {
-  const int64_t E = type == LINEAR_NORM_E4M3 ? 2 : 1;
+  const int64_t E = is8(type) ? 2 : 1;
   LinArgs p = {};
   p.A = (const uint16_t*)a.p;
   p.B = (const uint16_t*)b.p;
@@ -270,6 +273,10 @@ LinArgs part_args(const LinArgs& whole, const Part& t, void* ws) {
   }
   p.out += t.m0 * p.ldo + t.n0;
   if (p.pre) p.pre += t.m0 * p.ldp + t.n0;
+  if (p.pre8) {   // n0 is a multiple of 256
+    p.pre8 += t.m0 * p.ldp8 + t.n0;
+    p.pre8_scale += t.m0 * p.ldps + t.n0 / 32;
+  }
   if (p.res) p.res += t.m0 * p.ldr + t.n0;
   if (p.bias) p.bias += t.n0;
   if (p.scale_a) p.scale_a += t.m0;
@@ -299,6 +306,7 @@ int launch(int64_t type, const Product& q, const LinArgs& whole, void* ws, void*
     const GemmPlan& g = q.part[i].g;
     const hipError_t e = type == LINEAR_NORM_F16    ? lk::launch_type<lk::kF16>(g, p, s)
                          : type == LINEAR_NORM_BF16 ? lk::launch_type<lk::kBF16>(g, p, s)
+                         : type == LINEAR_NORM_I8   ? lk::launch_type<lk::kI8>(g, p, s)
                                                     : lk::launch_type<lk::kE4M3>(g, p, s);
     if (e != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
@@ -316,37 +324,60 @@ int64_t partial_bytes(int64_t groups, int64_t cols) { return groups * round_up(c
 
 bool bad_dim(int64_t d) { return d < 0 || d >= kMax; }
 
+// ---- checkpoints in 8 bits -----------------------------------------------------------------------
+constexpr int64_t kBlock = 32;   // values that share a scale
+int check_packed(packed8_matrix* p, int64_t rows, int64_t dim) {
+  int rc = check_rows(p->values, rows, dim, &p->values_row, 1, true);
+  if (rc == 0) rc = check_rows(p->scale, rows, cdiv(dim, kBlock), &p->scale_row, 1, true);
+  return rc;
+}
+Region values_region(const packed8_matrix& p, int64_t rows, int64_t dim) {
+  return region(p.values, rows, dim, p.values_row, 1);
+}
+Region scale_region(const packed8_matrix& p, int64_t rows, int64_t dim) {
+  return region(p.scale, rows, cdiv(dim, kBlock), p.scale_row, 1);
+}
+
 // ---- linear_forward ----------------------------------------------------------------------------
 struct ForwardPlan {
   Operand a, b;
   Product q;   // no parts: an empty result
 };
-int plan_forward(linear_forward_args& x, ForwardPlan* f) {
+// `pre`: where the value before the activation goes in 8 bits, or null
+int plan_forward(linear_forward_args& x, packed8_matrix* pre, ForwardPlan* f) {
   *f = {};
   if (bad_dim(x.m) || bad_dim(x.n) || bad_dim(x.k)) return GEMM_F16F32_ERR_DIM;
-  if (!is16(x.type) && x.type != LINEAR_NORM_E4M3) return GEMM_F16F32_ERR_OPTS;
+  if (!is16(x.type) && !is8(x.type)) return GEMM_F16F32_ERR_OPTS;
   if (!is16(x.out_type) || (is16(x.type) && x.out_type != x.type)) return GEMM_F16F32_ERR_OPTS;
   if (x.activation < LINEAR_ACT_NONE || x.activation > LINEAR_ACT_SILU)
     return GEMM_F16F32_ERR_OPTS;
   if (is16(x.type) && (x.scale_a || x.scale_b)) return GEMM_F16F32_ERR_OPTS;
+  if (pre && x.pre) return GEMM_F16F32_ERR_OPTS;
+  // sums of products of up to 2^14 in 32-bit integers
+  if (x.type == LINEAR_NORM_I8 && x.k >= (1 << 17)) return GEMM_F16F32_ERR_TOO_LARGE;
   if (x.m == 0 || x.n == 0) return GEMM_F16F32_OK;
   int rc = operand(x.a, x.m, x.k, x.a_row, x.a_col, x.type, &f->a);
   if (rc == 0) rc = operand(x.b, x.n, x.k, x.b_col, x.b_row, x.type, &f->b);
   if (rc == 0) rc = check_rows(x.out, x.m, x.n, &x.out_row, 2, true);
   if (rc == 0) rc = check_rows(x.pre, x.m, x.n, &x.pre_row, 2, false);
   if (rc == 0) rc = check_rows(x.residual, x.m, x.n, &x.residual_row, 2, false);
+  if (rc == 0 && pre) rc = check_packed(pre, x.m, x.n);
   if (rc != 0) return rc;
   if (((uintptr_t)x.bias & 1) || (((uintptr_t)x.scale_a | (uintptr_t)x.scale_b) & 3))
     return GEMM_F16F32_ERR_OPTS;
-  const Region w[] = {region(x.out, x.m, x.n, x.out_row, 2), region(x.pre, x.m, x.n, x.pre_row, 2)};
+  const packed8_matrix none = {}, &p8 = pre ? *pre : none;
+  const Region w[] = {region(x.out, x.m, x.n, x.out_row, 2), region(x.pre, x.m, x.n, x.pre_row, 2),
+                      values_region(p8, x.m, x.n), scale_region(p8, x.m, x.n)};
   const Region r[] = {operand_region(f->a, x.m, x.k, x.type), operand_region(f->b, x.n, x.k, x.type),
                       region(x.bias, 1, x.n, x.n, 2), region(x.scale_a, 1, x.m, x.m, 4),
                       region(x.scale_b, 1, x.n, x.n, 4)};
-  if (conflict(w, 2, r, 5)) return GEMM_F16F32_ERR_OVERLAP;
+  if (conflict(w, 4, r, 5)) return GEMM_F16F32_ERR_OVERLAP;
   const Region res = region(x.residual, x.m, x.n, x.residual_row, 2);
   const bool in_place = x.residual == x.out && x.residual_row == x.out_row;
-  if (overlap(w[1], res) || (!in_place && overlap(w[0], res))) return GEMM_F16F32_ERR_OVERLAP;
-  return plan_product(x.type, x.m, x.n, x.k, f->a, f->b, &f->q);
+  if (overlap(w[1], res) || overlap(w[2], res) || overlap(w[3], res) ||
+      (!in_place && overlap(w[0], res)))
+    return GEMM_F16F32_ERR_OVERLAP;
+  return plan_product(x.type, x.m, x.n, x.k, f->a, f->b, pre != nullptr, &f->q);
 }
 
 // ---- linear_backward ----------------------------------------------------------------------------
@@ -359,17 +390,29 @@ struct BackwardPlan {
   Product qa, qb;            // da's and db's products
   int64_t ldd;               // dpre's row stride
   int row_blocks, rows_per_block;
-  int64_t dpre_bytes, part_bytes, w_bytes;
+  int64_t dpre_bytes, part_bytes, a_bytes, w_bytes;
+  int64_t lda;               // row stride of a, restored from 8 bits
+  int64_t bytes() const { return dpre_bytes + part_bytes + a_bytes + w_bytes; }
 };
-int plan_backward(linear_backward_args& x, BackwardPlan* f) {
+// `kept`: what stands in for a and pre, its parts null where they are given in 16 bits; or null
+int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
   *f = {};
   if (bad_dim(x.m) || bad_dim(x.n) || bad_dim(x.k)) return GEMM_F16F32_ERR_DIM;
   if (!is16(x.type)) return GEMM_F16F32_ERR_OPTS;
   if (x.activation < LINEAR_ACT_NONE || x.activation > LINEAR_ACT_SILU)
     return GEMM_F16F32_ERR_OPTS;
   const bool act = x.activation != LINEAR_ACT_NONE;
+  linear_kept none = {};
+  linear_kept& k8 = kept ? *kept : none;
+  const bool pre8 = act && k8.pre.values, a8 = k8.a.values != nullptr;
+  if (k8.a_activation < LINEAR_ACT_NONE || k8.a_activation > LINEAR_ACT_SILU)
+    return GEMM_F16F32_ERR_OPTS;
+  if ((pre8 && x.pre) || (a8 && x.a) || (!a8 && k8.a_activation != LINEAR_ACT_NONE))
+    return GEMM_F16F32_ERR_OPTS;
   int rc = check_rows(x.dc, x.m, x.n, &x.dc_row, 2, true);
-  if (rc == 0 && act) rc = check_rows(x.pre, x.m, x.n, &x.pre_row, 2, true);
+  if (rc == 0 && act && !pre8) rc = check_rows(x.pre, x.m, x.n, &x.pre_row, 2, true);
+  if (rc == 0 && pre8) rc = check_packed(&k8.pre, x.m, x.n);
+  if (rc == 0 && a8) rc = check_packed(&k8.a, x.m, x.k);
   if (rc == 0) rc = check_rows(x.da, x.m, x.k, &x.da_row, 2, false);
   if (rc != 0) return rc;
   if ((uintptr_t)x.dbias & 1) return GEMM_F16F32_ERR_OPTS;
@@ -380,9 +423,15 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     rb = operand_region(f->b, x.k, x.n, x.type);
   }
   if (x.db && x.k > 0 && x.n > 0) {
-    rc = operand(x.a, x.k, x.m, x.a_col, x.a_row, x.type, &f->a);
-    if (rc != 0) return rc;
-    ra = operand_region(f->a, x.k, x.m, x.type);
+    if (a8) {   // in the workspace, rows on 128-byte lines
+      f->lda = round_up(x.k, 64);
+      f->a = {x.dc, f->lda, false};
+      f->a_bytes = x.m > 0 ? round_up(x.m * f->lda * 2, 256) : 0;
+    } else {
+      rc = operand(x.a, x.k, x.m, x.a_col, x.a_row, x.type, &f->a);
+      if (rc != 0) return rc;
+      ra = operand_region(f->a, x.k, x.m, x.type);
+    }
     // db's order: a unit stride along n, or along k
     if ((x.db_col == 1 || x.n == 1) && (x.k == 1 || x.db_row >= x.n)) {
       rc = check_rows(x.db, x.k, x.n, &x.db_row, 2, true);
@@ -398,8 +447,12 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
   }
   const Region w[] = {region(x.da, x.m, x.k, x.da_row, 2), rdb, region(x.dbias, 1, x.n, x.n, 2)};
   const Region r[] = {region(x.dc, x.m, x.n, x.dc_row, 2), ra, rb,
-                      region(act ? x.pre : nullptr, x.m, x.n, x.pre_row, 2)};
-  if (conflict(w, 3, r, 4)) return GEMM_F16F32_ERR_OVERLAP;
+                      region(act ? x.pre : nullptr, x.m, x.n, x.pre_row, 2),
+                      values_region(k8.a, x.m, x.k), scale_region(k8.a, x.m, x.k),
+                      region(pre8 ? k8.pre.values : nullptr, x.m, x.n, k8.pre.values_row, 1),
+                      region(pre8 ? k8.pre.scale : nullptr, x.m, cdiv(x.n, kBlock),
+                             k8.pre.scale_row, 1)};
+  if (conflict(w, 3, r, 8)) return GEMM_F16F32_ERR_OVERLAP;
 
   // the element-wise pass: dpre (rows on 128-byte lines), and blocks of rows for its column sums
   f->dact = x.n > 0 && ((act && x.m > 0) || x.dbias);
@@ -424,14 +477,14 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
   const int64_t ldd = act ? f->ldd : x.dc_row;
   if (x.da && x.m > 0 && x.k > 0) {
     const Operand d = {x.dc, ldd, true};
-    rc = plan_product(x.type, x.m, x.k, x.n, d, f->b, &f->qa);
+    rc = plan_product(x.type, x.m, x.k, x.n, d, f->b, false, &f->qa);
     if (rc != 0) return rc;
     if (f->qa.w_bytes > f->w_bytes) f->w_bytes = f->qa.w_bytes;
   }
   if (x.db && x.k > 0 && x.n > 0) {
     f->dt = {x.dc, ldd, false};
-    rc = f->db_cols ? plan_product(x.type, x.n, x.k, x.m, f->dt, f->a, &f->qb)
-                    : plan_product(x.type, x.k, x.n, x.m, f->a, f->dt, &f->qb);
+    rc = f->db_cols ? plan_product(x.type, x.n, x.k, x.m, f->dt, f->a, false, &f->qb)
+                    : plan_product(x.type, x.k, x.n, x.m, f->a, f->dt, false, &f->qb);
     if (rc != 0) return rc;
     if (f->qb.w_bytes > f->w_bytes) f->w_bytes = f->qb.w_bytes;
   }
@@ -457,7 +510,7 @@ int plan_backward(linear_backward_args& x, BackwardPlan* f) {
     // 7.5, 4 x 200 x 300 8.9 and 7.9, 64 x 256 x 3000 8.2 and 7.9, 300^3, past the rule, 11.8 and
     // 9.6).  At four panels only the launch's 3 us of host time speak for it, which a captured
     // graph does not pay.
-    f->small = f->pair && deep <= 4 && x.n >= 8 && x.k >= 8;
+    f->small = f->pair && deep <= 4 && x.n >= 8 && x.k >= 8 && !a8 && !pre8;
     if (f->pair) {
       GemmPlan t = {};
       t.path = lk::kPathTiles;
@@ -501,20 +554,38 @@ void with_row_shape(int64_t dim, F f) {
   else f(std::integral_constant<int, 16>{}, std::integral_constant<int, 0>{});
 }
 
-template <int TY, bool Q8>
+template <int TY, int OUT, bool LN>
 void norm_forward(const nk::NormArgs& p, hipStream_t s) {
   with_row_shape(p.dim, [&](auto nw, auto c) {
-    hipLaunchKernelGGL((nk::rms_norm_fwd<TY, Q8, nw.value, c.value>), dim3((uint32_t)p.rows),
+    hipLaunchKernelGGL((nk::norm_fwd<TY, OUT, LN, nw.value, c.value>), dim3((uint32_t)p.rows),
                        dim3(64 * nw.value), 0, s, p);
   });
+}
+template <int TY, int OUT>
+void quantize(const nk::QuantizeArgs& p, int64_t rows, hipStream_t s) {
+  with_row_shape(p.dim, [&](auto nw, auto c) {
+    hipLaunchKernelGGL((nk::quantize_rows<TY, OUT, nw.value, c.value>), dim3((uint32_t)rows),
+                       dim3(64 * nw.value), 0, s, p);
+  });
+}
+// f(type, form) with a 16-bit type and a form of rows (nk::kOut16, ...) as constants.
+template <class F>
+void with_types(int64_t type, int64_t out_type, F f) {
+  auto with_out = [&](auto ty) {
+    if (out_type == LINEAR_NORM_E4M3) f(ty, std::integral_constant<int, nk::kOutE4M3>{});
+    else if (out_type == LINEAR_NORM_I8) f(ty, std::integral_constant<int, nk::kOutI8>{});
+    else f(ty, std::integral_constant<int, nk::kOut16>{});
+  };
+  if (type == LINEAR_NORM_BF16) with_out(std::integral_constant<int, lk::kBF16>{});
+  else with_out(std::integral_constant<int, lk::kF16>{});
 }
 // The backward pass: as above, but short rows take one wave, four of them a workgroup, and rows
 // above 8192 fewer waves of more registers.
 constexpr int64_t kShortRow = 1024, kLongRow = 16384;
-template <int TY>
+template <int TY, bool LN>
 void norm_backward(const nk::NormBwdArgs& p, int grid, hipStream_t s) {
 #define LN_BACKWARD(NW, C, RW)                                                               \
-  hipLaunchKernelGGL((nk::rms_norm_bwd<TY, NW, C, RW>), dim3((uint32_t)grid), dim3(64 * NW * RW), \
+  hipLaunchKernelGGL((nk::norm_bwd<TY, LN, NW, C, RW>), dim3((uint32_t)grid), dim3(64 * NW * RW), \
                      0, s, p)
   if (p.dim <= 512) LN_BACKWARD(1, 1, 4);
   else if (p.dim <= kShortRow) LN_BACKWARD(1, 2, 4);
@@ -523,7 +594,7 @@ void norm_backward(const nk::NormBwdArgs& p, int grid, hipStream_t s) {
   else if (p.dim <= 8192) LN_BACKWARD(8, 2, 1);
   else if (p.dim <= kLongRow) LN_BACKWARD(8, 4, 1);
   else
-    hipLaunchKernelGGL((nk::rms_norm_bwd_long<TY, 16>), dim3((uint32_t)grid), dim3(1024), 0, s, p);
+    hipLaunchKernelGGL((nk::norm_bwd_long<TY, LN, 16>), dim3((uint32_t)grid), dim3(1024), 0, s, p);
 #undef LN_BACKWARD
 }
 
@@ -543,39 +614,228 @@ bool backward_sums(int64_t rows, int64_t dim) {
   return dim > kLongRow || backward_groups(rows, dim) != 1;
 }
 
-int64_t norm_backward_bytes(const rms_norm_backward_args& x) {
-  return x.dweight && backward_sums(x.rows, x.dim)
-             ? partial_bytes(backward_groups(x.rows, x.dim), x.dim)
-             : 0;
+// Bytes of one gradient's partial sums, and of all.
+int64_t norm_part_bytes(int64_t rows, int64_t dim) {
+  return backward_sums(rows, dim) ? partial_bytes(backward_groups(rows, dim), dim) : 0;
+}
+int64_t norm_backward_bytes(const layer_norm_backward_args& x) {
+  return ((x.dweight != nullptr) + (x.dbias != nullptr)) * norm_part_bytes(x.rows, x.dim);
 }
 
+// Column sums from their partial sums; `more`: another gradient's, whose partial sums follow, or null
 template <int TY>
-void launch_sum(const float* part, int n, int64_t cols, void* out, hipStream_t s) {
-  const int64_t blocks = cdiv(cols, 32), most = kThreads / 256 - 1;
-  for (int64_t first = 0; first < blocks; first += most) {
-    const int64_t grid = blocks - first < most ? blocks - first : most;
+void launch_sum(const float* part, int n, int64_t cols, void* out, void* more, hipStream_t s) {
+  const int64_t blocks = cdiv(cols, 32), all = more ? 2 * blocks : blocks;
+  const int64_t most = kThreads / 256 - 1;
+  for (int64_t first = 0; first < all; first += most) {
+    const int64_t grid = all - first < most ? all - first : most;
     hipLaunchKernelGGL((nk::sum_partials<TY>), dim3((uint32_t)grid), dim3(256), 0, s, part, n,
-                       (int)first, (int)cols, (uint16_t*)out);
+                       (int)first, (int)cols, (int)blocks, (uint16_t*)out, (uint16_t*)more);
   }
+}
+
+int norm_forward_call(layer_norm_forward_args x, bool ln) {
+  int rc = check_norm(x.rows, x.dim, x.type);
+  if (rc != GEMM_F16F32_OK) return rc;
+  const bool q8 = is8(x.out_type);
+  if ((!q8 && x.out_type != x.type) || !(x.eps >= 0.0) || (x.scale && !q8))
+    return GEMM_F16F32_ERR_OPTS;
+  if (x.rows == 0) return GEMM_F16F32_OK;
+  rc = check_rows(x.x, x.rows, x.dim, &x.x_row, 2, true);
+  if (rc == 0) rc = check_rows(x.residual, x.rows, x.dim, &x.residual_row, 2, false);
+  if (rc == 0) rc = check_rows(x.y, x.rows, x.dim, &x.y_row, q8 ? 1 : 2, true);
+  if (rc == 0) rc = check_rows(x.h, x.rows, x.dim, &x.h_row, 2, x.residual != nullptr);
+  if (rc != 0) return rc;
+  if (x.weight == nullptr || (q8 && x.scale == nullptr)) return GEMM_F16F32_ERR_NULL;
+  if ((((uintptr_t)x.weight | (uintptr_t)x.bias) & 1) ||
+      (((uintptr_t)x.scale | (uintptr_t)x.mean | (uintptr_t)x.rstd) & 3))
+    return GEMM_F16F32_ERR_OPTS;
+  const Region rx = region(x.x, x.rows, x.dim, x.x_row, 2);
+  const Region rr = region(x.residual, x.rows, x.dim, x.residual_row, 2);
+  const Region rh = region(x.h, x.rows, x.dim, x.h_row, 2);
+  const Region w[] = {region(x.y, x.rows, x.dim, x.y_row, q8 ? 1 : 2),
+                      region(x.scale, 1, x.rows, x.rows, 4), region(x.mean, 1, x.rows, x.rows, 4),
+                      region(x.rstd, 1, x.rows, x.rows, 4), rh};
+  const Region r[] = {rx, rr, region(x.weight, 1, x.dim, x.dim, 2),
+                      region(x.bias, 1, x.dim, x.dim, 2)};
+  if (conflict(w, 4, r, 4) || conflict(w, 5, r + 2, 2)) return GEMM_F16F32_ERR_OVERLAP;
+  if ((!(x.h == x.x && x.h_row == x.x_row) && overlap(rh, rx)) ||
+      (!(x.h == x.residual && x.h_row == x.residual_row) && overlap(rh, rr)))
+    return GEMM_F16F32_ERR_OVERLAP;
+  const int64_t ys = q8 ? 1 : 2;
+  for (int64_t r0 = 0; r0 < x.rows; r0 += kRowsPerLaunch) {
+    nk::NormArgs p = {};
+    p.x = (const uint16_t*)x.x + r0 * x.x_row;
+    p.x_row = x.x_row;
+    if (x.residual) p.res = (const uint16_t*)x.residual + r0 * x.residual_row;
+    p.res_row = x.residual_row;
+    p.weight = (const uint16_t*)x.weight;
+    p.bias = (const uint16_t*)x.bias;
+    p.y = (char*)x.y + ys * r0 * x.y_row;
+    p.y_row = x.y_row;
+    if (x.scale) p.scale = x.scale + r0;
+    if (x.h) p.h = (uint16_t*)x.h + r0 * x.h_row;
+    p.h_row = x.h_row;
+    if (x.mean) p.mean = x.mean + r0;
+    if (x.rstd) p.rstd = x.rstd + r0;
+    p.rows = (int32_t)(x.rows - r0 < kRowsPerLaunch ? x.rows - r0 : kRowsPerLaunch);
+    p.dim = (int32_t)x.dim;
+    p.eps = (float)x.eps;
+    p.inv_dim = (float)(1.0 / (double)x.dim);
+    with_types(x.type, x.out_type, [&](auto ty, auto out) {
+      ln ? norm_forward<ty.value, out.value, true>(p, (hipStream_t)x.stream)
+         : norm_forward<ty.value, out.value, false>(p, (hipStream_t)x.stream);
+    });
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  return GEMM_F16F32_OK;
+}
+
+int norm_backward_call(layer_norm_backward_args x, bool ln) {
+  int rc = check_norm(x.rows, x.dim, x.type);
+  if (rc == 0) rc = check_rows(x.dy, x.rows, x.dim, &x.dy_row, 2, true);
+  if (rc == 0) rc = check_rows(x.h, x.rows, x.dim, &x.h_row, 2, true);
+  if (rc == 0) rc = check_rows(x.dh, x.rows, x.dim, &x.dh_row, 2, false);
+  if (rc == 0) rc = check_rows(x.dx, x.rows, x.dim, &x.dx_row, 2, true);
+  if (rc != 0) return rc;
+  if (x.rows > 0 && (x.weight == nullptr || x.rstd == nullptr || (ln && x.mean == nullptr)))
+    return GEMM_F16F32_ERR_NULL;
+  if ((((uintptr_t)x.weight | (uintptr_t)x.dweight | (uintptr_t)x.dbias) & 1) ||
+      (((uintptr_t)x.mean | (uintptr_t)x.rstd) & 3))
+    return GEMM_F16F32_ERR_OPTS;
+  const int64_t need = norm_backward_bytes(x);
+  rc = check_workspace(x.workspace, x.workspace_bytes, need);
+  if (rc != GEMM_F16F32_OK) return rc;
+  const Region rdx = region(x.dx, x.rows, x.dim, x.dx_row, 2);
+  const Region rdy = region(x.dy, x.rows, x.dim, x.dy_row, 2);
+  const Region rdh = region(x.dh, x.rows, x.dim, x.dh_row, 2);
+  const Region w[] = {region(x.dweight, 1, x.dim, x.dim, 2), region(x.dbias, 1, x.dim, x.dim, 2),
+                      {x.workspace, (uint64_t)need}, rdx};
+  const Region r[] = {region(x.h, x.rows, x.dim, x.h_row, 2),
+                      region(x.weight, 1, x.dim, x.dim, 2), region(x.mean, 1, x.rows, x.rows, 4),
+                      region(x.rstd, 1, x.rows, x.rows, 4), rdy, rdh};
+  if (conflict(w, 3, r, 6) || conflict(w, 4, r, 4)) return GEMM_F16F32_ERR_OVERLAP;
+  if ((!(x.dx == x.dy && x.dx_row == x.dy_row) && overlap(rdx, rdy)) ||
+      (!(x.dx == x.dh && x.dx_row == x.dh_row) && overlap(rdx, rdh)))
+    return GEMM_F16F32_ERR_OVERLAP;
+  const hipStream_t s = (hipStream_t)x.stream;
+  const bool bf = x.type == LINEAR_NORM_BF16;
+  const int groups = backward_groups(x.rows, x.dim);
+  const bool sums = backward_sums(x.rows, x.dim);
+  float* const part = (float*)x.workspace;
+  if (groups > 0) {
+    nk::NormBwdArgs p = {};
+    p.dy = (const uint16_t*)x.dy;
+    p.dy_row = x.dy_row;
+    p.h = (const uint16_t*)x.h;
+    p.h_row = x.h_row;
+    p.weight = (const uint16_t*)x.weight;
+    p.mean = x.mean;
+    p.rstd = x.rstd;
+    p.dh = (const uint16_t*)x.dh;
+    p.dh_row = x.dh_row;
+    p.dx = (uint16_t*)x.dx;
+    p.dx_row = x.dx_row;
+    if (sums) {   // dweight's, then dbias'
+      if (x.dweight) p.part = part;
+      if (x.dbias)
+        p.part_bias = part + (x.dweight ? norm_part_bytes(x.rows, x.dim) / 4 : 0);
+    } else {
+      p.dweight = (uint16_t*)x.dweight;
+      p.dbias = (uint16_t*)x.dbias;
+    }
+    p.rows = (int32_t)x.rows;
+    p.dim = (int32_t)x.dim;
+    p.inv_dim = (float)(1.0 / (double)x.dim);
+    if (ln)
+      bf ? norm_backward<lk::kBF16, true>(p, groups, s) : norm_backward<lk::kF16, true>(p, groups, s);
+    else
+      bf ? norm_backward<lk::kBF16, false>(p, groups, s)
+         : norm_backward<lk::kF16, false>(p, groups, s);
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  if ((x.dweight || x.dbias) && sums) {
+    void* const first = x.dweight ? x.dweight : x.dbias;
+    void* const more = x.dweight ? x.dbias : nullptr;
+    bf ? launch_sum<lk::kBF16>(part, groups, x.dim, first, more, s)
+       : launch_sum<lk::kF16>(part, groups, x.dim, first, more, s);
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+  }
+  return GEMM_F16F32_OK;
+}
+
+// ---- checkpoints in 8 bits: launches ---------------------------------------------------------
+// Pieces of a row's 8-column chunks: a wave's 64, or for shorter rows the next power of two from 4
+// (a block of 32 columns stays in 4 lanes of one wave).
+nk::PackArgs pack_args(int64_t dim, const packed8_matrix& p) {
+  nk::PackArgs a = {};
+  const int64_t chunks = cdiv(dim, kBlock) * 4;
+  a.lanes = 2;
+  while (a.lanes < 6 && ((int64_t)1 << a.lanes) < chunks) ++a.lanes;
+  a.segs = (int32_t)cdiv(chunks, (int64_t)1 << a.lanes);
+  a.q = (uint8_t*)p.values;
+  a.q_row = p.values_row;
+  a.scale = (uint8_t*)p.scale;
+  a.s_row = p.scale_row;
+  a.dim = (int32_t)dim;
+  return a;
+}
+// Launches f(args, grid) over all rows, in launches that stay below kThreads.
+template <class F>
+int pack_launches(nk::PackArgs a, int64_t rows, F f) {
+  const int64_t per = (int64_t)4 * nk::kPackRows * (64 >> a.lanes);   // rows a workgroup
+  const int64_t most = (kThreads / 256 - 1) / a.segs * per;           // segs is below 2^23
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    const int64_t n = rows - r0 < most ? rows - r0 : most;
+    a.rows = (int32_t)n;
+    f(a, dim3((uint32_t)(cdiv(n, per) * a.segs)));
+    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+    if (a.x) a.x += n * a.x_row;
+    if (a.y) a.y += n * a.y_row;
+    a.q += n * a.q_row;
+    a.scale += n * a.s_row;
+  }
+  return GEMM_F16F32_OK;
+}
+int unpack_rows(int64_t type, int64_t rows, int64_t dim, const packed8_matrix& p, int64_t activation,
+                void* y, int64_t y_row, hipStream_t s) {
+  nk::PackArgs a = pack_args(dim, p);
+  a.y = (uint16_t*)y;
+  a.y_row = y_row;
+  a.act = (int32_t)activation;
+  return pack_launches(a, rows, [&](const nk::PackArgs& b, dim3 grid) {
+    if (type == LINEAR_NORM_BF16)
+      hipLaunchKernelGGL((nk::unpack8_rows<lk::kBF16>), grid, dim3(256), 0, s, b);
+    else
+      hipLaunchKernelGGL((nk::unpack8_rows<lk::kF16>), grid, dim3(256), 0, s, b);
+  });
 }
 
 }  // namespace
 
 extern "C" {
 
-int64_t linear_forward_workspace(const linear_forward_args* args) {
+int64_t linear_forward_packed_workspace(const linear_forward_args* args,
+                                        const packed8_matrix* pre) {
   if (args == nullptr) return GEMM_F16F32_ERR_NULL;
   linear_forward_args x = *args;
+  packed8_matrix p8 = pre ? *pre : packed8_matrix{};
   ForwardPlan f;
-  const int rc = plan_forward(x, &f);
+  const int rc = plan_forward(x, pre ? &p8 : nullptr, &f);
   return rc != GEMM_F16F32_OK ? rc : f.q.w_bytes;
 }
+int64_t linear_forward_workspace(const linear_forward_args* args) {
+  return linear_forward_packed_workspace(args, nullptr);
+}
 
-int linear_forward(const linear_forward_args* args) {
+int linear_forward(const linear_forward_args* args) { return linear_forward_packed(args, nullptr); }
+
+int linear_forward_packed(const linear_forward_args* args, const packed8_matrix* pre) {
   if (args == nullptr) return GEMM_F16F32_ERR_NULL;
   linear_forward_args x = *args;
+  packed8_matrix p8 = pre ? *pre : packed8_matrix{};
   ForwardPlan f;
-  int rc = plan_forward(x, &f);
+  int rc = plan_forward(x, pre ? &p8 : nullptr, &f);
   if (rc != GEMM_F16F32_OK || f.q.parts == 0) return rc;
   rc = check_workspace(x.workspace, x.workspace_bytes, f.q.w_bytes);
   if (rc != GEMM_F16F32_OK) return rc;
@@ -585,14 +845,19 @@ int linear_forward(const linear_forward_args* args) {
                         region(x.residual, x.m, x.n, x.residual_row, 2),
                         operand_region(f.a, x.m, x.k, x.type), operand_region(f.b, x.n, x.k, x.type),
                         region(x.bias, 1, x.n, x.n, 2), region(x.scale_a, 1, x.m, x.m, 4),
-                        region(x.scale_b, 1, x.n, x.n, 4)};
-    if (conflict(&w, 1, o, 8)) return GEMM_F16F32_ERR_OVERLAP;
+                        region(x.scale_b, 1, x.n, x.n, 4), values_region(p8, x.m, x.n),
+                        scale_region(p8, x.m, x.n)};
+    if (conflict(&w, 1, o, 10)) return GEMM_F16F32_ERR_OVERLAP;
   }
   LinArgs p = product(x.type, x.k, f.a, f.b);
   p.out = (uint16_t*)x.out;
   p.ldo = x.out_row;
   p.pre = (uint16_t*)x.pre;
   p.ldp = x.pre_row;
+  p.pre8 = (uint8_t*)p8.values;
+  p.ldp8 = p8.values_row;
+  p.pre8_scale = (uint8_t*)p8.scale;
+  p.ldps = p8.scale_row;
   p.res = (const uint16_t*)x.residual;
   p.ldr = x.residual_row;
   p.bias = (const uint16_t*)x.bias;
@@ -603,22 +868,33 @@ int linear_forward(const linear_forward_args* args) {
   return launch(x.type, f.q, p, x.workspace, x.stream);
 }
 
-int64_t linear_backward_workspace(const linear_backward_args* args) {
+int64_t linear_backward_packed_workspace(const linear_backward_args* args,
+                                         const linear_kept* kept) {
   if (args == nullptr) return GEMM_F16F32_ERR_NULL;
   linear_backward_args x = *args;
+  linear_kept k8 = kept ? *kept : linear_kept{};
   BackwardPlan f;
-  const int rc = plan_backward(x, &f);
-  return rc != GEMM_F16F32_OK ? rc : f.dpre_bytes + f.part_bytes + f.w_bytes;
+  const int rc = plan_backward(x, &k8, &f);
+  return rc != GEMM_F16F32_OK ? rc : f.bytes();
+}
+int64_t linear_backward_workspace(const linear_backward_args* args) {
+  return linear_backward_packed_workspace(args, nullptr);
 }
 
 int linear_backward(const linear_backward_args* args) {
+  return linear_backward_packed(args, nullptr);
+}
+
+int linear_backward_packed(const linear_backward_args* args, const linear_kept* kept) {
   if (args == nullptr) return GEMM_F16F32_ERR_NULL;
   linear_backward_args x = *args;
+  linear_kept k8 = kept ? *kept : linear_kept{};
   BackwardPlan f;
-  int rc = plan_backward(x, &f);
+  int rc = plan_backward(x, &k8, &f);
   if (rc != GEMM_F16F32_OK) return rc;
   const bool act = x.activation != LINEAR_ACT_NONE;
-  const int64_t need = f.dpre_bytes + f.part_bytes + f.w_bytes;
+  const bool pre8 = act && k8.pre.values != nullptr;
+  const int64_t need = f.bytes();
   rc = check_workspace(x.workspace, x.workspace_bytes, need);
   if (rc != GEMM_F16F32_OK) return rc;
   if (need > 0) {
@@ -626,10 +902,15 @@ int linear_backward(const linear_backward_args* args) {
     const Region o[] = {region(x.dc, x.m, x.n, x.dc_row, 2),
                         region(act ? x.pre : nullptr, x.m, x.n, x.pre_row, 2),
                         region(x.da, x.m, x.k, x.da_row, 2), region(x.dbias, 1, x.n, x.n, 2),
-                        operand_region(f.a, x.k, x.m, x.type), operand_region(f.b, x.k, x.n, x.type),
+                        f.a_bytes ? Region{} : operand_region(f.a, x.k, x.m, x.type),
+                        operand_region(f.b, x.k, x.n, x.type),
                         f.db_cols ? region(x.db, x.n, x.k, x.db_col, 2)
-                                  : region(x.db, x.k, x.n, x.db_row, 2)};
-    if (conflict(&w, 1, o, 7)) return GEMM_F16F32_ERR_OVERLAP;
+                                  : region(x.db, x.k, x.n, x.db_row, 2),
+                        values_region(k8.a, x.m, x.k), scale_region(k8.a, x.m, x.k),
+                        region(pre8 ? k8.pre.values : nullptr, x.m, x.n, k8.pre.values_row, 1),
+                        region(pre8 ? k8.pre.scale : nullptr, x.m, cdiv(x.n, kBlock),
+                               k8.pre.scale_row, 1)};
+    if (conflict(&w, 1, o, 11)) return GEMM_F16F32_ERR_OVERLAP;
   }
   const bool bf = x.type == LINEAR_NORM_BF16;
   const hipStream_t s = (hipStream_t)x.stream;
@@ -643,8 +924,15 @@ int linear_backward(const linear_backward_args* args) {
     d.dc = (const uint16_t*)x.dc;
     d.dc_row = x.dc_row;
     if (act) {
-      d.pre = (const uint16_t*)x.pre;
-      d.pre_row = x.pre_row;
+      if (pre8) {
+        d.pre8 = (const uint8_t*)k8.pre.values;
+        d.pre8_row = k8.pre.values_row;
+        d.pre8_scale = (const uint8_t*)k8.pre.scale;
+        d.ps_row = k8.pre.scale_row;
+      } else {
+        d.pre = (const uint16_t*)x.pre;
+        d.pre_row = x.pre_row;
+      }
       d.dpre = (uint16_t*)ws;
       d.dpre_row = f.ldd;
       dpre = ws;
@@ -665,12 +953,17 @@ int linear_backward(const linear_backward_args* args) {
   }
   if (last && !f.pair) {
     if (bf)
-      launch_sum<lk::kBF16>(part, f.row_blocks, x.n, x.dbias, s);
+      launch_sum<lk::kBF16>(part, f.row_blocks, x.n, x.dbias, nullptr, s);
     else
-      launch_sum<lk::kF16>(part, f.row_blocks, x.n, x.dbias, s);
+      launch_sum<lk::kF16>(part, f.row_blocks, x.n, x.dbias, nullptr, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
-  void* const W = ws ? ws + f.dpre_bytes + f.part_bytes : nullptr;
+  if (f.a_bytes > 0) {
+    f.a.p = ws + f.dpre_bytes + f.part_bytes;
+    rc = unpack_rows(x.type, x.m, x.k, k8.a, k8.a_activation, (void*)f.a.p, f.lda, s);
+    if (rc != GEMM_F16F32_OK) return rc;
+  }
+  void* const W = ws ? ws + f.dpre_bytes + f.part_bytes + f.a_bytes : nullptr;
   LinArgs da = {}, db = {};
   const int64_t ldd = act && !f.small ? f.ldd : x.dc_row;
   if (f.qa.parts > 0) {
@@ -707,122 +1000,148 @@ int linear_backward(const linear_backward_args* args) {
 
 int rms_norm_forward(const rms_norm_forward_args* args) {
   if (args == nullptr) return GEMM_F16F32_ERR_NULL;
-  rms_norm_forward_args x = *args;
-  int rc = check_norm(x.rows, x.dim, x.type);
-  if (rc != GEMM_F16F32_OK) return rc;
-  const bool q8 = x.out_type == LINEAR_NORM_E4M3;
-  if ((!q8 && x.out_type != x.type) || !(x.eps >= 0.0) || (x.scale && !q8))
-    return GEMM_F16F32_ERR_OPTS;
-  if (x.rows == 0) return GEMM_F16F32_OK;
-  rc = check_rows(x.x, x.rows, x.dim, &x.x_row, 2, true);
-  if (rc == 0) rc = check_rows(x.residual, x.rows, x.dim, &x.residual_row, 2, false);
-  if (rc == 0) rc = check_rows(x.y, x.rows, x.dim, &x.y_row, q8 ? 1 : 2, true);
-  if (rc == 0) rc = check_rows(x.h, x.rows, x.dim, &x.h_row, 2, x.residual != nullptr);
-  if (rc != 0) return rc;
-  if (x.weight == nullptr || (q8 && x.scale == nullptr)) return GEMM_F16F32_ERR_NULL;
-  if (((uintptr_t)x.weight & 1) || (((uintptr_t)x.scale | (uintptr_t)x.rstd) & 3))
-    return GEMM_F16F32_ERR_OPTS;
-  const Region rx = region(x.x, x.rows, x.dim, x.x_row, 2);
-  const Region rr = region(x.residual, x.rows, x.dim, x.residual_row, 2);
-  const Region rh = region(x.h, x.rows, x.dim, x.h_row, 2);
-  const Region w[] = {region(x.y, x.rows, x.dim, x.y_row, q8 ? 1 : 2),
-                      region(x.scale, 1, x.rows, x.rows, 4), region(x.rstd, 1, x.rows, x.rows, 4),
-                      rh};
-  const Region r[] = {rx, rr, region(x.weight, 1, x.dim, x.dim, 2)};
-  if (conflict(w, 3, r, 3) || conflict(w, 4, r + 2, 1)) return GEMM_F16F32_ERR_OVERLAP;
-  if ((!(x.h == x.x && x.h_row == x.x_row) && overlap(rh, rx)) ||
-      (!(x.h == x.residual && x.h_row == x.residual_row) && overlap(rh, rr)))
-    return GEMM_F16F32_ERR_OVERLAP;
-  const int64_t ys = q8 ? 1 : 2;
-  for (int64_t r0 = 0; r0 < x.rows; r0 += kRowsPerLaunch) {
-    nk::NormArgs p = {};
-    p.x = (const uint16_t*)x.x + r0 * x.x_row;
-    p.x_row = x.x_row;
-    if (x.residual) p.res = (const uint16_t*)x.residual + r0 * x.residual_row;
-    p.res_row = x.residual_row;
-    p.weight = (const uint16_t*)x.weight;
-    p.y = (char*)x.y + ys * r0 * x.y_row;
-    p.y_row = x.y_row;
-    if (x.scale) p.scale = x.scale + r0;
-    if (x.h) p.h = (uint16_t*)x.h + r0 * x.h_row;
-    p.h_row = x.h_row;
-    if (x.rstd) p.rstd = x.rstd + r0;
-    p.rows = (int32_t)(x.rows - r0 < kRowsPerLaunch ? x.rows - r0 : kRowsPerLaunch);
-    p.dim = (int32_t)x.dim;
-    p.eps = (float)x.eps;
-    p.inv_dim = (float)(1.0 / (double)x.dim);
-    const hipStream_t s = (hipStream_t)x.stream;
-    if (x.type == LINEAR_NORM_BF16)
-      q8 ? norm_forward<lk::kBF16, true>(p, s) : norm_forward<lk::kBF16, false>(p, s);
-    else
-      q8 ? norm_forward<lk::kF16, true>(p, s) : norm_forward<lk::kF16, false>(p, s);
-    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
-  }
-  return GEMM_F16F32_OK;
+  const rms_norm_forward_args& a = *args;
+  layer_norm_forward_args x = {};
+  x.rows = a.rows;
+  x.dim = a.dim;
+  x.type = a.type;
+  x.out_type = a.out_type;
+  x.x = a.x;
+  x.x_row = a.x_row;
+  x.residual = a.residual;
+  x.residual_row = a.residual_row;
+  x.weight = a.weight;
+  x.y = a.y;
+  x.y_row = a.y_row;
+  x.scale = a.scale;
+  x.h = a.h;
+  x.h_row = a.h_row;
+  x.rstd = a.rstd;
+  x.eps = a.eps;
+  x.stream = a.stream;
+  return norm_forward_call(x, false);
+}
+
+int layer_norm_forward(const layer_norm_forward_args* args) {
+  return args == nullptr ? (int)GEMM_F16F32_ERR_NULL : norm_forward_call(*args, true);
 }
 
 int64_t rms_norm_backward_workspace(const rms_norm_backward_args* args) {
   if (args == nullptr) return GEMM_F16F32_ERR_NULL;
   const int rc = check_norm(args->rows, args->dim, args->type);
-  return rc != GEMM_F16F32_OK ? rc : norm_backward_bytes(*args);
+  return rc != GEMM_F16F32_OK ? rc
+                              : (args->dweight != nullptr) * norm_part_bytes(args->rows, args->dim);
 }
 
 int rms_norm_backward(const rms_norm_backward_args* args) {
   if (args == nullptr) return GEMM_F16F32_ERR_NULL;
-  rms_norm_backward_args x = *args;
+  const rms_norm_backward_args& a = *args;
+  layer_norm_backward_args x = {};
+  x.rows = a.rows;
+  x.dim = a.dim;
+  x.type = a.type;
+  x.dy = a.dy;
+  x.dy_row = a.dy_row;
+  x.h = a.h;
+  x.h_row = a.h_row;
+  x.weight = a.weight;
+  x.rstd = a.rstd;
+  x.dh = a.dh;
+  x.dh_row = a.dh_row;
+  x.dx = a.dx;
+  x.dx_row = a.dx_row;
+  x.dweight = a.dweight;
+  x.workspace = a.workspace;
+  x.workspace_bytes = a.workspace_bytes;
+  x.stream = a.stream;
+  return norm_backward_call(x, false);
+}
+
+int64_t layer_norm_backward_workspace(const layer_norm_backward_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  const int rc = check_norm(args->rows, args->dim, args->type);
+  return rc != GEMM_F16F32_OK ? rc : norm_backward_bytes(*args);
+}
+
+int layer_norm_backward(const layer_norm_backward_args* args) {
+  return args == nullptr ? (int)GEMM_F16F32_ERR_NULL : norm_backward_call(*args, true);
+}
+
+int quantize_rows(const quantize_rows_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  quantize_rows_args x = *args;
   int rc = check_norm(x.rows, x.dim, x.type);
-  if (rc == 0) rc = check_rows(x.dy, x.rows, x.dim, &x.dy_row, 2, true);
-  if (rc == 0) rc = check_rows(x.h, x.rows, x.dim, &x.h_row, 2, true);
-  if (rc == 0) rc = check_rows(x.dh, x.rows, x.dim, &x.dh_row, 2, false);
-  if (rc == 0) rc = check_rows(x.dx, x.rows, x.dim, &x.dx_row, 2, true);
-  if (rc != 0) return rc;
-  if (x.rows > 0 && (x.weight == nullptr || x.rstd == nullptr)) return GEMM_F16F32_ERR_NULL;
-  if ((((uintptr_t)x.weight | (uintptr_t)x.dweight) & 1) || ((uintptr_t)x.rstd & 3))
-    return GEMM_F16F32_ERR_OPTS;
-  const int64_t need = norm_backward_bytes(x);
-  rc = check_workspace(x.workspace, x.workspace_bytes, need);
   if (rc != GEMM_F16F32_OK) return rc;
-  const Region rdx = region(x.dx, x.rows, x.dim, x.dx_row, 2);
-  const Region rdy = region(x.dy, x.rows, x.dim, x.dy_row, 2);
-  const Region rdh = region(x.dh, x.rows, x.dim, x.dh_row, 2);
-  const Region w[] = {region(x.dweight, 1, x.dim, x.dim, 2), {x.workspace, (uint64_t)need}, rdx};
-  const Region r[] = {region(x.h, x.rows, x.dim, x.h_row, 2),
-                      region(x.weight, 1, x.dim, x.dim, 2), region(x.rstd, 1, x.rows, x.rows, 4),
-                      rdy, rdh};
-  if (conflict(w, 2, r, 5) || conflict(w, 3, r, 3)) return GEMM_F16F32_ERR_OVERLAP;
-  if ((!(x.dx == x.dy && x.dx_row == x.dy_row) && overlap(rdx, rdy)) ||
-      (!(x.dx == x.dh && x.dx_row == x.dh_row) && overlap(rdx, rdh)))
-    return GEMM_F16F32_ERR_OVERLAP;
-  const hipStream_t s = (hipStream_t)x.stream;
-  const bool bf = x.type == LINEAR_NORM_BF16;
-  const int groups = backward_groups(x.rows, x.dim);
-  if (groups > 0) {
-    nk::NormBwdArgs p = {};
-    p.dy = (const uint16_t*)x.dy;
-    p.dy_row = x.dy_row;
-    p.h = (const uint16_t*)x.h;
-    p.h_row = x.h_row;
-    p.weight = (const uint16_t*)x.weight;
-    p.rstd = x.rstd;
-    p.dh = (const uint16_t*)x.dh;
-    p.dh_row = x.dh_row;
-    p.dx = (uint16_t*)x.dx;
-    p.dx_row = x.dx_row;
-    const bool sums = backward_sums(x.rows, x.dim);
-    p.part = x.dweight && sums ? (float*)x.workspace : nullptr;
-    p.dweight = sums ? nullptr : (uint16_t*)x.dweight;
-    p.rows = (int32_t)x.rows;
+  if (!is8(x.out_type)) return GEMM_F16F32_ERR_OPTS;
+  if (x.rows == 0) return GEMM_F16F32_OK;
+  rc = check_rows(x.x, x.rows, x.dim, &x.x_row, 2, true);
+  if (rc == 0) rc = check_rows(x.values, x.rows, x.dim, &x.values_row, 1, true);
+  if (rc != 0) return rc;
+  if (x.scale == nullptr) return GEMM_F16F32_ERR_NULL;
+  if ((uintptr_t)x.scale & 3) return GEMM_F16F32_ERR_OPTS;
+  const Region w[] = {region(x.values, x.rows, x.dim, x.values_row, 1),
+                      region(x.scale, 1, x.rows, x.rows, 4)};
+  const Region r = region(x.x, x.rows, x.dim, x.x_row, 2);
+  if (conflict(w, 2, &r, 1)) return GEMM_F16F32_ERR_OVERLAP;
+  for (int64_t r0 = 0; r0 < x.rows; r0 += kRowsPerLaunch) {
+    const int64_t n = x.rows - r0 < kRowsPerLaunch ? x.rows - r0 : kRowsPerLaunch;
+    nk::QuantizeArgs p = {};
+    p.x = (const uint16_t*)x.x + r0 * x.x_row;
+    p.x_row = x.x_row;
+    p.y = (uint8_t*)x.values + r0 * x.values_row;
+    p.y_row = x.values_row;
+    p.scale = x.scale + r0;
     p.dim = (int32_t)x.dim;
-    p.inv_dim = (float)(1.0 / (double)x.dim);
-    bf ? norm_backward<lk::kBF16>(p, groups, s) : norm_backward<lk::kF16>(p, groups, s);
-    if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
-  }
-  if (x.dweight && backward_sums(x.rows, x.dim)) {
-    bf ? launch_sum<lk::kBF16>((const float*)x.workspace, groups, x.dim, x.dweight, s)
-       : launch_sum<lk::kF16>((const float*)x.workspace, groups, x.dim, x.dweight, s);
+    const hipStream_t s = (hipStream_t)x.stream;
+    const bool bf = x.type == LINEAR_NORM_BF16;
+    if (x.out_type == LINEAR_NORM_I8)
+      bf ? quantize<lk::kBF16, nk::kOutI8>(p, n, s) : quantize<lk::kF16, nk::kOutI8>(p, n, s);
+    else
+      bf ? quantize<lk::kBF16, nk::kOutE4M3>(p, n, s) : quantize<lk::kF16, nk::kOutE4M3>(p, n, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   return GEMM_F16F32_OK;
+}
+
+int pack8(const pack8_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  pack8_args x = *args;
+  if (bad_dim(x.rows) || bad_dim(x.dim)) return GEMM_F16F32_ERR_DIM;
+  if (!is16(x.type)) return GEMM_F16F32_ERR_OPTS;
+  if (x.rows == 0 || x.dim == 0) return GEMM_F16F32_OK;
+  int rc = check_rows(x.x, x.rows, x.dim, &x.x_row, 2, true);
+  if (rc == 0) rc = check_packed(&x.out, x.rows, x.dim);
+  if (rc != 0) return rc;
+  const Region w[] = {values_region(x.out, x.rows, x.dim), scale_region(x.out, x.rows, x.dim)};
+  const Region r = region(x.x, x.rows, x.dim, x.x_row, 2);
+  if (conflict(w, 2, &r, 1)) return GEMM_F16F32_ERR_OVERLAP;
+  nk::PackArgs a = pack_args(x.dim, x.out);
+  a.x = (const uint16_t*)x.x;
+  a.x_row = x.x_row;
+  const hipStream_t s = (hipStream_t)x.stream;
+  return pack_launches(a, x.rows, [&](const nk::PackArgs& b, dim3 grid) {
+    if (x.type == LINEAR_NORM_BF16)
+      hipLaunchKernelGGL((nk::pack8<lk::kBF16>), grid, dim3(256), 0, s, b);
+    else
+      hipLaunchKernelGGL((nk::pack8<lk::kF16>), grid, dim3(256), 0, s, b);
+  });
+}
+
+int unpack8(const unpack8_args* args) {
+  if (args == nullptr) return GEMM_F16F32_ERR_NULL;
+  unpack8_args x = *args;
+  if (bad_dim(x.rows) || bad_dim(x.dim)) return GEMM_F16F32_ERR_DIM;
+  if (!is16(x.type) || x.activation < LINEAR_ACT_NONE || x.activation > LINEAR_ACT_SILU)
+    return GEMM_F16F32_ERR_OPTS;
+  if (x.rows == 0 || x.dim == 0) return GEMM_F16F32_OK;
+  int rc = check_packed(&x.in, x.rows, x.dim);
+  if (rc == 0) rc = check_rows(x.y, x.rows, x.dim, &x.y_row, 2, true);
+  if (rc != 0) return rc;
+  const Region w = region(x.y, x.rows, x.dim, x.y_row, 2);
+  const Region r[] = {values_region(x.in, x.rows, x.dim), scale_region(x.in, x.rows, x.dim)};
+  if (conflict(&w, 1, r, 2)) return GEMM_F16F32_ERR_OVERLAP;
+  return unpack_rows(x.type, x.rows, x.dim, x.in, x.activation, x.y, x.y_row,
+                     (hipStream_t)x.stream);
 }
 
 }  // extern "C"

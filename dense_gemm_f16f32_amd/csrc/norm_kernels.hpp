@@ -1,5 +1,6 @@
-// Device code of the root-mean-square norm, its backward pass, and the element-wise part of the
-// linear layer's backward pass.  All of them move each element once; HBM bounds them.
+// Device code of the root-mean-square norm and the layer norm, their backward passes, rows in 8 bits,
+// and the element-wise part of the linear layer's backward pass.  All of them move each element
+// once; HBM bounds them.
 #pragma once
 
 #include "linear_kernels.hpp"
@@ -19,6 +20,29 @@ __device__ __forceinline__ float group_sum(float v, float* s) {
     v = 0.f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) v += s[i];
+  }
+  return v;
+}
+// Two sums at once; `s` holds 2 NW floats.
+template <int NW>
+__device__ __forceinline__ float2v group_sum2(float2v v, float* s) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    v[0] += __shfl_xor(v[0], d);
+    v[1] += __shfl_xor(v[1], d);
+  }
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 63) == 0) {
+      s[2 * (threadIdx.x >> 6)] = v[0];
+      s[2 * (threadIdx.x >> 6) + 1] = v[1];
+    }
+    __syncthreads();
+    v = float2v{0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      v[0] += s[2 * i];
+      v[1] += s[2 * i + 1];
+    }
   }
   return v;
 }
@@ -43,9 +67,11 @@ struct NormArgs {
   const uint16_t* x;
   const uint16_t* res;
   const uint16_t* weight;
+  const uint16_t* bias;   // layer norm only; may be null
   void* y;
   float* scale;
   uint16_t* h;
+  float* mean;   // layer norm only
   float* rstd;
   int64_t x_row, res_row, y_row, h_row;
   int32_t rows, dim;
@@ -92,30 +118,65 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[8], Divisor d) {
   o.y = (uint32_t)hi;
   return o;
 }
-struct __attribute__((packed)) Bytes8 {
-  uint32_t x, y;
-};
-__device__ __forceinline__ void store_e4m3x8(uint8_t* p, const float (&v)[8], Divisor d, int n) {
-  const uint2 q = to_e4m3x8(v, d);
-  if (n >= 8) {
-    *(Bytes8*)p = Bytes8{q.x, q.y};
-  } else {
+// scale of a row in int8: the largest magnitude over 127 (1 for a row of zeros), the quotient in
+// fp32.  The integers cannot hold a NaN: a row with one, or with an infinity, has a scale that
+// makes every product with it NaN.
+__device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return __builtin_nanf("");
+  const float amax = __builtin_bit_cast(float, amax_bits);
+  return amax > 0.f ? fmaxf(amax / 127.f, 1.17549435e-38f) : 1.f;
+}
+// 8 quotients to integers, nearest, ties to even (the addition rounds, and leaves the integer in the
+// low bits).  The clamp catches the scale's own rounding, and turns NaN into a number.
+__device__ __forceinline__ uint2 to_int8x8(const float (&v)[8], Divisor d) {
+  uint32_t q[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) p[e] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
-  }
+  for (int e = 0; e < 8; ++e)
+    q[e] = __builtin_bit_cast(
+        uint32_t, __builtin_amdgcn_fmed3f(quotient(v[e], d), -127.f, 127.f) + 12582912.f);
+  auto bytes = [&](int i) __attribute__((always_inline)) {
+    const uint32_t x = __builtin_amdgcn_perm(q[i + 1], q[i], 0x0C0C0400u);
+    const uint32_t y = __builtin_amdgcn_perm(q[i + 3], q[i + 2], 0x0C0C0400u);
+    return x | (y << 16);
+  };
+  return uint2{bytes(0), bytes(4)};
 }
 
-// One pass: the sum of squares, the 8-bit scale and y come from the row in registers.  HBM bounds
+// What rows are stored as: their own 16-bit type, or 8 bits with a scale a row.
+enum { kOut16, kOutE4M3, kOutI8 };
+template <int OUT>
+__device__ __forceinline__ float row_scale(uint32_t amax_bits) {
+  return OUT == kOutI8 ? int8_scale(amax_bits) : e4m3_scale(amax_bits);
+}
+template <int OUT>
+__device__ __forceinline__ void store_row8(uint8_t* p, const float (&v)[8], Divisor d, int n) {
+  const uint2 q = OUT == kOutI8 ? to_int8x8(v, d) : to_e4m3x8(v, d);
+  store_bytes8(p, q.x, q.y, n);
+}
+__device__ __forceinline__ uint32_t max_bits8(const float (&v)[8], uint32_t m) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = abs_bits(v[e]);
+    m = m > b ? m : b;
+  }
+  return m;
+}
+
+// One pass: the row's statistics, the 8-bit scale and y come from the row in registers.  HBM bounds
 // it: 8192 x 8192 bf16 with residual to e4m3 88 us (5.3 TB/s), 4095 x 4093 f16 29 us (4.6 TB/s; 24.5
 // where the rows are partly in the last-level cache).
 // One row a workgroup of 64 NW threads, 8 columns a thread at a time.  C > 0: rows of at most
 // 512 NW C columns, held in registers.  C == 0: longer rows, read again for each step that
 // needs them.
-template <int TY, bool Q8, int NW, int C>
-__global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
+//
+// LN (the layer norm): the mean first, then the sums of the differences from it and of their
+// squares, in one reduction.  The sum of the differences would be 0 but for the mean's rounding; its
+// mean d corrects both statistics, mean += d and var = mean(c^2) - d^2, so that rows far from 0
+// keep their deviation's bits.  (A mean of squares less the mean's square would lose them.)
+template <int TY, int OUT, bool LN, int NW, int C>
+__global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   const bool back = p.dim >= 8;
-  __shared__ float ssum[NW];
+  __shared__ float ssum[2 * NW];
   __shared__ uint32_t smax[NW];
   constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
   const int64_t row = blockIdx.x;
@@ -124,7 +185,8 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
   uint16_t* const h = p.h ? p.h + row * p.h_row : nullptr;
   const int c0 = threadIdx.x * 8;
   const int steps = C > 0 ? C : (p.dim - 1) / STEP + 1;   // dim > 0; dim + STEP need not fit
-  float hv[CR][8], wv[CR][8];
+  float hv[CR][8], wv[CR][8], bv[CR][8];
+  float mean = 0.f;
   auto load_h = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
     load8(v, x + col, p.dim - col, TY, back);
     if (res) {
@@ -134,76 +196,127 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
       for (int e = 0; e < 8; ++e) v[e] += r[e];
     }
   };
-  float sum = 0.f;
+  auto load_bias = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
+    if (LN && p.bias) {
+      load8(v, p.bias + col, p.dim - col, TY, back);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+  };
+  // differences from the mean; columns past dim stay 0
+  auto centre = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
+    if constexpr (LN) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? v[e] - mean : 0.f;
+    }
+  };
+  float2v sum = {0.f, 0.f};   // of the values or differences (layer norm), of their squares
+  auto add = [&](const float (&v)[8], float unit) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = v[e] * unit;
+      if constexpr (LN) sum[0] += u;
+      sum[1] += u * u;
+    }
+  };
+  // mean of the squares about the mean, with what is added to mean, in units of 1 / unit
+  float shift = 0.f;
+  auto moments = [&](float unit) __attribute__((always_inline)) {
+    if constexpr (LN) {
+      const float2v s = group_sum2<NW>(sum, ssum);
+      shift = s[0] * p.inv_dim;
+      const float var = s[1] * p.inv_dim - shift * shift;
+      return (var < 0.f ? 0.f : var) + p.eps * unit * unit;   // NaN stays
+    } else {
+      return group_sum<NW>(sum[1], ssum) * p.inv_dim + p.eps * unit * unit;
+    }
+  };
   if constexpr (C > 0) {
 #pragma unroll
     for (int i = 0; i < C; ++i) load_h(c0 + i * STEP, hv[i]);
 #pragma unroll
     for (int i = 0; i < C; ++i) load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY, back);
+    if constexpr (LN) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) load_bias(c0 + i * STEP, bv[i]);
+    }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = c0 + i * STEP;
       if (h && col < p.dim) store8(h + col, hv[i], p.dim - col, TY);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += hv[i][e] * hv[i][e];
-    }
-  } else {
-    for (int i = 0; i < steps; ++i) {
-      load_h(c0 + i * STEP, hv[0]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += hv[0][e] * hv[0][e];
     }
   }
-  float square = group_sum<NW>(sum, ssum) * p.inv_dim + p.eps, unit = 1.f;
-  // Squares outside fp32's range (bf16 rows above 1e19, or below 1e-9 with a tiny eps) are summed
-  // again in units that bring them into it; every thread of the row holds the same sum.
-  if (square < 0x1p-60f || square == __builtin_inff()) {
-    unit = square < 1.f ? 0x1p64f : 0x1p-96f;
-    if constexpr (NW > 1) __syncthreads();   // the first sum has been read
-    sum = 0.f;
+  if constexpr (LN) {
+    // terms of the mean, not of the sum: it cannot leave fp32's range where the values have not
 #pragma unroll CR
     for (int i = 0; i < steps; ++i) {
       if constexpr (C == 0) load_h(c0 + i * STEP, hv[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = hv[C > 0 ? i : 0][e] * unit;
-        sum += v * v;
-      }
+      for (int e = 0; e < 8; ++e) mean += hv[C > 0 ? i : 0][e] * p.inv_dim;
     }
-    square = group_sum<NW>(sum, ssum) * p.inv_dim + p.eps * unit * unit;
+    mean = group_sum<NW>(mean, ssum);
+    if constexpr (NW > 1) __syncthreads();   // it has been read
+  }
+#pragma unroll CR
+  for (int i = 0; i < steps; ++i) {
+    if constexpr (C == 0) load_h(c0 + i * STEP, hv[0]);
+    centre(c0 + i * STEP, hv[C > 0 ? i : 0]);
+    add(hv[C > 0 ? i : 0], 1.f);
+  }
+  float square = moments(1.f), unit = 1.f;
+  // Squares outside fp32's range (bf16 rows above 1e19, or below 1e-9 with a tiny eps) are summed
+  // again in units that bring them into it; every thread of the row holds the same sum.  (The layer
+  // norm's infinite sum less its infinite correction is NaN.)
+  if (square < 0x1p-60f || square == __builtin_inff() || (LN && square != square)) {
+    unit = square < 1.f ? 0x1p64f : 0x1p-96f;
+    if constexpr (NW > 1) __syncthreads();   // the first sum has been read
+    sum = float2v{0.f, 0.f};
+#pragma unroll CR
+    for (int i = 0; i < steps; ++i) {
+      if constexpr (C == 0) {
+        load_h(c0 + i * STEP, hv[0]);
+        centre(c0 + i * STEP, hv[0]);
+      }
+      add(hv[C > 0 ? i : 0], unit);
+    }
+    square = moments(unit);
+    shift /= unit;
   }
   const float rstd = unit / sqrtf(square);
-  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  if (threadIdx.x == 0) {
+    if (p.rstd) p.rstd[row] = rstd;
+    if (LN && p.mean) p.mean[row] = mean + shift;
+  }
   // y of step i
   auto norm = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
     const int col = c0 + i * STEP;
-    float w[8];
+    float w[8], b[8];
     if constexpr (C == 0) {
       load_h(col, v);
+      centre(col, v);
       load8(w, p.weight + col, p.dim - col, TY, back);
+      if constexpr (LN) load_bias(col, b);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if constexpr (C > 0)
-        v[e] = hv[i][e] * rstd * wv[i][e];
+      const float u = C > 0 ? hv[i][e] : v[e], g = C > 0 ? wv[i][e] : w[e];
+      if constexpr (LN)
+        v[e] = (u - shift) * rstd * g + (C > 0 ? bv[i][e] : b[e]);
       else
-        v[e] = v[e] * rstd * w[e];
+        v[e] = u * rstd * g;
     }
   };
   Divisor by = {1.f, 1.f};
-  if constexpr (Q8) {
+  if constexpr (OUT != kOut16) {
     uint32_t m = 0u;
 #pragma unroll CR
     for (int i = 0; i < steps; ++i) {
       float v[8];
       norm(i, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = abs_bits(v[e]);   // columns past dim are 0 (their weight reads as 0)
-        m = m > b ? m : b;
-      }
+      m = max_bits8(v, m);   // columns past dim are 0 (their weight and bias read as 0)
     }
-    const float scale = e4m3_scale(group_max<NW>(m, smax));
+    const float scale = row_scale<OUT>(group_max<NW>(m, smax));
     if (threadIdx.x == 0) p.scale[row] = scale;
     by = divisor(scale);
   }
@@ -213,8 +326,8 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
     if (col >= p.dim) break;
     float v[8];
     norm(i, v);
-    if constexpr (Q8)
-      store_e4m3x8((uint8_t*)p.y + row * p.y_row + col, v, by, p.dim - col);
+    if constexpr (OUT != kOut16)
+      store_row8<OUT>((uint8_t*)p.y + row * p.y_row + col, v, by, p.dim - col);
     else
       store8((uint16_t*)p.y + row * p.y_row + col, v, p.dim - col, TY);
     // h may be x's or the residual's memory: without registers it is written last
@@ -227,15 +340,60 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_fwd(NormArgs p) {
   }
 }
 
+// Rows in 8 bits with a scale a row, as the norm's: one row a workgroup.
+struct QuantizeArgs {
+  const uint16_t* x;
+  uint8_t* y;
+  float* scale;
+  int64_t x_row, y_row;
+  int32_t dim;
+};
+template <int TY, int OUT, int NW, int C>
+__global__ void __launch_bounds__(64 * NW) quantize_rows(QuantizeArgs p) {
+  const bool back = p.dim >= 8;
+  __shared__ uint32_t smax[NW];
+  constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
+  const int64_t row = blockIdx.x;
+  const uint16_t* const x = p.x + row * p.x_row;
+  const int c0 = threadIdx.x * 8;
+  const int steps = C > 0 ? C : (p.dim - 1) / STEP + 1;
+  float xv[CR][8];
+  uint32_t m = 0u;
+#pragma unroll CR
+  for (int i = 0; i < steps; ++i) {
+    const int col = c0 + i * STEP;
+    load8(xv[C > 0 ? i : 0], x + col, p.dim - col, TY, back);
+    if constexpr (C == 0) m = max_bits8(xv[0], m);
+  }
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) m = max_bits8(xv[i], m);
+  }
+  const float scale = row_scale<OUT>(group_max<NW>(m, smax));
+  if (threadIdx.x == 0) p.scale[row] = scale;
+  const Divisor by = divisor(scale);
+#pragma unroll CR
+  for (int i = 0; i < steps; ++i) {
+    const int col = c0 + i * STEP;
+    if (col >= p.dim) break;
+    if constexpr (C == 0) load8(xv[0], x + col, p.dim - col, TY, back);
+    store_row8<OUT>(p.y + row * p.y_row + col, xv[C > 0 ? i : 0], by, p.dim - col);
+  }
+}
+
 struct NormBwdArgs {
   const uint16_t* dy;
   const uint16_t* h;
   const uint16_t* weight;
+  const float* mean;   // layer norm only
   const float* rstd;
   const uint16_t* dh;
   uint16_t* dx;
   uint16_t* dweight;
-  float* part;   // partial dweight sums of every workgroup; null: dweight itself, or nothing
+  uint16_t* dbias;   // layer norm only
+  // partial sums of every workgroup; null: dweight and dbias themselves, or nothing
+  float* part;
+  float* part_bias;
   int64_t dy_row, h_row, dh_row, dx_row;
   int32_t rows, dim;
   float inv_dim;
@@ -257,30 +415,42 @@ __device__ __forceinline__ void store_partial8(float* part, int groups, int grou
 // RW rows of at most 512 NW C columns at a time, NW waves each: workgroup b takes rows b RW ..,
 // (b + grid) RW .., ...; where registers allow, the next row's values are loaded before the
 // current row is worked on.  Each thread keeps its columns' dweight sums in registers; the
-// workgroup adds and writes them once.  Short rows (one wave each) go four to a workgroup.  HBM
+// workgroup adds and writes them once (LN, the layer norm: dbias' sums too).  Short rows (one wave each) go four to a workgroup.  HBM
 // bounds it: 8192 x 4096 bf16 50 us (5.4 TB/s of dy, h, dh and dx), and 5 for sum_partials; with the
 // rows partly in the last-level cache 41 us, and there without the loads ahead 70.
-template <int TY, int NW, int C, int RW>
-__global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
+template <int TY, bool LN, int NW, int C, int RW>
+__global__ void __launch_bounds__(64 * NW * RW) norm_bwd(NormBwdArgs p) {
   static_assert(NW == 1 || RW == 1, "rows of several waves share the workgroup's barrier");
   const bool back = p.dim >= 8;
-  __shared__ float ssum[2][NW];
-  constexpr int STEP = 512 * NW;
+  __shared__ float ssum[2][2 * NW];
+  constexpr int STEP = 512 * NW, CB = LN ? C : 1;
   const int c0 = (RW > 1 ? threadIdx.x & 63 : threadIdx.x) * 8;
   const int rw = RW > 1 ? threadIdx.x >> 6 : 0;
-  float wv[C][8], dw[C][8];
+  // With four steps of a row the layer norm's second set of sums leaves no registers for the
+  // weights in fp32, nor for the row's values across the sum: both are unpacked twice.
+  constexpr bool kTight = LN && C > 2;
+  float wv[kTight ? 1 : C][8], dw[C][8], db[CB][8];
+  u32x4 wr[kTight ? C : 1];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY, back);
+    if constexpr (kTight)
+      wr[i] = raw8(p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, back);
+    else
+      load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY, back);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+    if constexpr (LN) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) db[i][e] = 0.f;
+    }
   }
   struct Row {
     u32x4 d[C], h[C], r[C];   // dy, h, dh
-    float4v s;                // rstd first; a lone float's padding would be copied through memory
+    float4v s;                // rstd, mean; a lone float's padding would be copied through memory
   };
   auto load = [&](Row& q, int64_t row) __attribute__((always_inline)) {
     q.s[0] = p.rstd[row];
+    if constexpr (LN) q.s[1] = p.mean[row];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = c0 + i * STEP, n = p.dim - col;
@@ -298,12 +468,17 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
     if (!kAhead) load(cur, row);
     nxt = cur;
     if (kAhead && row + step < p.rows) load(nxt, row + step);
-    const float rstd = cur.s[0];
-    float sum = 0.f;
+    const float rstd = cur.s[0], mean = LN ? cur.s[1] : 0.f;
+    float2v sum = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float d[8], x[8];
       const int n = p.dim - c0 - i * STEP;
+      if constexpr (kTight) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" : "+v"(wr[i]));
+        unpack8(wv[0], wr[i], TY);
+      }
       cur.d[i] = raw8_shift(cur.d[i], n, back);
       cur.h[i] = raw8_shift(cur.h[i], n, back);
       cur.r[i] = raw8_shift(cur.r[i], n, back);
@@ -311,35 +486,61 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
       unpack8(x, cur.h[i], TY);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] *= rstd;
+        x[e] = LN ? (x[e] - mean) * rstd : x[e] * rstd;
         dw[i][e] += d[e] * x[e];
-        sum += d[e] * wv[i][e] * x[e];
+        if constexpr (LN) {
+          db[i][e] += d[e];
+          sum[1] += d[e] * wv[kTight ? 0 : i][e];
+        }
+        sum[0] += d[e] * wv[kTight ? 0 : i][e] * x[e];
       }
     }
     // two sets of sums in turn, so that one barrier a row is enough
-    const float mean = group_sum<NW>(sum, ssum[turn]) * p.inv_dim;
+    if constexpr (LN)
+      sum = group_sum2<NW>(sum, ssum[turn]);
+    else
+      sum[0] = group_sum<NW>(sum[0], ssum[turn]);
+    const float along = sum[0] * p.inv_dim, level = sum[1] * p.inv_dim;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = c0 + i * STEP;
       float d[8], x[8], r[8];
+      if constexpr (kTight) {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" : "+v"(cur.d[i]), "+v"(cur.h[i]), "+v"(wr[i]));
+        unpack8(wv[0], wr[i], TY);
+      }
       unpack8(d, cur.d[i], TY);
       unpack8(x, cur.h[i], TY);
       unpack8(r, cur.r[i], TY);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        r[e] += rstd * (d[e] * wv[i][e] - x[e] * rstd * mean);
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (LN)
+          r[e] += rstd * (d[e] * wv[kTight ? 0 : i][e] - level - (x[e] - mean) * rstd * along);
+        else
+          r[e] += rstd * (d[e] * wv[kTight ? 0 : i][e] - x[e] * rstd * along);
+      }
       if (col < p.dim) store8(p.dx + row * p.dx_row + col, r, p.dim - col, TY);
     }
     cur = nxt;
   }
-  if (p.part == nullptr && p.dweight == nullptr) return;
+  if (p.part == nullptr && p.dweight == nullptr &&
+      (!LN || (p.part_bias == nullptr && p.dbias == nullptr)))
+    return;
   if constexpr (RW > 1) {   // the other rows' sums, in their order
-    __shared__ float sdw[RW - 1][C * 512];
+    __shared__ float sdw[RW - 1][(C + (LN ? C : 0)) * 512];
     if (rw > 0) {
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sdw[rw - 1][(i * 8 + e) * 64 + (threadIdx.x & 63)] = dw[i][e];
+      if constexpr (LN) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            sdw[rw - 1][((C + i) * 8 + e) * 64 + (threadIdx.x & 63)] = db[i][e];
+      }
     }
     __syncthreads();
     if (rw > 0) return;
@@ -348,7 +549,10 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] += sdw[r][(i * 8 + e) * 64 + threadIdx.x];
+        for (int e = 0; e < 8; ++e) {
+          dw[i][e] += sdw[r][(i * 8 + e) * 64 + threadIdx.x];
+          if constexpr (LN) db[i][e] += sdw[r][((C + i) * 8 + e) * 64 + threadIdx.x];
+        }
   }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -356,22 +560,28 @@ __global__ void __launch_bounds__(64 * NW * RW) rms_norm_bwd(NormBwdArgs p) {
     if (col >= p.dim) continue;
     if (p.part != nullptr)
       store_partial8(p.part, gridDim.x, blockIdx.x, col, dw[i]);
-    else   // the only workgroup
+    else if (p.dweight != nullptr)   // the only workgroup
       store8(p.dweight + col, dw[i], p.dim - col, TY);
+    if constexpr (LN) {
+      if (p.part_bias != nullptr)
+        store_partial8(p.part_bias, gridDim.x, blockIdx.x, col, db[i]);
+      else if (p.dbias != nullptr)
+        store8(p.dbias + col, db[i], p.dim - col, TY);
+    }
   }
 }
 
-// Rows too long for registers: read twice, the dweight sums kept in the workgroup's
+// Rows too long for registers: read twice, the dweight and dbias sums kept in the workgroup's
 // part of the workspace.
-template <int TY, int NW>
-__global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
+template <int TY, bool LN, int NW>
+__global__ void __launch_bounds__(64 * NW) norm_bwd_long(NormBwdArgs p) {
   const bool back = p.dim >= 8;
-  __shared__ float ssum[2][NW];
+  __shared__ float ssum[2][2 * NW];
   constexpr int STEP = 512 * NW;
   const int c0 = threadIdx.x * 8;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    const float rstd = p.rstd[row];
+    const float rstd = p.rstd[row], mean = LN ? p.mean[row] : 0.f;
     auto load = [&](int col, float (&g)[8], float (&x)[8], float (&d)[8])
                     __attribute__((always_inline)) {
       const int n = p.dim - col;
@@ -381,17 +591,25 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
       load8(w, p.weight + col, n, TY, back);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] *= rstd;
+        x[e] = LN ? (x[e] - mean) * rstd : x[e] * rstd;
         g[e] = d[e] * w[e];
       }
     };
-    float g[8], x[8], d[8], sum = 0.f;
+    float g[8], x[8], d[8];
+    float2v sum = {0.f, 0.f};
     for (uint32_t col = c0; col < (uint32_t)p.dim; col += STEP) {
       load(col, g, x, d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += g[e] * x[e];
+      for (int e = 0; e < 8; ++e) {
+        sum[0] += g[e] * x[e];
+        if constexpr (LN) sum[1] += g[e];
+      }
     }
-    const float mean = group_sum<NW>(sum, ssum[turn]) * p.inv_dim;
+    if constexpr (LN)
+      sum = group_sum2<NW>(sum, ssum[turn]);
+    else
+      sum[0] = group_sum<NW>(sum[0], ssum[turn]);
+    const float along = sum[0] * p.inv_dim, level = sum[1] * p.inv_dim;
     for (uint32_t col = c0; col < (uint32_t)p.dim; col += STEP) {
       float v[8];
       load(col, g, x, d);
@@ -401,11 +619,17 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += rstd * (g[e] - x[e] * mean);
+      for (int e = 0; e < 8; ++e)
+        v[e] += rstd * (LN ? g[e] - level - x[e] * along : g[e] - x[e] * along);
       if (p.part) {
         float* const o = partial(p.part, gridDim.x, blockIdx.x, col);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = (row == blockIdx.x ? 0.f : o[e]) + d[e] * x[e];
+      }
+      if (LN && p.part_bias) {
+        float* const o = partial(p.part_bias, gridDim.x, blockIdx.x, col);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = (row == blockIdx.x ? 0.f : o[e]) + d[e];
       }
       store8(p.dx + row * p.dx_row + col, v, p.dim - col, TY);
     }
@@ -413,19 +637,26 @@ __global__ void __launch_bounds__(64 * NW) rms_norm_bwd_long(NormBwdArgs p) {
 }
 
 // out[j] = the sum of n partial sums; one block of 32 columns a workgroup, from block `first` on.
+// Blocks past out's `blocks` are those of `more`, whose partial sums follow.
 template <int TY>
 __global__ void __launch_bounds__(256) sum_partials(const float* part, int n, int first, int cols,
-                                                    uint16_t* out) {
-  sum_block<TY>(part, n, first + blockIdx.x, cols, out);
+                                                    int blocks, uint16_t* out, uint16_t* more) {
+  const int b = first + blockIdx.x;
+  if (b < blocks)
+    sum_block<TY>(part, n, b, cols, out);
+  else
+    sum_block<TY>(part + (int64_t)blocks * n * 32, n, b - blocks, cols, more);
 }
 
 struct DactArgs {
   const uint16_t* dc;
-  const uint16_t* pre;   // null: dpre is dc
+  const uint16_t* pre;   // null (and pre8 too): dpre is dc
+  const uint8_t* pre8;   // pre in 8 bits, in its place
+  const uint8_t* pre8_scale;
   uint16_t* dpre;
   float* part;           // partial column sums of every row block, or null
   uint16_t* sum;         // the column sums themselves (one row block), or null
-  int64_t dc_row, pre_row, dpre_row;
+  int64_t dc_row, pre_row, dpre_row, pre8_row, ps_row;
   int32_t m, n, act;
   int32_t row_blocks, rows_per_block;   // at most 2^30
 };
@@ -450,6 +681,8 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
   const int rows = p.m - r0 < p.rows_per_block ? (int)(p.m - r0) : p.rows_per_block;
   const uint16_t* const dc = p.dc + r0 * p.dc_row + col;
   const uint16_t* const pre = p.pre + r0 * p.pre_row + col;
+  const uint8_t* const pre8 = p.pre8 + r0 * p.pre8_row + col;
+  const uint8_t* const ps = p.pre8_scale + r0 * p.ps_row + (col >> 5);
   uint16_t* const dpre = p.dpre + r0 * p.dpre_row + col;
   float sum[8];
 #pragma unroll
@@ -459,9 +692,14 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
     for (int row = g; row < rows; row += 4) {
       float v[8];
       load8(v, dc + row * p.dc_row, n, TY, p.n >= 8);
-      if (p.pre) {
+      if (p.pre || p.pre8) {
         float u[8];
-        load8(u, pre + row * p.pre_row, n, TY, p.n >= 8);
+        if (p.pre8) {
+          const uint2 q = load_bytes8(pre8 + row * p.pre8_row, n, p.n >= 8);
+          unpack_block8(u, q.x, q.y, ps[row * p.ps_row]);
+        } else {
+          load8(u, pre + row * p.pre_row, n, TY, p.n >= 8);
+        }
         slope8(v, u, p.act);
         store8(dpre + row * p.dpre_row, v, n, TY);
       }
@@ -484,6 +722,79 @@ __global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
       store8(p.sum + col, sum, n, TY);
     else
       store_partial8(p.part, p.row_blocks, rb, col, sum);
+  }
+}
+
+// ---- checkpoints in 8 bits (see pack_block8) -----------------------------------------------
+// A wave takes 8 << `lanes` columns of 64 >> lanes rows at once, 8 columns a lane; segs such pieces
+// cover a row.  kPackRows pieces of rows a wave one below the other, all of their loads in flight.
+struct PackArgs {
+  const uint16_t* x;      // packing; null: unpacking
+  uint16_t* y;            // unpacking: act(values), in 16 bits
+  uint8_t* q;
+  uint8_t* scale;
+  int64_t x_row, y_row, q_row, s_row;
+  int32_t rows, dim, lanes, segs, act;
+};
+constexpr int kPackRows = 4;
+struct PackPlace {
+  int64_t row, col;   // of the lane's first piece; the others are 64 >> lanes rows apart
+  int n;              // columns that exist from col on
+};
+__device__ __forceinline__ PackPlace pack_place(const PackArgs& p) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const uint32_t seg = blockIdx.x % (uint32_t)p.segs, block = blockIdx.x / (uint32_t)p.segs;
+  const int per = 64 >> p.lanes;
+  PackPlace t;
+  t.row = ((int64_t)block * 4 + w) * (per * kPackRows) + (lane >> p.lanes);
+  t.col = (int64_t)seg * (8 << p.lanes) + (lane & ((1 << p.lanes) - 1)) * 8;
+  t.n = (int)(p.dim - t.col);
+  return t;
+}
+template <int TY>
+__global__ void __launch_bounds__(256) pack8(PackArgs p) {
+  const PackPlace t = pack_place(p);
+  const int per = 64 >> p.lanes;
+  const bool back = p.dim >= 8;
+  u32x4 v[kPackRows];
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {   // rows past the last: that one again, not stored
+    const int64_t r = t.row + i * per < p.rows ? t.row + i * per : p.rows - 1;
+    v[i] = raw8_load(p.x + r * p.x_row + t.col, t.n, back);
+  }
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    float x[8];
+    unpack8(x, raw8_shift(v[i], t.n, back), TY);
+    const Block8 b = pack_block8(x, TY);   // quads are whole: every lane is here
+    const int64_t r = t.row + i * per;
+    if (r >= p.rows || t.n <= 0) continue;
+    store_bytes8(p.q + r * p.q_row + t.col, b.lo, b.hi, t.n);
+    if ((t.col & 31) == 0) p.scale[r * p.s_row + (t.col >> 5)] = (uint8_t)b.scale;
+  }
+}
+template <int TY>
+__global__ void __launch_bounds__(256) unpack8_rows(PackArgs p) {
+  const PackPlace t = pack_place(p);
+  if (t.n <= 0) return;
+  const int per = 64 >> p.lanes;
+  const bool back = p.dim >= 8;
+  uint2 q[kPackRows];
+  uint32_t b[kPackRows];
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    const int64_t r = t.row + i * per < p.rows ? t.row + i * per : p.rows - 1;
+    q[i] = load_bytes8(p.q + r * p.q_row + t.col, t.n, back);
+    b[i] = p.scale[r * p.s_row + (t.col >> 5)];
+  }
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    const int64_t r = t.row + i * per;
+    if (r >= p.rows) continue;
+    float v[8];
+    unpack_block8(v, q[i].x, q[i].y, b[i]);
+    act_n(v, p.act);
+    store8(p.y + r * p.y_row + t.col, v, t.n, TY);
   }
 }
 

@@ -9,7 +9,11 @@ namespace lk {
 
 template <int TY>
 __device__ __forceinline__ void mma16x16(float4v& acc, const int4v& a, const int4v& b) {
-  if constexpr (TY == kF16)
+  if constexpr (TY == kI8)
+    acc = __builtin_bit_cast(
+        float4v, __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, __builtin_bit_cast(int4v, acc), 0, 0,
+                                                       0));
+  else if constexpr (TY == kF16)
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a),
                                                  __builtin_bit_cast(half8, b), acc, 0, 0, 0);
   else
@@ -27,7 +31,7 @@ __device__ __forceinline__ int4v load16(const uint16_t* p) {
 // row it does not fit 31 bits.
 template <int TY, bool SHORT>
 __device__ __forceinline__ u32x4 chunk_load(const uint16_t* row, uint32_t k, uint32_t K) {
-  constexpr int E = TY == kE4M3 ? 16 : 8, B = 16 / E;
+  constexpr int E = kBytes<TY> ? 16 : 8, B = 16 / E;
   if constexpr (!SHORT) {
     typedef u32x4 any __attribute__((aligned(1)));
     const uint32_t at = k + E <= K ? k : K - E;
@@ -37,7 +41,7 @@ __device__ __forceinline__ u32x4 chunk_load(const uint16_t* row, uint32_t k, uin
 #pragma unroll
   for (int e = 0; e < E - 1; ++e) {
     if (k + e < K) {
-      if (TY == kE4M3)
+      if (kBytes<TY>)
         v[e / 4] |= (uint32_t)((const uint8_t*)row)[k + e] << (8 * (e % 4));
       else
         v[e / 2] |= (uint32_t)row[k + e] << (16 * (e % 2));
@@ -48,7 +52,7 @@ __device__ __forceinline__ u32x4 chunk_load(const uint16_t* row, uint32_t k, uin
 // `live`: whether the chunk counts at all (else 0).
 template <int TY, bool SHORT>
 __device__ __forceinline__ int4v chunk_shift(u32x4 v, uint32_t k, uint32_t K, bool live) {
-  constexpr int E = TY == kE4M3 ? 16 : 8, B = 16 / E;
+  constexpr int E = kBytes<TY> ? 16 : 8, B = 16 / E;
   if (!live) v = u32x4{0u, 0u, 0u, 0u};
   if (!SHORT && k + E > K) v = shift_down(v, (int)(8 * B * (k + E - K)));
   return __builtin_bit_cast(int4v, v);
@@ -70,14 +74,14 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
   // 8 columns of one row a thread; each output element is one thread's sum in wave order
   for (int t = tid; t < 16 * NC / 8; t += NW * 64) {
     const int row = t / (NC / 8), cc = t % (NC / 8) * 8, col = n0 + cc;
-    if (row >= p.M || col >= p.N) continue;
+    if (!takes_part(p, row, col)) continue;
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = 0.f;
 #pragma unroll
     for (int u = 0; u < NW; ++u)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] += s[(u * 16 + row) * LDC + cc + e];
+      for (int e = 0; e < 8; ++e) f[e] = sum_add<TY>(f[e], s[(u * 16 + row) * LDC + cc + e]);
     if (W != nullptr) {
       float* const o = W + row * NC + cc;
       *(float4v*)o = float4v{f[0], f[1], f[2], f[3]};
@@ -97,7 +101,7 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
 // the last-level cache: 24.7, 23.4 and 13.7 us.
 template <int TY, int NB, int NW, bool SHORT>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
-  constexpr int UE = TY == kE4M3 ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk
+  constexpr int UE = kBytes<TY> ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk
   constexpr int NC = 16 * NB, U = 4;
   __shared__ float s[NW * 16 * (NC + 4)];
   const int lane = threadIdx.x & 63;
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
     // Every load is on its way before the first is used.  With one block of 16-bit columns the
     // waves are many and small, and do without (weights partly in the last-level cache: 16 rows of
     // e4m3, 8192 x 8192: 18.9 -> 16.7 us; one of bf16, 16384 x 4096: 23.1 without, 24.0 with).
-    if constexpr (NB > 1 || TY == kE4M3) __builtin_amdgcn_sched_barrier(0);
+    if constexpr (NB > 1 || kBytes<TY>) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
