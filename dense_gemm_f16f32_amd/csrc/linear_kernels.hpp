@@ -640,7 +640,6 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
                                          char GK_LDS* slab, float* W) {   // W: a slice's block, or null
   using S = Slab<T>;
   constexpr int RB = 32 / T::XB;   // MFMA rows of blocks in a slab
-  constexpr int U = S::U;
   float GK_LDS* const s = (float GK_LDS*)slab;
   const int rr = lane / S::LANES, cc = (lane % S::LANES) * 8;
   const int col = n0 + wn * T::WTN + cc;
@@ -649,8 +648,8 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
   const int ot = kBytes<T::TY> ? p.out_type : T::TY;
   const Columns c = load_columns<T::TY>(p, col);
   const float GK_LDS* const sr = s + rr * S::LDW + cc;
-#pragma unroll
-  for (int t = 0; t < T::TM / RB; ++t) {
+  // block t of the slab's rows
+  auto deposit = [&](int t) __attribute__((always_inline)) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slab's last reads are done
 #pragma unroll
     for (int b = 0; b < RB; ++b)
@@ -664,8 +663,11 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
           *(float4v GK_LDS*)(s + r * S::LDW + x) = float4v{q[v], q[v + 1], q[v + 2], q[v + 3]};
         }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int row_t = row0 + t * 32;
-    if (W != nullptr) {
+  };
+  if (W != nullptr) {
+#pragma unroll
+    for (int t = 0; t < T::TM / RB; ++t) {
+      deposit(t);
       float* const w = W + (int64_t)(wm * T::WTM + t * 32 + rr) * T::BN + wn * T::WTN + cc;
 #pragma unroll
       for (int i = 0; i < S::ITERS; ++i) {
@@ -673,72 +675,84 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
         *(float4v*)(w + i * S::ROWS * T::BN) = *(const float4v GK_LDS*)q;
         *(float4v*)(w + i * S::ROWS * T::BN + 4) = *(const float4v GK_LDS*)(q + 4);
       }
-      continue;
     }
-    if (!whole) {
-#pragma unroll 1
-      for (int i = 0; i < S::ITERS; ++i) {
-        const int row = row_t + i * S::ROWS;
-        const float4v lo = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW);
-        const float4v hi = *(const float4v GK_LDS*)(sr + i * S::ROWS * S::LDW + 4);
-        if (takes_part(p, row, col)) {
-          float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          finish8<T::TY>(p, row, col, f, c);
-        }
-      }
-      continue;
-    }
-    // a tile inside the matrix: no bounds, U rows of a lane at once
-#pragma unroll 1
-    for (int i = 0; i < S::ITERS; i += U) {
-      float f[U * 8];
-      u32x4 res[U];
-      float sa[U];
-      const int64_t row = row_t + i * S::ROWS;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (kBytes<T::TY>) sa[u] = p.scale_a ? p.scale_a[row + u * S::ROWS] : 1.f;
-        if (p.res) res[u] = *(const u32x4_any*)(p.res + (row + u * S::ROWS) * p.ldr + col);
-        const float GK_LDS* const q = sr + (i + u) * S::ROWS * S::LDW;
-        const float4v lo = *(const float4v GK_LDS*)q, hi = *(const float4v GK_LDS*)(q + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = sum_value<T::TY>(e < 4 ? lo[e & 3] : hi[e & 3]);
-          f[u * 8 + e] = kBytes<T::TY> ? v * sa[u] * c.sb[e] + c.bias[e] : v + c.bias[e];
-        }
-      }
-      auto put = [&](uint16_t* base, int64_t ld) __attribute__((always_inline)) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = f[u * 8 + e];
-          *(u32x4_any*)(base + (row + u * S::ROWS) * ld + col) = pack8(v, ot);
-        }
-      };
-      if (p.pre) put(p.pre, p.ldp);
-      if (p.pre8) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = f[u * 8 + e];
-          put_pre8(p, row + u * S::ROWS, col, v, 8, ot);
-        }
-      }
-      act_n(f, p.act);
-      if (p.res) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float r[8];
-          unpack8(r, res[u], ot);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[u * 8 + e] += r[e];
-        }
-      }
-      put(p.out, p.ldo);
-    }
+    return;
   }
+  // U rows of a lane at once, their loads in flight together.  INSIDE: a tile inside the matrix,
+  // no bounds; else rows past the last one repeat its loads, and nothing outside is stored.
+  auto finish = [&](auto inside) __attribute__((always_inline)) {
+    constexpr bool INSIDE = decltype(inside)::value;
+    constexpr int U = S::U;
+#pragma unroll
+    for (int t = 0; t < T::TM / RB; ++t) {
+      deposit(t);
+      const int row_t = row0 + t * 32;
+#pragma unroll 1
+      for (int i = 0; i < S::ITERS; i += U) {
+        float f[U * 8];
+        u32x4 res[U];
+        float sa[U];
+        const int row = row_t + i * S::ROWS;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          int64_t r = row + u * S::ROWS;
+          if (!INSIDE && r >= p.M) r = p.M - 1;
+          if (kBytes<T::TY>) sa[u] = p.scale_a ? p.scale_a[r] : 1.f;
+          if (p.res)
+            res[u] = INSIDE ? (u32x4)*(const u32x4_any*)(p.res + r * p.ldr + col)
+                            : raw8_load(p.res + r * p.ldr + col, c.n, p.N >= 8);
+          const float GK_LDS* const q = sr + (i + u) * S::ROWS * S::LDW;
+          const float4v lo = *(const float4v GK_LDS*)q, hi = *(const float4v GK_LDS*)(q + 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = sum_value<T::TY>(e < 4 ? lo[e & 3] : hi[e & 3]);
+            f[u * 8 + e] = kBytes<T::TY> ? v * sa[u] * c.sb[e] + c.bias[e] : v + c.bias[e];
+          }
+        }
+        auto values = [&](float (&v)[8], int u) __attribute__((always_inline)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = f[u * 8 + e];
+        };
+        auto put = [&](uint16_t* base, int64_t ld) __attribute__((always_inline)) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[8];
+            values(v, u);
+            const int64_t r = row + u * S::ROWS;
+            if constexpr (INSIDE)
+              *(u32x4_any*)(base + r * ld + col) = pack8(v, ot);
+            else if (r < p.M && c.n > 0)
+              store8(base + r * ld + col, v, c.n, ot);
+          }
+        };
+        if (p.pre) put(p.pre, p.ldp);
+        if (p.pre8) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float v[8];
+            values(v, u);
+            const int64_t r = row + u * S::ROWS;
+            put_pre8(p, r, col, v, INSIDE ? 8 : r < p.M ? c.n : 0, ot);
+          }
+        }
+        act_n(f, p.act);
+        if (p.res) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float r[8];
+            unpack8(r, INSIDE ? res[u] : raw8_shift(res[u], c.n, p.N >= 8), ot);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[u * 8 + e] += r[e];
+          }
+        }
+        put(p.out, p.ldo);
+      }
+    }
+  };
+  if (whole)
+    finish(std::true_type{});
+  else
+    finish(std::false_type{});
 }
 
 // k slots of the matrices, and the ragged panel
