@@ -780,16 +780,26 @@ nk::PackArgs pack_args(int64_t dim, const packed8_matrix& p) {
   a.dim = (int32_t)dim;
   return a;
 }
-// Launches f(args, grid) over all rows, in launches that stay below kThreads.
+nk::PackArgs unpack_args(int64_t dim, const packed8_matrix& p, int64_t activation, void* y,
+                         int64_t y_row) {
+  nk::PackArgs a = pack_args(dim, p);
+  a.y = (uint16_t*)y;
+  a.y_row = y_row;
+  a.act = (int32_t)activation;
+  return a;
+}
+// Launches f(args, grid) over all rows, each launch of at most `most` workgroups; `before` more are
+// added to the first one's grid.
 template <class F>
-int pack_launches(nk::PackArgs a, int64_t rows, F f) {
+int pack_launches(nk::PackArgs a, int64_t rows, int64_t before, int64_t most, F f) {
   const int64_t per = (int64_t)4 * nk::kPackRows * (64 >> a.lanes);   // rows a workgroup
-  const int64_t most = (kThreads / 256 - 1) / a.segs * per;           // segs is below 2^23
+  most = (most / a.segs > 0 ? most / a.segs : 1) * per;               // segs is below 2^23
   for (int64_t r0 = 0; r0 < rows; r0 += most) {
     const int64_t n = rows - r0 < most ? rows - r0 : most;
     a.rows = (int32_t)n;
-    f(a, dim3((uint32_t)(cdiv(n, per) * a.segs)));
+    f(a, dim3((uint32_t)(before + cdiv(n, per) * a.segs)));
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
+    before = 0;
     if (a.x) a.x += n * a.x_row;
     if (a.y) a.y += n * a.y_row;
     a.q += n * a.q_row;
@@ -797,18 +807,14 @@ int pack_launches(nk::PackArgs a, int64_t rows, F f) {
   }
   return GEMM_F16F32_OK;
 }
-int unpack_rows(int64_t type, int64_t rows, int64_t dim, const packed8_matrix& p, int64_t activation,
-                void* y, int64_t y_row, hipStream_t s) {
-  nk::PackArgs a = pack_args(dim, p);
-  a.y = (uint16_t*)y;
-  a.y_row = y_row;
-  a.act = (int32_t)activation;
-  return pack_launches(a, rows, [&](const nk::PackArgs& b, dim3 grid) {
-    if (type == LINEAR_NORM_BF16)
-      hipLaunchKernelGGL((nk::unpack8_rows<lk::kBF16>), grid, dim3(256), 0, s, b);
-    else
-      hipLaunchKernelGGL((nk::unpack8_rows<lk::kF16>), grid, dim3(256), 0, s, b);
-  });
+constexpr int64_t kWorkgroups = kThreads / 256 - 1;   // of 256 threads in a launch
+
+void prepare(int64_t type, const nk::DactArgs& d, const nk::PackArgs& u, int64_t before, dim3 grid,
+             hipStream_t s) {
+  if (type == LINEAR_NORM_BF16)
+    hipLaunchKernelGGL((nk::lin_prepare<lk::kBF16>), grid, dim3(256), 0, s, d, u, (int)before);
+  else
+    hipLaunchKernelGGL((nk::lin_prepare<lk::kF16>), grid, dim3(256), 0, s, d, u, (int)before);
 }
 
 }  // namespace
@@ -919,8 +925,9 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
   const bool sums = x.dbias != nullptr && f.dact;
   const bool last = sums && f.row_blocks != 1;   // dbias has a second step
   float* const part = last ? (float*)(ws + f.dpre_bytes) : nullptr;
+  nk::DactArgs d = {};
+  int64_t before = 0;   // workgroups of the element-wise pass
   if (f.dact && f.row_blocks > 0) {
-    nk::DactArgs d = {};
     d.dc = (const uint16_t*)x.dc;
     d.dc_row = x.dc_row;
     if (act) {
@@ -944,11 +951,21 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
     d.act = (int32_t)x.activation;
     d.row_blocks = f.row_blocks;
     d.rows_per_block = f.rows_per_block;
-    const dim3 grid((uint32_t)(cdiv(x.n, 512) * f.row_blocks));
-    if (bf)
-      hipLaunchKernelGGL((nk::lin_dact<lk::kBF16>), grid, dim3(256), 0, s, d);
-    else
-      hipLaunchKernelGGL((nk::lin_dact<lk::kF16>), grid, dim3(256), 0, s, d);
+    before = cdiv(x.n, 512) * f.row_blocks;
+  }
+  // a from 8 bits beside it, as far as one launch's workgroups go
+  nk::PackArgs u = {};
+  if (f.a_bytes > 0) {
+    f.a.p = ws + f.dpre_bytes + f.part_bytes;
+    u = unpack_args(x.k, k8.a, k8.a_activation, (void*)f.a.p, f.lda);
+    rc = pack_launches(u, x.m, before, kWorkgroups - before, [&](const nk::PackArgs& b, dim3 grid) {
+      prepare(x.type, d, b, before, grid, s);
+      before = 0;
+    });
+    if (rc != GEMM_F16F32_OK) return rc;
+  }
+  if (before > 0) {
+    prepare(x.type, d, u, before, dim3((uint32_t)before), s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   if (last && !f.pair) {
@@ -957,11 +974,6 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
     else
       launch_sum<lk::kF16>(part, f.row_blocks, x.n, x.dbias, nullptr, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
-  }
-  if (f.a_bytes > 0) {
-    f.a.p = ws + f.dpre_bytes + f.part_bytes;
-    rc = unpack_rows(x.type, x.m, x.k, k8.a, k8.a_activation, (void*)f.a.p, f.lda, s);
-    if (rc != GEMM_F16F32_OK) return rc;
   }
   void* const W = ws ? ws + f.dpre_bytes + f.part_bytes + f.a_bytes : nullptr;
   LinArgs da = {}, db = {};
@@ -1119,7 +1131,7 @@ int pack8(const pack8_args* args) {
   a.x = (const uint16_t*)x.x;
   a.x_row = x.x_row;
   const hipStream_t s = (hipStream_t)x.stream;
-  return pack_launches(a, x.rows, [&](const nk::PackArgs& b, dim3 grid) {
+  return pack_launches(a, x.rows, 0, kWorkgroups, [&](const nk::PackArgs& b, dim3 grid) {
     if (x.type == LINEAR_NORM_BF16)
       hipLaunchKernelGGL((nk::pack8<lk::kBF16>), grid, dim3(256), 0, s, b);
     else
@@ -1140,8 +1152,14 @@ int unpack8(const unpack8_args* args) {
   const Region w = region(x.y, x.rows, x.dim, x.y_row, 2);
   const Region r[] = {values_region(x.in, x.rows, x.dim), scale_region(x.in, x.rows, x.dim)};
   if (conflict(&w, 1, r, 2)) return GEMM_F16F32_ERR_OVERLAP;
-  return unpack_rows(x.type, x.rows, x.dim, x.in, x.activation, x.y, x.y_row,
-                     (hipStream_t)x.stream);
+  const nk::PackArgs a = unpack_args(x.dim, x.in, x.activation, x.y, x.y_row);
+  const hipStream_t s = (hipStream_t)x.stream;
+  return pack_launches(a, x.rows, 0, kWorkgroups, [&](const nk::PackArgs& b, dim3 grid) {
+    if (x.type == LINEAR_NORM_BF16)
+      hipLaunchKernelGGL((nk::unpack8_rows<lk::kBF16>), grid, dim3(256), 0, s, b);
+    else
+      hipLaunchKernelGGL((nk::unpack8_rows<lk::kF16>), grid, dim3(256), 0, s, b);
+  });
 }
 
 }  // extern "C"

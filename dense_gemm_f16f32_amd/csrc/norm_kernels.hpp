@@ -670,42 +670,70 @@ struct DactArgs {
 // doubles their work (at 4096^3 from 216 us to 432) to take a gradient's error, relative in the
 // norm, from 0.0023 to the 0.0017 of its own rounding in bf16 (f16: from 0.00029 to 0.00021).  The
 // column sums take the unrounded values.
-template <int TY>
-__global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
-  __shared__ float s[3][512];
-  const int cb = blockIdx.x / p.row_blocks, rb = blockIdx.x - cb * p.row_blocks;
-  const int t = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int col = cb * 512 + t * 8, n = p.n - col;
-  // rows counted from the block's first: numbers past the last row need not fit 31 bits
-  const int64_t r0 = (int64_t)rb * p.rows_per_block;
-  const int rows = p.m - r0 < p.rows_per_block ? (int)(p.m - r0) : p.rows_per_block;
+constexpr int kPre16 = 1, kPre8 = 2;
+template <int TY, int PRE>
+__device__ __forceinline__ void dact_rows(const DactArgs& p, int64_t r0, int rows, int g, int col,
+                                          float (&sum)[8]) {
+  constexpr int R = 4;   // rows of a thread whose loads are in flight at once
+  const int n = p.n - col;
+  const bool back = p.n >= 8;
   const uint16_t* const dc = p.dc + r0 * p.dc_row + col;
   const uint16_t* const pre = p.pre + r0 * p.pre_row + col;
   const uint8_t* const pre8 = p.pre8 + r0 * p.pre8_row + col;
   const uint8_t* const ps = p.pre8_scale + r0 * p.ps_row + (col >> 5);
   uint16_t* const dpre = p.dpre + r0 * p.dpre_row + col;
-  float sum[8];
+  for (int row = g; row < rows; row += 4 * R) {
+    u32x4 d[R], u[PRE == kPre16 ? R : 1];
+    uint2 q[PRE == kPre8 ? R : 1];
+    uint32_t b[PRE == kPre8 ? R : 1];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  if (n > 0) {
-#pragma unroll 4
-    for (int row = g; row < rows; row += 4) {
+    for (int i = 0; i < R; ++i) {   // past the last row: that one again, not counted
+      const int64_t r = row + 4 * i < rows ? row + 4 * i : rows - 1;
+      d[i] = raw8_load(dc + r * p.dc_row, n, back);
+      if constexpr (PRE == kPre16) u[i] = raw8_load(pre + r * p.pre_row, n, back);
+      if constexpr (PRE == kPre8) {
+        q[i] = load_bytes8(pre8 + r * p.pre8_row, n, back);
+        b[i] = ps[r * p.ps_row];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t r = row + 4 * i;
+      if (r >= rows) break;
       float v[8];
-      load8(v, dc + row * p.dc_row, n, TY, p.n >= 8);
-      if (p.pre || p.pre8) {
-        float u[8];
-        if (p.pre8) {
-          const uint2 q = load_bytes8(pre8 + row * p.pre8_row, n, p.n >= 8);
-          unpack_block8(u, q.x, q.y, ps[row * p.ps_row]);
-        } else {
-          load8(u, pre + row * p.pre_row, n, TY, p.n >= 8);
-        }
-        slope8(v, u, p.act);
-        store8(dpre + row * p.dpre_row, v, n, TY);
+      unpack8(v, raw8_shift(d[i], n, back), TY);
+      if constexpr (PRE != 0) {
+        float x[8];
+        if constexpr (PRE == kPre8)
+          unpack_block8(x, q[i].x, q[i].y, b[i]);
+        else
+          unpack8(x, raw8_shift(u[i], n, back), TY);
+        slope8(v, x, p.act);
+        store8(dpre + r * p.dpre_row, v, n, TY);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += v[e];
     }
+  }
+}
+template <int TY>
+__device__ __forceinline__ void dact_block(const DactArgs& p, int block, float (&s)[3][512]) {
+  const int cb = block / p.row_blocks, rb = block - cb * p.row_blocks;
+  const int t = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int col = cb * 512 + t * 8, n = p.n - col;
+  // rows counted from the block's first: numbers past the last row need not fit 31 bits
+  const int64_t r0 = (int64_t)rb * p.rows_per_block;
+  const int rows = p.m - r0 < p.rows_per_block ? (int)(p.m - r0) : p.rows_per_block;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  if (n > 0) {
+    if (p.pre8)
+      dact_rows<TY, kPre8>(p, r0, rows, g, col, sum);
+    else if (p.pre)
+      dact_rows<TY, kPre16>(p, r0, rows, g, col, sum);
+    else
+      dact_rows<TY, 0>(p, r0, rows, g, col, sum);
   }
   if (p.part == nullptr && p.sum == nullptr) return;
   if (g > 0) {
@@ -741,9 +769,9 @@ struct PackPlace {
   int64_t row, col;   // of the lane's first piece; the others are 64 >> lanes rows apart
   int n;              // columns that exist from col on
 };
-__device__ __forceinline__ PackPlace pack_place(const PackArgs& p) {
+__device__ __forceinline__ PackPlace pack_place(const PackArgs& p, uint32_t workgroup) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const uint32_t seg = blockIdx.x % (uint32_t)p.segs, block = blockIdx.x / (uint32_t)p.segs;
+  const uint32_t seg = workgroup % (uint32_t)p.segs, block = workgroup / (uint32_t)p.segs;
   const int per = 64 >> p.lanes;
   PackPlace t;
   t.row = ((int64_t)block * 4 + w) * (per * kPackRows) + (lane >> p.lanes);
@@ -753,7 +781,7 @@ __device__ __forceinline__ PackPlace pack_place(const PackArgs& p) {
 }
 template <int TY>
 __global__ void __launch_bounds__(256) pack8(PackArgs p) {
-  const PackPlace t = pack_place(p);
+  const PackPlace t = pack_place(p, blockIdx.x);
   const int per = 64 >> p.lanes;
   const bool back = p.dim >= 8;
   u32x4 v[kPackRows];
@@ -774,8 +802,8 @@ __global__ void __launch_bounds__(256) pack8(PackArgs p) {
   }
 }
 template <int TY>
-__global__ void __launch_bounds__(256) unpack8_rows(PackArgs p) {
-  const PackPlace t = pack_place(p);
+__device__ __forceinline__ void unpack8_block(const PackArgs& p, uint32_t workgroup) {
+  const PackPlace t = pack_place(p, workgroup);
   if (t.n <= 0) return;
   const int per = 64 >> p.lanes;
   const bool back = p.dim >= 8;
@@ -796,6 +824,21 @@ __global__ void __launch_bounds__(256) unpack8_rows(PackArgs p) {
     act_n(v, p.act);
     store8(p.y + r * p.y_row + t.col, v, t.n, TY);
   }
+}
+template <int TY>
+__global__ void __launch_bounds__(256) unpack8_rows(PackArgs p) {
+  unpack8_block<TY>(p, blockIdx.x);
+}
+
+// What stands before the products of a backward pass, in one launch: dpre and the column sums in the
+// first dact_blocks workgroups, a restored from 8 bits in the others.
+template <int TY>
+__global__ void __launch_bounds__(256) lin_prepare(DactArgs d, PackArgs u, int dact_blocks) {
+  __shared__ float s[3][512];
+  if ((int)blockIdx.x < dact_blocks)
+    dact_block<TY>(d, blockIdx.x, s);
+  else
+    unpack8_block<TY>(u, blockIdx.x - dact_blocks);
 }
 
 }  // namespace nk
