@@ -670,13 +670,14 @@ struct DactArgs {
 // doubles their work (at 4096^3 from 216 us to 432) to take a gradient's error, relative in the
 // norm, from 0.0023 to the 0.0017 of its own rounding in bf16 (f16: from 0.00029 to 0.00021).  The
 // column sums take the unrounded values.
+// WHOLE: the workgroup's 512 columns all exist, and nothing is spent on a row's end.
 constexpr int kPre16 = 1, kPre8 = 2;
-template <int TY, int PRE>
+template <int TY, int PRE, bool WHOLE>
 __device__ __forceinline__ void dact_rows(const DactArgs& p, int64_t r0, int rows, int g, int col,
                                           float (&sum)[8]) {
   constexpr int R = 4;   // rows of a thread whose loads are in flight at once
-  const int n = p.n - col;
-  const bool back = p.n >= 8;
+  const int n = WHOLE ? 8 : p.n - col;
+  const bool back = WHOLE || p.n >= 8;
   const uint16_t* const dc = p.dc + r0 * p.dc_row + col;
   const uint16_t* const pre = p.pre + r0 * p.pre_row + col;
   const uint8_t* const pre8 = p.pre8 + r0 * p.pre8_row + col;
@@ -727,14 +728,18 @@ __device__ __forceinline__ void dact_block(const DactArgs& p, int block, float (
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  if (n > 0) {
+  auto work = [&](auto whole) __attribute__((always_inline)) {
     if (p.pre8)
-      dact_rows<TY, kPre8>(p, r0, rows, g, col, sum);
+      dact_rows<TY, kPre8, decltype(whole)::value>(p, r0, rows, g, col, sum);
     else if (p.pre)
-      dact_rows<TY, kPre16>(p, r0, rows, g, col, sum);
+      dact_rows<TY, kPre16, decltype(whole)::value>(p, r0, rows, g, col, sum);
     else
-      dact_rows<TY, 0>(p, r0, rows, g, col, sum);
-  }
+      dact_rows<TY, 0, decltype(whole)::value>(p, r0, rows, g, col, sum);
+  };
+  if (p.n - cb * 512 >= 512)
+    work(std::true_type{});
+  else if (n > 0)
+    work(std::false_type{});
   if (p.part == nullptr && p.sum == nullptr) return;
   if (g > 0) {
 #pragma unroll
@@ -768,6 +773,7 @@ constexpr int kPackRows = 4;
 struct PackPlace {
   int64_t row, col;   // of the lane's first piece; the others are 64 >> lanes rows apart
   int n;              // columns that exist from col on
+  bool whole;         // all columns of the workgroup's piece of a row exist
 };
 __device__ __forceinline__ PackPlace pack_place(const PackArgs& p, uint32_t workgroup) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -777,42 +783,48 @@ __device__ __forceinline__ PackPlace pack_place(const PackArgs& p, uint32_t work
   t.row = ((int64_t)block * 4 + w) * (per * kPackRows) + (lane >> p.lanes);
   t.col = (int64_t)seg * (8 << p.lanes) + (lane & ((1 << p.lanes) - 1)) * 8;
   t.n = (int)(p.dim - t.col);
+  t.whole = p.dim - (int64_t)seg * (8 << p.lanes) >= (8 << p.lanes);
   return t;
 }
-template <int TY>
-__global__ void __launch_bounds__(256) pack8(PackArgs p) {
-  const PackPlace t = pack_place(p, blockIdx.x);
-  const int per = 64 >> p.lanes;
-  const bool back = p.dim >= 8;
+template <int TY, bool WHOLE>
+__device__ __forceinline__ void pack8_piece(const PackArgs& p, const PackPlace& t) {
+  const int per = 64 >> p.lanes, n = WHOLE ? 8 : t.n;
+  const bool back = WHOLE || p.dim >= 8;
   u32x4 v[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {   // rows past the last: that one again, not stored
     const int64_t r = t.row + i * per < p.rows ? t.row + i * per : p.rows - 1;
-    v[i] = raw8_load(p.x + r * p.x_row + t.col, t.n, back);
+    v[i] = raw8_load(p.x + r * p.x_row + t.col, n, back);
   }
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     float x[8];
-    unpack8(x, raw8_shift(v[i], t.n, back), TY);
+    unpack8(x, raw8_shift(v[i], n, back), TY);
     const Block8 b = pack_block8(x, TY);   // quads are whole: every lane is here
     const int64_t r = t.row + i * per;
-    if (r >= p.rows || t.n <= 0) continue;
-    store_bytes8(p.q + r * p.q_row + t.col, b.lo, b.hi, t.n);
+    if (r >= p.rows || n <= 0) continue;
+    store_bytes8(p.q + r * p.q_row + t.col, b.lo, b.hi, n);
     if ((t.col & 31) == 0) p.scale[r * p.s_row + (t.col >> 5)] = (uint8_t)b.scale;
   }
 }
 template <int TY>
-__device__ __forceinline__ void unpack8_block(const PackArgs& p, uint32_t workgroup) {
-  const PackPlace t = pack_place(p, workgroup);
-  if (t.n <= 0) return;
-  const int per = 64 >> p.lanes;
-  const bool back = p.dim >= 8;
+__global__ void __launch_bounds__(256) pack8(PackArgs p) {
+  const PackPlace t = pack_place(p, blockIdx.x);
+  if (t.whole)
+    pack8_piece<TY, true>(p, t);
+  else
+    pack8_piece<TY, false>(p, t);
+}
+template <int TY, bool WHOLE>
+__device__ __forceinline__ void unpack8_piece(const PackArgs& p, const PackPlace& t) {
+  const int per = 64 >> p.lanes, n = WHOLE ? 8 : t.n;
+  const bool back = WHOLE || p.dim >= 8;
   uint2 q[kPackRows];
   uint32_t b[kPackRows];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const int64_t r = t.row + i * per < p.rows ? t.row + i * per : p.rows - 1;
-    q[i] = load_bytes8(p.q + r * p.q_row + t.col, t.n, back);
+    q[i] = load_bytes8(p.q + r * p.q_row + t.col, n, back);
     b[i] = p.scale[r * p.s_row + (t.col >> 5)];
   }
 #pragma unroll
@@ -822,8 +834,16 @@ __device__ __forceinline__ void unpack8_block(const PackArgs& p, uint32_t workgr
     float v[8];
     unpack_block8(v, q[i].x, q[i].y, b[i]);
     act_n(v, p.act);
-    store8(p.y + r * p.y_row + t.col, v, t.n, TY);
+    store8(p.y + r * p.y_row + t.col, v, n, TY);
   }
+}
+template <int TY>
+__device__ __forceinline__ void unpack8_block(const PackArgs& p, uint32_t workgroup) {
+  const PackPlace t = pack_place(p, workgroup);
+  if (t.whole)
+    unpack8_piece<TY, true>(p, t);
+  else if (t.n > 0)
+    unpack8_piece<TY, false>(p, t);
 }
 template <int TY>
 __global__ void __launch_bounds__(256) unpack8_rows(PackArgs p) {
