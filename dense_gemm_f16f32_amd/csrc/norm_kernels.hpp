@@ -23,14 +23,32 @@ __device__ __forceinline__ float group_sum(float v, float* s) {
   }
   return v;
 }
+// Sum over a wave, all of whose lanes are active, by moves between lanes inside the vector unit: a
+// step takes some ten cycles, and one through LDS (__shfl_xor) about a hundred.
+template <int CTRL>
+__device__ __forceinline__ float lane_move(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_value(float v, int lane = 0) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ float row_sum16(float v) {   // over each 16 lanes, in all of them
+  v += lane_move<0xB1>(v);    // quads: 1 0 3 2
+  v += lane_move<0x4E>(v);    // 2 3 0 1
+  v += lane_move<0x141>(v);   // 8 lanes mirrored
+  v += lane_move<0x140>(v);   // 16 lanes mirrored
+  return v;
+}
+__device__ __forceinline__ float row_sum(float v) { return lane_value(row_sum16(v)); }
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row_sum16(v);
+  return (lane_value(v) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
 // Two sums at once; `s` holds 2 NW floats.
 template <int NW>
 __device__ __forceinline__ float2v group_sum2(float2v v, float* s) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    v[0] += __shfl_xor(v[0], d);
-    v[1] += __shfl_xor(v[1], d);
-  }
+  v = float2v{wave_sum(v[0]), wave_sum(v[1])};
   if constexpr (NW > 1) {
     if ((threadIdx.x & 63) == 0) {
       s[2 * (threadIdx.x >> 6)] = v[0];
@@ -48,11 +66,18 @@ __device__ __forceinline__ float2v group_sum2(float2v v, float* s) {
 }
 template <int NW>
 __device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* s) {
+  v = quad_max(v);
+  uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);
+  v = v > o ? v : o;
+  o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);
+  v = v > o ? v : o;
+  uint32_t r = 0u;
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t o = __shfl_xor(v, d);
-    v = v > o ? v : o;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * i);
+    r = r > x ? r : x;
   }
+  v = r;
   if constexpr (NW > 1) {
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -169,14 +194,19 @@ __device__ __forceinline__ uint32_t max_bits8(const float (&v)[8], uint32_t m) {
 // 512 NW C columns, held in registers.  C == 0: longer rows, read again for each step that
 // needs them.
 //
-// LN (the layer norm): the mean first, then the sums of the differences from it and of their
-// squares, in one reduction.  The sum of the differences would be 0 but for the mean's rounding; its
-// mean d corrects both statistics, mean += d and var = mean(c^2) - d^2, so that rows far from 0
-// keep their deviation's bits.  (A mean of squares less the mean's square would lose them.)
+// LN (the layer norm): each wave takes the mean of its own columns, m_w, and the sums of the
+// differences c from it and of their squares, s_w and q_w (s_w would be 0 but for the mean's
+// rounding).  They meet once: with n_w columns a wave and e_w = m_w - m_0,
+//   d = sum(n_w e_w + s_w) / n;  mean = m_0 + d
+//   var = sum(q_w + 2 (e_w - d) s_w + n_w (e_w - d)^2) / n
+// all in differences, so that rows far from 0 keep their deviation's bits (a mean of squares less
+// the mean's square would lose them), and with one barrier (with the row's mean first it took
+// three).
 template <int TY, int OUT, bool LN, int NW, int C>
 __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   const bool back = p.dim >= 8;
-  __shared__ float ssum[2 * NW];
+  __shared__ float ssum[LN ? 1 : NW];
+  __shared__ float4v swave[LN ? 2 : 1][LN ? NW : 1];
   __shared__ uint32_t smax[NW];
   constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
   const int64_t row = blockIdx.x;
@@ -186,7 +216,7 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   const int c0 = threadIdx.x * 8;
   const int steps = C > 0 ? C : (p.dim - 1) / STEP + 1;   // dim > 0; dim + STEP need not fit
   float hv[CR][8], wv[CR][8], bv[CR][8];
-  float mean = 0.f;
+  float own = 0.f, mean = 0.f, shift = 0.f;   // layer norm: the wave's mean, the row's, d - e_w
   auto load_h = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
     load8(v, x + col, p.dim - col, TY, back);
     if (res) {
@@ -204,11 +234,11 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
       for (int e = 0; e < 8; ++e) v[e] = 0.f;
     }
   };
-  // differences from the mean; columns past dim stay 0
+  // differences from the wave's mean; columns past dim stay 0
   auto centre = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
     if constexpr (LN) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? v[e] - mean : 0.f;
+      for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? v[e] - own : 0.f;
     }
   };
   float2v sum = {0.f, 0.f};   // of the values or differences (layer norm), of their squares
@@ -220,13 +250,37 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
       sum[1] += u * u;
     }
   };
-  // mean of the squares about the mean, with what is added to mean, in units of 1 / unit
-  float shift = 0.f;
-  auto moments = [&](float unit) __attribute__((always_inline)) {
+  // columns of wave w
+  auto columns = [&](int w) __attribute__((always_inline)) {
+    const int rest = p.dim % STEP - 512 * w;
+    return (float)(p.dim / STEP * 512 + (rest < 0 ? 0 : rest < 512 ? rest : 512));
+  };
+  // mean of the squares (layer norm: about the mean) and eps, in units of 1 / unit^2
+  auto moments = [&](float unit, int turn) __attribute__((always_inline)) {
     if constexpr (LN) {
-      const float2v s = group_sum2<NW>(sum, ssum);
-      shift = s[0] * p.inv_dim;
-      const float var = s[1] * p.inv_dim - shift * shift;
+      const float s1 = wave_sum(sum[0]), q = wave_sum(sum[1]);
+      float var;
+      if constexpr (NW == 1) {
+        const float d = s1 * p.inv_dim;
+        var = q * p.inv_dim - d * d;
+        shift = d / unit;
+        mean = own + shift;
+      } else {
+        float4v(&sw)[NW] = swave[turn];
+        if ((threadIdx.x & 63) == 0) sw[threadIdx.x >> 6] = float4v{own, s1, q, 0.f};
+        __syncthreads();
+        // lane w mod 16 takes wave w's part
+        const int w = threadIdx.x & 15;
+        const float n = w < NW ? columns(w) : 0.f;
+        const float4v t = sw[w < NW ? w : 0];
+        const float m0 = lane_value(t[0]);
+        const float e = n > 0.f ? (t[0] - m0) * unit : 0.f;
+        const float d = row_sum(n > 0.f ? (n * e + t[1]) * p.inv_dim : 0.f);
+        const float f = e - d;
+        var = row_sum(n > 0.f ? (t[2] + 2.f * f * t[1] + n * f * f) * p.inv_dim : 0.f);
+        mean = m0 + d / unit;
+        shift = d / unit - (own - m0);
+      }
       return (var < 0.f ? 0.f : var) + p.eps * unit * unit;   // NaN stays
     } else {
       return group_sum<NW>(sum[1], ssum) * p.inv_dim + p.eps * unit * unit;
@@ -249,14 +303,14 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   }
   if constexpr (LN) {
     // terms of the mean, not of the sum: it cannot leave fp32's range where the values have not
+    const float n = columns(threadIdx.x >> 6), inv = n > 0.f ? 1.f / n : 0.f;
 #pragma unroll CR
     for (int i = 0; i < steps; ++i) {
       if constexpr (C == 0) load_h(c0 + i * STEP, hv[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mean += hv[C > 0 ? i : 0][e] * p.inv_dim;
+      for (int e = 0; e < 8; ++e) own += hv[C > 0 ? i : 0][e] * inv;
     }
-    mean = group_sum<NW>(mean, ssum);
-    if constexpr (NW > 1) __syncthreads();   // it has been read
+    own = wave_sum(own);
   }
 #pragma unroll CR
   for (int i = 0; i < steps; ++i) {
@@ -264,13 +318,13 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
     centre(c0 + i * STEP, hv[C > 0 ? i : 0]);
     add(hv[C > 0 ? i : 0], 1.f);
   }
-  float square = moments(1.f), unit = 1.f;
+  float square = moments(1.f, 0), unit = 1.f;
   // Squares outside fp32's range (bf16 rows above 1e19, or below 1e-9 with a tiny eps) are summed
   // again in units that bring them into it; every thread of the row holds the same sum.  (The layer
   // norm's infinite sum less its infinite correction is NaN.)
   if (square < 0x1p-60f || square == __builtin_inff() || (LN && square != square)) {
     unit = square < 1.f ? 0x1p64f : 0x1p-96f;
-    if constexpr (NW > 1) __syncthreads();   // the first sum has been read
+    if constexpr (NW > 1 && !LN) __syncthreads();   // the first sum has been read
     sum = float2v{0.f, 0.f};
 #pragma unroll CR
     for (int i = 0; i < steps; ++i) {
@@ -280,13 +334,12 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
       }
       add(hv[C > 0 ? i : 0], unit);
     }
-    square = moments(unit);
-    shift /= unit;
+    square = moments(unit, 1);
   }
   const float rstd = unit / sqrtf(square);
   if (threadIdx.x == 0) {
     if (p.rstd) p.rstd[row] = rstd;
-    if (LN && p.mean) p.mean[row] = mean + shift;
+    if (LN && p.mean) p.mean[row] = mean;
   }
   // y of step i
   auto norm = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
