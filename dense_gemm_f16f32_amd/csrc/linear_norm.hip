@@ -582,11 +582,23 @@ void with_types(int64_t type, int64_t out_type, F f) {
 // The backward pass: as above, but short rows take one wave, four of them a workgroup, and rows
 // above 8192 fewer waves of more registers.
 constexpr int64_t kShortRow = 1024, kLongRow = 16384;
+// `small`: the column sums in the same launch (layer norm only, up to 8192 columns).
 template <int TY, bool LN>
-void norm_backward(const nk::NormBwdArgs& p, int grid, hipStream_t s) {
+void norm_backward(const nk::NormBwdArgs& p, int grid, bool small, hipStream_t s) {
 #define LN_BACKWARD(NW, C, RW)                                                               \
-  hipLaunchKernelGGL((nk::norm_bwd<TY, LN, NW, C, RW>), dim3((uint32_t)grid), dim3(64 * NW * RW), \
-                     0, s, p)
+  do {                                                                                       \
+    if constexpr (LN && C <= 2) {                                                            \
+      if (small) {                                                                           \
+        const int columns = (int)cdiv(p.dim, nk::small_columns(512 * NW * C));               \
+        hipLaunchKernelGGL((nk::layer_norm_bwd_small<TY, NW, C, RW>),                        \
+                           dim3((uint32_t)(grid + columns)), dim3(64 * NW * RW), 0, s, p,    \
+                           columns);                                                         \
+        break;                                                                               \
+      }                                                                                      \
+    }                                                                                        \
+    hipLaunchKernelGGL((nk::norm_bwd<TY, LN, NW, C, RW>), dim3((uint32_t)grid),              \
+                       dim3(64 * NW * RW), 0, s, p);                                         \
+  } while (0)
   if (p.dim <= 512) LN_BACKWARD(1, 1, 4);
   else if (p.dim <= kShortRow) LN_BACKWARD(1, 2, 4);
   else if (p.dim <= 2048) LN_BACKWARD(4, 1, 1);
@@ -618,7 +630,15 @@ bool backward_sums(int64_t rows, int64_t dim) {
 int64_t norm_part_bytes(int64_t rows, int64_t dim) {
   return backward_sums(rows, dim) ? partial_bytes(backward_groups(rows, dim), dim) : 0;
 }
+// Whether the layer norm's column sums go in the launch of dx, from dy and h read a second time: up to
+// 1024 rows, whose columns a workgroup takes in one or two steps.  In a graph / launched one by one,
+// in two launches and in one: 256 x 1021 7.1 / 9.4 and 4.6 / 5.9 us, 1024 x 512 5.9 / 9.1 and 5.9 /
+// 5.7, 1024 x 8192 28.3 / 27.6 and 24.1 / 23.8; past the rule 2048 x 512 7.2 / 8.9 and 12.3 / 12.1.
+bool norm_small(int64_t rows, int64_t dim) {
+  return rows <= 1024 && dim <= 8192 && backward_sums(rows, dim) && rows > 0;
+}
 int64_t norm_backward_bytes(const layer_norm_backward_args& x) {
+  if (norm_small(x.rows, x.dim)) return 0;
   return ((x.dweight != nullptr) + (x.dbias != nullptr)) * norm_part_bytes(x.rows, x.dim);
 }
 
@@ -703,7 +723,8 @@ int norm_backward_call(layer_norm_backward_args x, bool ln) {
   if ((((uintptr_t)x.weight | (uintptr_t)x.dweight | (uintptr_t)x.dbias) & 1) ||
       (((uintptr_t)x.mean | (uintptr_t)x.rstd) & 3))
     return GEMM_F16F32_ERR_OPTS;
-  const int64_t need = norm_backward_bytes(x);
+  const int64_t need = ln ? norm_backward_bytes(x)
+                          : (x.dweight != nullptr) * norm_part_bytes(x.rows, x.dim);
   rc = check_workspace(x.workspace, x.workspace_bytes, need);
   if (rc != GEMM_F16F32_OK) return rc;
   const Region rdx = region(x.dx, x.rows, x.dim, x.dx_row, 2);
@@ -721,7 +742,8 @@ int norm_backward_call(layer_norm_backward_args x, bool ln) {
   const hipStream_t s = (hipStream_t)x.stream;
   const bool bf = x.type == LINEAR_NORM_BF16;
   const int groups = backward_groups(x.rows, x.dim);
-  const bool sums = backward_sums(x.rows, x.dim);
+  const bool small = ln && (x.dweight || x.dbias) && norm_small(x.rows, x.dim);
+  const bool sums = !small && backward_sums(x.rows, x.dim);
   float* const part = (float*)x.workspace;
   if (groups > 0) {
     nk::NormBwdArgs p = {};
@@ -748,10 +770,11 @@ int norm_backward_call(layer_norm_backward_args x, bool ln) {
     p.dim = (int32_t)x.dim;
     p.inv_dim = (float)(1.0 / (double)x.dim);
     if (ln)
-      bf ? norm_backward<lk::kBF16, true>(p, groups, s) : norm_backward<lk::kF16, true>(p, groups, s);
+      bf ? norm_backward<lk::kBF16, true>(p, groups, small, s)
+         : norm_backward<lk::kF16, true>(p, groups, small, s);
     else
-      bf ? norm_backward<lk::kBF16, false>(p, groups, s)
-         : norm_backward<lk::kF16, false>(p, groups, s);
+      bf ? norm_backward<lk::kBF16, false>(p, groups, false, s)
+         : norm_backward<lk::kF16, false>(p, groups, false, s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   if ((x.dweight || x.dbias) && sums) {

@@ -471,8 +471,9 @@ __device__ __forceinline__ void store_partial8(float* part, int groups, int grou
 // workgroup adds and writes them once (LN, the layer norm: dbias' sums too).  Short rows (one wave each) go four to a workgroup.  HBM
 // bounds it: 8192 x 4096 bf16 50 us (5.4 TB/s of dy, h, dh and dx), and 5 for sum_partials; with the
 // rows partly in the last-level cache 41 us, and there without the loads ahead 70.
-template <int TY, bool LN, int NW, int C, int RW>
-__global__ void __launch_bounds__(64 * NW * RW) norm_bwd(NormBwdArgs p) {
+// Without SUMS dx alone.
+template <int TY, bool LN, int NW, int C, int RW, bool SUMS>
+__device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& p, int group, int groups) {
   static_assert(NW == 1 || RW == 1, "rows of several waves share the workgroup's barrier");
   const bool back = p.dim >= 8;
   __shared__ float ssum[2][2 * NW];
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(64 * NW * RW) norm_bwd(NormBwdArgs p) {
     }
   };
   constexpr bool kAhead = C <= 2;
-  const int64_t first = (int64_t)blockIdx.x * RW + rw, step = (int64_t)gridDim.x * RW;
+  const int64_t first = (int64_t)group * RW + rw, step = (int64_t)groups * RW;
   Row cur, nxt;
   if (kAhead && first < p.rows) load(cur, first);
   int turn = 0;
@@ -540,9 +541,9 @@ __global__ void __launch_bounds__(64 * NW * RW) norm_bwd(NormBwdArgs p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] = LN ? (x[e] - mean) * rstd : x[e] * rstd;
-        dw[i][e] += d[e] * x[e];
+        if constexpr (SUMS) dw[i][e] += d[e] * x[e];
         if constexpr (LN) {
-          db[i][e] += d[e];
+          if constexpr (SUMS) db[i][e] += d[e];
           sum[1] += d[e] * wv[kTight ? 0 : i][e];
         }
         sum[0] += d[e] * wv[kTight ? 0 : i][e] * x[e];
@@ -577,6 +578,7 @@ __global__ void __launch_bounds__(64 * NW * RW) norm_bwd(NormBwdArgs p) {
     }
     cur = nxt;
   }
+  if constexpr (!SUMS) return;
   if (p.part == nullptr && p.dweight == nullptr &&
       (!LN || (p.part_bias == nullptr && p.dbias == nullptr)))
     return;
@@ -612,16 +614,92 @@ __global__ void __launch_bounds__(64 * NW * RW) norm_bwd(NormBwdArgs p) {
     const int col = c0 + i * STEP;
     if (col >= p.dim) continue;
     if (p.part != nullptr)
-      store_partial8(p.part, gridDim.x, blockIdx.x, col, dw[i]);
+      store_partial8(p.part, groups, group, col, dw[i]);
     else if (p.dweight != nullptr)   // the only workgroup
       store8(p.dweight + col, dw[i], p.dim - col, TY);
     if constexpr (LN) {
       if (p.part_bias != nullptr)
-        store_partial8(p.part_bias, gridDim.x, blockIdx.x, col, db[i]);
+        store_partial8(p.part_bias, groups, group, col, db[i]);
       else if (p.dbias != nullptr)
         store8(p.dbias + col, db[i], p.dim - col, TY);
     }
   }
+}
+template <int TY, bool LN, int NW, int C, int RW>
+__global__ void __launch_bounds__(64 * NW * RW) norm_bwd(NormBwdArgs p) {
+  norm_bwd_rows<TY, LN, NW, C, RW, true>(p, blockIdx.x, gridDim.x);
+}
+
+// The layer norm's weight and bias gradients of COLS columns over all rows, by a workgroup of T
+// threads: 8 columns a thread, T / LANES rows at once.
+template <int TY, int T, int COLS>
+__device__ __forceinline__ void norm_columns(const NormBwdArgs& p, int block) {
+  constexpr int R = 8, LANES = COLS / 8, STEP = T / LANES;   // R: rows of a thread in flight
+  __shared__ float s[T / 16][2][COLS];
+  static_assert(LANES == 2 || LANES == 4, "the moves between lanes");
+  const int t = threadIdx.x, c = block * COLS + (t % LANES) * 8, n = p.dim - c;
+  const bool back = p.dim >= 8;
+  float dw[8], db[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dw[e] = db[e] = 0.f;
+  for (int row = t / LANES; row < p.rows; row += R * STEP) {
+    u32x4 d[R], h[R];
+    float mean[R], rstd[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {   // past the last row: that one again, not counted
+      const int64_t r = row + i * STEP < p.rows ? row + i * STEP : p.rows - 1;
+      d[i] = raw8_load(p.dy + r * p.dy_row + c, n, back);
+      h[i] = raw8_load(p.h + r * p.h_row + c, n, back);
+      mean[i] = p.mean[r];
+      rstd[i] = p.rstd[r];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (row + i * STEP >= p.rows) break;
+      float g[8], x[8];
+      unpack8(g, raw8_shift(d[i], n, back), TY);
+      unpack8(x, raw8_shift(h[i], n, back), TY);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw[e] += g[e] * ((x[e] - mean[i]) * rstd[i]);
+        db[e] += g[e];
+      }
+    }
+  }
+  // lanes LANES apart hold the same columns: over each 16 lanes, then over these in order
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float& v = k ? db[e] : dw[e];
+      v += lane_move<0x128>(v);                             // 16 lanes rotated by 8
+      v += lane_move<0x124>(v);                             // by 4
+      if constexpr (LANES == 2) v += lane_move<0x4E>(v);    // quads: 2 3 0 1
+      if ((t & 15) < LANES) s[t >> 4][k][(t & 15) * 8 + e] = v;
+    }
+  }
+  __syncthreads();
+  if (t < 2 * COLS) {   // the columns of dweight, then of dbias
+    const int j = t % COLS, col = block * COLS + j;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < T / 16; ++w) v += s[w][t / COLS][j];
+    uint16_t* const out = t < COLS ? p.dweight : p.dbias;
+    if (out != nullptr && col < p.dim) out[col] = to_16(v, TY);
+  }
+}
+// Columns of a workgroup: 32 of them fill a cache line's half, 16 leave fewer rows to a thread; rows of
+// up to 1024 columns have the workgroups to spare for that.
+constexpr int small_columns(int row_columns) { return row_columns <= 1024 ? 16 : 32; }
+// A small backward pass in one launch: `columns` workgroups for some columns each of the weight's and
+// the bias' gradients, which read dy and h a second time, from a cache, and the others for dx.
+template <int TY, int NW, int C, int RW>
+__global__ void __launch_bounds__(64 * NW * RW) layer_norm_bwd_small(NormBwdArgs p, int columns) {
+  if ((int)blockIdx.x < columns) {
+    norm_columns<TY, 64 * NW * RW, small_columns(512 * NW * C)>(p, blockIdx.x);
+    return;
+  }
+  norm_bwd_rows<TY, true, NW, C, RW, false>(p, blockIdx.x - columns, gridDim.x - columns);
 }
 
 // Rows too long for registers: read twice, the dweight and dbias sums kept in the workgroup's

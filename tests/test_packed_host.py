@@ -51,7 +51,7 @@ def norm(call="layer_norm_forward", **change):
 
 
 def norm_backward(call="layer_norm_backward", **change):
-    base = dict(rows=400, dim=64, type=F16, dy=G, dy_row=64, h=2 * G, h_row=64, weight=3 * G,
+    base = dict(rows=4000, dim=64, type=F16, dy=G, dy_row=64, h=2 * G, h_row=64, weight=3 * G,
                 mean=4 * G, rstd=5 * G, dh=6 * G, dh_row=64, dx=7 * G, dx_row=64, dweight=8 * G,
                 dbias=9 * G, workspace=10 * G, workspace_bytes=G)
     return getattr(ln.lib(), call)(fields(NORM_BACKWARD, base, change))
@@ -155,7 +155,7 @@ def test_layer_norm_workspace():
     size = lambda **c: norm_backward("layer_norm_backward_workspace", **c)  # noqa: E731
     both = size()
     assert both > 0 and size(dweight=0) == size(dbias=0) == both // 2
-    assert size(dweight=0, dbias=0) == 0 and size(rows=4) == 0 and size(dim=0) == g.ERR_DIM
+    assert size(dweight=0, dbias=0) == 0 and size(rows=1024) == size(rows=4) == 0 and size(dim=0) == g.ERR_DIM
 
 
 @pytest.mark.parametrize("change,code", [
