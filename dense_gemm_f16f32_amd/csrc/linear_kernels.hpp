@@ -73,6 +73,11 @@ struct LinArgs {
   // its sums in W, a BM x BN block at (i splits + z) BM BN; lin_reduce adds the slices.
   float* W;
   int32_t first_split, splits, per_split;
+  // Column sums that are to be had of partial sums (see sum_block), by the workgroups behind the
+  // product's: a launch less.  Null: none.
+  const float* sum_part;
+  uint16_t* sum_out;
+  int32_t sum_n, sum_cols, sum_first;   // sum_first: workgroups of the product
 };
 
 // A workgroup's tile and k slice: the whole tiles first, then the slices, all tiles of slice 0,
@@ -927,23 +932,12 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, co
     S[3] = (char GK_LDS*)stage3;                                                 \
   }
 
-template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM,
-          bool HALVES>
-__global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
-  using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32, HALVES>;
-  LK_DECLARE_STAGES(NS, T::STAGE)
-  int m0, n0;
-  const Work k = work_of<BM, BN>(p, blockIdx.x);
-  corner_of<BM, BN>(p, k.tile, m0, n0);
-  staged_tile<T, NS, RD, AKM, BKM>(p, m0, n0, k, S);
-}
-
 // Sum over n partial rows of one block of 32 columns (see store_partial8), in order within a
 // thread and then over the 32 threads of a column, 4 columns a thread of 256.
+typedef float4v SumLds[32][9];
 template <int TY>
 __device__ __forceinline__ void sum_block(const float* part, int n, int block, int cols,
-                                          uint16_t* out) {
-  __shared__ float4v s[32][9];
+                                          uint16_t* out, SumLds& s) {
   const int t = threadIdx.x, c = t & 7, r = t >> 3;
   const float* const q = part + (int64_t)block * n * 32 + c * 4;
   float4v v = {0.f, 0.f, 0.f, 0.f};
@@ -957,6 +951,29 @@ __device__ __forceinline__ void sum_block(const float* part, int n, int block, i
     for (int i = 0; i < 32; ++i) sum += s[i][t / 4][t % 4];
     out[block * 32 + t] = to_16(sum, TY);
   }
+}
+
+// The workgroups of a product's launch that add partial sums.
+template <int TY>
+__device__ __forceinline__ bool sums_done(const LinArgs& p, SumLds& s) {
+  if (p.sum_part == nullptr || (int)blockIdx.x < p.sum_first) return false;
+  sum_block<TY>(p.sum_part, p.sum_n, blockIdx.x - p.sum_first, p.sum_cols, p.sum_out, s);
+  return true;
+}
+
+template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM,
+          bool HALVES>
+__global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
+  using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32, HALVES>;
+  LK_DECLARE_STAGES(NS, T::STAGE)
+  if constexpr (!kBytes<TY>) {
+    __shared__ SumLds sums;
+    if (sums_done<TY>(p, sums)) return;
+  }
+  int m0, n0;
+  const Work k = work_of<BM, BN>(p, blockIdx.x);
+  corner_of<BM, BN>(p, k.tile, m0, n0);
+  staged_tile<T, NS, RD, AKM, BKM>(p, m0, n0, k, S);
 }
 
 // Both products of a small backward pass and the last step of its bias gradient in one launch:
@@ -985,7 +1002,8 @@ __global__ void __launch_bounds__(256) lin_pair(PairArgs p) {
     staged_tile<TB, 4, 3, false, false>(p.db, m0, n0, Work{h, -1, nullptr}, S);
     return;
   }
-  sum_block<TY>(p.part, p.groups, h - p.db.num_programs, p.cols, p.dbias);
+  __shared__ SumLds sums;
+  sum_block<TY>(p.part, p.groups, h - p.db.num_programs, p.cols, p.dbias, sums);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1287,6 +1305,9 @@ __device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, cons
 template <int TY, bool AKM, bool BKM>
 __global__ void __launch_bounds__(256) lin_ring(LinArgs p) {
   GK_DECLARE_RING()
+  if constexpr (!kBytes<TY>) {
+    if (sums_done<TY>(p, *(SumLds*)slot0)) return;
+  }
   int m0, n0;
   const Work k = work_of<256, 256>(p, blockIdx.x);
   corner_of<256, 256>(p, k.tile, m0, n0);

@@ -64,7 +64,7 @@ void launch_reduce(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
 
 template <int TY>
 hipError_t launch_type(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)g.grid());
+  const dim3 grid((uint32_t)(g.grid() + (a.sum_part ? (a.sum_cols + 31) / 32 : 0)));
   if (g.path == kPathSkinnyK) {
     if (a.K < (kBytes<TY> ? 16 : 8)) {   // such rows need no more than one wave
       if (g.cols == 16)

@@ -296,13 +296,15 @@ LinArgs part_args(const LinArgs& whole, const Part& t, void* ws) {
   p.first_split = (int32_t)g.whole;
   p.splits = g.splits;
   p.per_split = g.per_split;
+  p.sum_first = (int32_t)g.grid();
   return p;
 }
 
 int launch(int64_t type, const Product& q, const LinArgs& whole, void* ws, void* stream) {
   const hipStream_t s = (hipStream_t)stream;
   for (int i = 0; i < q.parts; ++i) {
-    const LinArgs p = part_args(whole, q.part[i], ws);
+    LinArgs p = part_args(whole, q.part[i], ws);
+    if (i > 0) p.sum_part = nullptr;   // the first part's launch has done them
     const GemmPlan& g = q.part[i].g;
     const hipError_t e = type == LINEAR_NORM_F16    ? lk::launch_type<lk::kF16>(g, p, s)
                          : type == LINEAR_NORM_BF16 ? lk::launch_type<lk::kBF16>(g, p, s)
@@ -311,6 +313,13 @@ int launch(int64_t type, const Product& q, const LinArgs& whole, void* ws, void*
     if (e != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   return GEMM_F16F32_OK;
+}
+
+void carry_sums(LinArgs* p, const float* part, int n, int64_t cols, void* out) {
+  p->sum_part = part;
+  p->sum_n = n;
+  p->sum_cols = (int32_t)cols;
+  p->sum_out = (uint16_t*)out;
 }
 
 int check_workspace(const void* ws, int64_t have, int64_t need) {
@@ -383,6 +392,8 @@ int plan_forward(linear_forward_args& x, packed8_matrix* pre, ForwardPlan* f) {
 // ---- linear_backward ----------------------------------------------------------------------------
 struct BackwardPlan {
   bool dact;                 // the element-wise pass runs
+  bool copy;                 // ... and copies dc to aligned rows, for want of an activation
+  int carry;                 // dbias's last step goes with a product's launch: 1 da's, 2 db's; 0: not
   bool pair;                 // the products and dbias's last step go in one launch
   bool small;                // ... and the element-wise pass as well
   Operand b, a, dt;          // b as da's right operand; a and dpre as db's
@@ -456,7 +467,15 @@ int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
 
   // the element-wise pass: dpre (rows on 128-byte lines), and blocks of rows for its column sums
   f->dact = x.n > 0 && ((act && x.m > 0) || x.dbias);
-  if (f->dact && act) {
+  const bool to_da = x.da && x.m > 0 && x.k > 0, to_db = x.db && x.k > 0 && x.n > 0;
+  // Rows of dc that start off 16-byte boundaries slow the products' loads; where a pass over dc or one
+  // beside it runs anyway, and k pays for it, dc is copied as an activation's dpre would be.  In us,
+  // both products read in place / copied: m x n x k 2047 x 1025 x 4097 84 / 72, 1000 x 2001 x 999
+  // 28 / 27, 4095 x 4097 x 1023 115 / 105, for 2, 2 and 13 of copying.
+  f->copy = !act && x.m > 1 && x.n > 0 && to_da && to_db && x.k >= 2048 && (f->dact || a8) &&
+            (((uintptr_t)x.dc | (uintptr_t)(x.dc_row * 2)) & 15);
+  f->dact |= f->copy;
+  if (f->dact && (act || f->copy)) {
     f->ldd = round_up(x.n, 64);
     f->dpre_bytes = round_up(x.m * f->ldd * 2, 256);
   }
@@ -474,14 +493,14 @@ int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
       f->part_bytes = round_up(partial_bytes(f->row_blocks, x.n), 256);
     }
   }
-  const int64_t ldd = act ? f->ldd : x.dc_row;
-  if (x.da && x.m > 0 && x.k > 0) {
+  const int64_t ldd = act || f->copy ? f->ldd : x.dc_row;
+  if (to_da) {
     const Operand d = {x.dc, ldd, true};
     rc = plan_product(x.type, x.m, x.k, x.n, d, f->b, false, &f->qa);
     if (rc != 0) return rc;
     if (f->qa.w_bytes > f->w_bytes) f->w_bytes = f->qa.w_bytes;
   }
-  if (x.db && x.k > 0 && x.n > 0) {
+  if (to_db) {
     f->dt = {x.dc, ldd, false};
     rc = f->db_cols ? plan_product(x.type, x.n, x.k, x.m, f->dt, f->a, false, &f->qb)
                     : plan_product(x.type, x.k, x.n, x.m, f->a, f->dt, false, &f->qb);
@@ -530,6 +549,12 @@ int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
       }
     }
   }
+  // Else the bias gradient's last step goes with the first product on tiles.
+  auto carries = [&](const Product& q) {
+    return q.parts > 0 && q.part[0].g.path == lk::kPathTiles &&
+           (q.part[0].g.grid() + cdiv(x.n, 32)) * 256 < kThreads;
+  };
+  if (!f->pair && f->part_bytes > 0) f->carry = carries(f->qa) ? 1 : carries(f->qb) ? 2 : 0;
   return GEMM_F16F32_OK;
 }
 
@@ -963,6 +988,8 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
         d.pre = (const uint16_t*)x.pre;
         d.pre_row = x.pre_row;
       }
+    }
+    if (act || f.copy) {
       d.dpre = (uint16_t*)ws;
       d.dpre_row = f.ldd;
       dpre = ws;
@@ -991,7 +1018,7 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
     prepare(x.type, d, u, before, dim3((uint32_t)before), s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
-  if (last && !f.pair) {
+  if (last && !f.pair && f.carry == 0) {
     if (bf)
       launch_sum<lk::kBF16>(part, f.row_blocks, x.n, x.dbias, nullptr, s);
     else
@@ -1000,16 +1027,18 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
   }
   void* const W = ws ? ws + f.dpre_bytes + f.part_bytes + f.a_bytes : nullptr;
   LinArgs da = {}, db = {};
-  const int64_t ldd = act && !f.small ? f.ldd : x.dc_row;
+  const int64_t ldd = (act || f.copy) && !f.small ? f.ldd : x.dc_row;
   if (f.qa.parts > 0) {
     da = product(x.type, x.n, {dpre, ldd, true}, f.b);
     da.out = (uint16_t*)x.da;
+    if (f.carry == 1) carry_sums(&da, part, f.row_blocks, x.n, x.dbias);
     da.ldo = x.da_row;
   }
   if (f.qb.parts > 0) {
     const Operand d = {dpre, ldd, false};
     db = f.db_cols ? product(x.type, x.m, d, f.a) : product(x.type, x.m, f.a, d);
     db.out = (uint16_t*)x.db;
+    if (f.carry == 2) carry_sums(&db, part, f.row_blocks, x.n, x.dbias);
     db.ldo = f.db_cols ? x.db_col : x.db_row;
   }
   if (f.small) {

@@ -772,11 +772,12 @@ __global__ void __launch_bounds__(64 * NW) norm_bwd_long(NormBwdArgs p) {
 template <int TY>
 __global__ void __launch_bounds__(256) sum_partials(const float* part, int n, int first, int cols,
                                                     int blocks, uint16_t* out, uint16_t* more) {
+  __shared__ SumLds s;
   const int b = first + blockIdx.x;
   if (b < blocks)
-    sum_block<TY>(part, n, b, cols, out);
+    sum_block<TY>(part, n, b, cols, out, s);
   else
-    sum_block<TY>(part + (int64_t)blocks * n * 32, n, b - blocks, cols, more);
+    sum_block<TY>(part + (int64_t)blocks * n * 32, n, b - blocks, cols, more, s);
 }
 
 struct DactArgs {
@@ -784,7 +785,7 @@ struct DactArgs {
   const uint16_t* pre;   // null (and pre8 too): dpre is dc
   const uint8_t* pre8;   // pre in 8 bits, in its place
   const uint8_t* pre8_scale;
-  uint16_t* dpre;
+  uint16_t* dpre;        // null: not stored (without pre)
   float* part;           // partial column sums of every row block, or null
   uint16_t* sum;         // the column sums themselves (one row block), or null
   int64_t dc_row, pre_row, dpre_row, pre8_row, ps_row;
@@ -834,6 +835,7 @@ __device__ __forceinline__ void dact_rows(const DactArgs& p, int64_t r0, int row
       if (r >= rows) break;
       float v[8];
       unpack8(v, raw8_shift(d[i], n, back), TY);
+      if (PRE == 0 && p.dpre != nullptr) store8(dpre + r * p.dpre_row, v, n, TY);
       if constexpr (PRE != 0) {
         float x[8];
         if constexpr (PRE == kPre8)
