@@ -659,11 +659,13 @@ int64_t norm_part_bytes(int64_t rows, int64_t dim) {
 // 1024 rows, whose columns a workgroup takes in one or two steps.  In a graph / launched one by one,
 // in two launches and in one: 256 x 1021 7.1 / 9.4 and 4.6 / 5.9 us, 1024 x 512 5.9 / 9.1 and 5.9 /
 // 5.7, 1024 x 8192 28.3 / 27.6 and 24.1 / 23.8; past the rule 2048 x 512 7.2 / 8.9 and 12.3 / 12.1.
-bool norm_small(int64_t rows, int64_t dim) {
-  return rows <= 1024 && dim <= 8192 && backward_sums(rows, dim) && rows > 0;
+// dx in dy's memory would be written while the sums still read it.
+bool norm_small(const layer_norm_backward_args& x) {
+  return x.rows <= 1024 && x.dim <= 8192 && backward_sums(x.rows, x.dim) && x.rows > 0 &&
+         x.dx != x.dy;
 }
 int64_t norm_backward_bytes(const layer_norm_backward_args& x) {
-  if (norm_small(x.rows, x.dim)) return 0;
+  if (norm_small(x)) return 0;
   return ((x.dweight != nullptr) + (x.dbias != nullptr)) * norm_part_bytes(x.rows, x.dim);
 }
 
@@ -767,7 +769,7 @@ int norm_backward_call(layer_norm_backward_args x, bool ln) {
   const hipStream_t s = (hipStream_t)x.stream;
   const bool bf = x.type == LINEAR_NORM_BF16;
   const int groups = backward_groups(x.rows, x.dim);
-  const bool small = ln && (x.dweight || x.dbias) && norm_small(x.rows, x.dim);
+  const bool small = ln && (x.dweight || x.dbias) && norm_small(x);
   const bool sums = !small && backward_sums(x.rows, x.dim);
   float* const part = (float*)x.workspace;
   if (groups > 0) {

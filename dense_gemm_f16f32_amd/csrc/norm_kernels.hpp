@@ -213,32 +213,33 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   const uint16_t* const x = p.x + row * p.x_row;
   const uint16_t* const res = p.res ? p.res + row * p.res_row : nullptr;
   uint16_t* const h = p.h ? p.h + row * p.h_row : nullptr;
-  const int c0 = threadIdx.x * 8;
-  const int steps = C > 0 ? C : (p.dim - 1) / STEP + 1;   // dim > 0; dim + STEP need not fit
+  const uint32_t c0 = threadIdx.x * 8, dim = p.dim;   // col and dim + STEP fit 32 bits
+  const auto left = [&](uint32_t col) { return (int)(dim - col); };   // columns from col on
+  const int steps = C > 0 ? C : (p.dim - 1) / STEP + 1;   // dim > 0
   float hv[CR][8], wv[CR][8], bv[CR][8];
   float own = 0.f, mean = 0.f, shift = 0.f;   // layer norm: the wave's mean, the row's, d - e_w
-  auto load_h = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
-    load8(v, x + col, p.dim - col, TY, back);
+  auto load_h = [&](uint32_t col, float (&v)[8]) __attribute__((always_inline)) {
+    load8(v, x + col, left(col), TY, back);
     if (res) {
       float r[8];
-      load8(r, res + col, p.dim - col, TY, back);
+      load8(r, res + col, left(col), TY, back);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += r[e];
     }
   };
-  auto load_bias = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
+  auto load_bias = [&](uint32_t col, float (&v)[8]) __attribute__((always_inline)) {
     if (LN && p.bias) {
-      load8(v, p.bias + col, p.dim - col, TY, back);
+      load8(v, p.bias + col, left(col), TY, back);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.f;
     }
   };
   // differences from the wave's mean; columns past dim stay 0
-  auto centre = [&](int col, float (&v)[8]) __attribute__((always_inline)) {
+  auto centre = [&](uint32_t col, float (&v)[8]) __attribute__((always_inline)) {
     if constexpr (LN) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = col + e < p.dim ? v[e] - own : 0.f;
+      for (int e = 0; e < 8; ++e) v[e] = e < left(col) ? v[e] - own : 0.f;
     }
   };
   float2v sum = {0.f, 0.f};   // of the values or differences (layer norm), of their squares
@@ -290,15 +291,15 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
 #pragma unroll
     for (int i = 0; i < C; ++i) load_h(c0 + i * STEP, hv[i]);
 #pragma unroll
-    for (int i = 0; i < C; ++i) load8(wv[i], p.weight + c0 + i * STEP, p.dim - c0 - i * STEP, TY, back);
+    for (int i = 0; i < C; ++i) load8(wv[i], p.weight + c0 + i * STEP, left(c0 + i * STEP), TY, back);
     if constexpr (LN) {
 #pragma unroll
       for (int i = 0; i < C; ++i) load_bias(c0 + i * STEP, bv[i]);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int col = c0 + i * STEP;
-      if (h && col < p.dim) store8(h + col, hv[i], p.dim - col, TY);
+      const uint32_t col = c0 + (uint32_t)i * STEP;
+      if (h && col < dim) store8(h + col, hv[i], left(col), TY);
     }
   }
   if constexpr (LN) {
@@ -343,12 +344,12 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   }
   // y of step i
   auto norm = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
-    const int col = c0 + i * STEP;
+    const uint32_t col = c0 + (uint32_t)i * STEP;
     float w[8], b[8];
     if constexpr (C == 0) {
       load_h(col, v);
       centre(col, v);
-      load8(w, p.weight + col, p.dim - col, TY, back);
+      load8(w, p.weight + col, left(col), TY, back);
       if constexpr (LN) load_bias(col, b);
     }
 #pragma unroll
@@ -375,19 +376,19 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   }
 #pragma unroll CR
   for (int i = 0; i < steps; ++i) {
-    const int col = c0 + i * STEP;
-    if (col >= p.dim) break;
+    const uint32_t col = c0 + (uint32_t)i * STEP;
+    if (col >= dim) break;
     float v[8];
     norm(i, v);
     if constexpr (OUT != kOut16)
-      store_row8<OUT>((uint8_t*)p.y + row * p.y_row + col, v, by, p.dim - col);
+      store_row8<OUT>((uint8_t*)p.y + row * p.y_row + col, v, by, left(col));
     else
-      store8((uint16_t*)p.y + row * p.y_row + col, v, p.dim - col, TY);
+      store8((uint16_t*)p.y + row * p.y_row + col, v, left(col), TY);
     // h may be x's or the residual's memory: without registers it is written last
     if constexpr (C == 0) {
       if (h) {
         load_h(col, v);
-        store8(h + col, v, p.dim - col, TY);
+        store8(h + col, v, left(col), TY);
       }
     }
   }
@@ -408,14 +409,15 @@ __global__ void __launch_bounds__(64 * NW) quantize_rows(QuantizeArgs p) {
   constexpr int STEP = 512 * NW, CR = C > 0 ? C : 1;
   const int64_t row = blockIdx.x;
   const uint16_t* const x = p.x + row * p.x_row;
-  const int c0 = threadIdx.x * 8;
+  const uint32_t c0 = threadIdx.x * 8, dim = p.dim;   // col and dim + STEP fit 32 bits
+  const auto left = [&](uint32_t col) { return (int)(dim - col); };   // columns from col on
   const int steps = C > 0 ? C : (p.dim - 1) / STEP + 1;
   float xv[CR][8];
   uint32_t m = 0u;
 #pragma unroll CR
   for (int i = 0; i < steps; ++i) {
-    const int col = c0 + i * STEP;
-    load8(xv[C > 0 ? i : 0], x + col, p.dim - col, TY, back);
+    const uint32_t col = c0 + (uint32_t)i * STEP;
+    load8(xv[C > 0 ? i : 0], x + col, left(col), TY, back);
     if constexpr (C == 0) m = max_bits8(xv[0], m);
   }
   if constexpr (C > 0) {
@@ -427,10 +429,10 @@ __global__ void __launch_bounds__(64 * NW) quantize_rows(QuantizeArgs p) {
   const Divisor by = divisor(scale);
 #pragma unroll CR
   for (int i = 0; i < steps; ++i) {
-    const int col = c0 + i * STEP;
-    if (col >= p.dim) break;
-    if constexpr (C == 0) load8(xv[0], x + col, p.dim - col, TY, back);
-    store_row8<OUT>(p.y + row * p.y_row + col, xv[C > 0 ? i : 0], by, p.dim - col);
+    const uint32_t col = c0 + (uint32_t)i * STEP;
+    if (col >= dim) break;
+    if constexpr (C == 0) load8(xv[0], x + col, left(col), TY, back);
+    store_row8<OUT>(p.y + row * p.y_row + col, xv[C > 0 ? i : 0], by, left(col));
   }
 }
 
