@@ -65,8 +65,10 @@ ASM_MFMA_KERNELS = ("mfma_ceiling",                         # the rate probe (bo
                     "gemm_genericILi256ELi256ELb")          # gemm_generic, 256 x 256 tiles
 
 
-# The linear layer's 256 x 256 tile on int8 operands.
-ASM_INT_MFMA_KERNELS = ("lin_i8_ring",)
+# The linear layer's 256 x 256 tile on int8 operands, and with more to do beside the product: packing
+# the value before the activation (four storage orders of two 16-bit types, e4m3, int8), adding up
+# column sums (two orders of two types).
+ASM_MORE_MFMA_KERNELS = ("lin_more_ring",)
 
 
 def _asm_mfma_kernel(name: str, kernels=ASM_MFMA_KERNELS) -> bool:
@@ -191,8 +193,8 @@ def _refuse_private_arrays(so_path: str) -> None:
 
 def _check_linear_norm(so_path: str) -> None:
     _refuse_private_arrays(so_path)
-    if check_mfma_waits(so_path, ASM_INT_MFMA_KERNELS) != 1:
-        raise RuntimeError("the int8 tile's asm-MFMA kernel was not found to check")
+    if check_mfma_waits(so_path, ASM_MORE_MFMA_KERNELS) != 15:
+        raise RuntimeError("the large tile's other asm-MFMA kernels were not found to check")
 
 
 def build_linear_norm(extra=()) -> str:

@@ -418,10 +418,14 @@ __device__ __forceinline__ float sum_add(float v, float w) {
   else
     return v + w;
 }
+// What a product's launch does besides the product; kernels of their own, so that a plain one is not
+// longer for it: nothing, pack what stands before the activation (pre8), or add up column sums.
+enum { kPlain, kPack, kSums };
 // Whether a lane takes part in what finish8 does: columns that do not exist still belong to a
 // block of the checkpoint.
+template <int MORE>
 __device__ __forceinline__ bool takes_part(const LinArgs& p, int row, int col) {
-  return row < p.M && (col < p.N || p.pre8 != nullptr);
+  return row < p.M && (col < p.N || MORE == kPack);
 }
 __device__ __forceinline__ void put_pre8(const LinArgs& p, int64_t row, int col, const float (&v)[8],
                                          int n, int ot) {
@@ -433,7 +437,7 @@ __device__ __forceinline__ void put_pre8(const LinArgs& p, int64_t row, int col,
   store_bytes8(p.pre8 + row * p.ldp8 + col, b.lo, b.hi, n);
   if ((col & 31) == 0) p.pre8_scale[row * p.ldps + (col >> 5)] = (uint8_t)b.scale;
 }
-template <int TY>
+template <int TY, int MORE>
 __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, float (&v)[8],
                                         const Columns& c) {
   const int ot = kBytes<TY> ? p.out_type : TY;
@@ -449,7 +453,7 @@ __device__ __forceinline__ void finish8(const LinArgs& p, int row, int col, floa
     for (int e = 0; e < 8; ++e) v[e] += c.bias[e];
   }
   if (p.pre) store8(p.pre + (int64_t)row * p.ldp + col, v, c.n, ot);
-  if (p.pre8) {
+  if constexpr (MORE == kPack) {
     put_pre8(p, row, col, v, c.n, ot);
     if (c.n <= 0) return;
   }
@@ -639,7 +643,7 @@ struct Slab {
   static constexpr int U = ITERS < 4 ? ITERS : 4;   // rows of a lane in flight
 };
 
-template <class T>
+template <class T, int MORE>
 __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc (&acc)[T::TM][T::TN],
                                          int m0, int n0, int wm, int wn, int lane,
                                          char GK_LDS* slab, float* W) {   // W: a slice's block, or null
@@ -698,14 +702,28 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
         u32x4 res[U];
         float sa[U];
         const int row = row_t + i * S::ROWS;
+        auto row_of = [&](int u) __attribute__((always_inline)) {
+          const int64_t r = row + u * S::ROWS;
+          return !INSIDE && r >= p.M ? (int64_t)p.M - 1 : r;
+        };
+        // one branch for all of a lane's loads: after each the compiler would wait for them
+        if (p.res) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint16_t* const at = p.res + row_of(u) * p.ldr + col;
+            res[u] = INSIDE ? (u32x4)*(const u32x4_any*)at : raw8_load(at, c.n, p.N >= 8);
+          }
+        }
+        if (kBytes<T::TY>) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) sa[u] = 1.f;
+          if (p.scale_a) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) sa[u] = p.scale_a[row_of(u)];
+          }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          int64_t r = row + u * S::ROWS;
-          if (!INSIDE && r >= p.M) r = p.M - 1;
-          if (kBytes<T::TY>) sa[u] = p.scale_a ? p.scale_a[r] : 1.f;
-          if (p.res)
-            res[u] = INSIDE ? (u32x4)*(const u32x4_any*)(p.res + r * p.ldr + col)
-                            : raw8_load(p.res + r * p.ldr + col, c.n, p.N >= 8);
           const float GK_LDS* const q = sr + (i + u) * S::ROWS * S::LDW;
           const float4v lo = *(const float4v GK_LDS*)q, hi = *(const float4v GK_LDS*)(q + 4);
 #pragma unroll
@@ -731,7 +749,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
           }
         };
         if (p.pre) put(p.pre, p.ldp);
-        if (p.pre8) {
+        if constexpr (MORE == kPack) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             float v[8];
@@ -795,7 +813,7 @@ __device__ __forceinline__ void corner_of(const LinArgs& p, int tile, int& m0, i
 // TB/s); 128 x 128 with 2 stages, two workgroups a CU, where 256 x 256 tiles leave CUs idle (2048 x
 // 4096 x 4096 bf16: 62 us, 1.11 PFLOP/s; 256 x 256 71 us in two slices of k).
 // ---------------------------------------------------------------------------------------
-template <class T, int NS, int RD, bool AKM, bool BKM>
+template <class T, int NS, int RD, bool AKM, bool BKM, int MORE = kPlain>
 __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, const Work& k,
                                             char GK_LDS* const (&S)[NS]) {
   using OA = typename T::OA;
@@ -913,7 +931,7 @@ __device__ __forceinline__ void staged_tile(const LinArgs& p, int m0, int n0, co
     if (w % NS == j) slab_at = at;
   }
   char GK_LDS* const slab = (char GK_LDS*)(uintptr_t)slab_at + (w / NS) * Slab<T>::BYTES;
-  epilogue<T>(p, acc, m0, n0, wm, wn, lane, slab, k.w);
+  epilogue<T, MORE>(p, acc, m0, n0, wm, wn, lane, slab, k.w);
 }
 
 // The NS LDS stages of a staged tile as separate objects (a refill of one is then seen not to
@@ -962,18 +980,18 @@ __device__ __forceinline__ bool sums_done(const LinArgs& p, SumLds& s) {
 }
 
 template <int TY, int BM, int BN, int BK, int NS, int RD, int WM, int WN, bool AKM, bool BKM,
-          bool HALVES>
+          bool HALVES, int MORE>
 __global__ void __launch_bounds__(64 * WM * WN) lin_staged(LinArgs p) {
   using T = Tile<TY, BM, BN, BK, AKM, BKM, WM, WN, 32, HALVES>;
   LK_DECLARE_STAGES(NS, T::STAGE)
-  if constexpr (!kBytes<TY>) {
+  if constexpr (MORE == kSums) {
     __shared__ SumLds sums;
     if (sums_done<TY>(p, sums)) return;
   }
   int m0, n0;
   const Work k = work_of<BM, BN>(p, blockIdx.x);
   corner_of<BM, BN>(p, k.tile, m0, n0);
-  staged_tile<T, NS, RD, AKM, BKM>(p, m0, n0, k, S);
+  staged_tile<T, NS, RD, AKM, BKM, MORE>(p, m0, n0, k, S);
 }
 
 // Both products of a small backward pass and the last step of its bias gradient in one launch:
@@ -1145,7 +1163,7 @@ __device__ __forceinline__ void small_tile(const LinArgs& p, const SmallArgs& a,
     }
     __syncthreads();
   }
-  epilogue<T>(p, acc, m0, n0, wm, wn, lane, smem + w * Slab<T>::BYTES, nullptr);
+  epilogue<T, kPlain>(p, acc, m0, n0, wm, wn, lane, smem + w * Slab<T>::BYTES, nullptr);
 }
 
 // BKM: b as da's operand is k-contiguous.  COLS: db is column-major (its transpose computed).
@@ -1172,7 +1190,7 @@ __global__ void __launch_bounds__(256) lin_small_bwd(SmallArgs p) {
 // us (1.36 - 1.44 PFLOP/s, MFMA busy 72 %), e4m3 with bias and silu 398 - 423 us (2.6 - 2.76), no
 // LDS bank conflicts.
 // ---------------------------------------------------------------------------------------
-template <int TY, bool AKM, bool BKM>
+template <int TY, bool AKM, bool BKM, int MORE>
 __device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, const Work& k,
                                           char GK_LDS* const (&SA)[2],
                                           char GK_LDS* const (&SB)[3]) {
@@ -1299,33 +1317,34 @@ __device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, cons
   if (w == 1) slab = SA[1];
   if (w == 2) slab = SB[0];
   if (w == 3) slab = SB[1];
-  epilogue<T>(p, acc, m0, n0, wm, wn, lane, slab, k.w);
+  epilogue<T, MORE>(p, acc, m0, n0, wm, wn, lane, slab, k.w);
 }
 
-template <int TY, bool AKM, bool BKM>
-__global__ void __launch_bounds__(256) lin_ring(LinArgs p) {
+template <int TY, bool AKM, bool BKM, int MORE>
+__device__ __forceinline__ void ring(const LinArgs& p) {
   GK_DECLARE_RING()
-  if constexpr (!kBytes<TY>) {
+  if constexpr (MORE == kSums) {
     if (sums_done<TY>(p, *(SumLds*)slot0)) return;
   }
   int m0, n0;
   const Work k = work_of<256, 256>(p, blockIdx.x);
   corner_of<256, 256>(p, k.tile, m0, n0);
-  ring_tile<TY, AKM, BKM>(p, m0, n0, k, SA, SB);
+  ring_tile<TY, AKM, BKM, MORE>(p, m0, n0, k, SA, SB);
 }
-// The same on int8 operands.
-__global__ void __launch_bounds__(256) lin_i8_ring(LinArgs p) {
-  GK_DECLARE_RING()
-  int m0, n0;
-  const Work k = work_of<256, 256>(p, blockIdx.x);
-  corner_of<256, 256>(p, k.tile, m0, n0);
-  ring_tile<kI8, true, true>(p, m0, n0, k, SA, SB);
+template <int TY, bool AKM, bool BKM>
+__global__ void __launch_bounds__(256) lin_ring(LinArgs p) {
+  ring<TY, AKM, BKM, kPlain>(p);
+}
+// The same on int8 operands, or with more to do.
+template <int TY, bool AKM, bool BKM, int MORE>
+__global__ void __launch_bounds__(256) lin_more_ring(LinArgs p) {
+  ring<TY, AKM, BKM, MORE>(p);
 }
 
 // The k slices of the split tiles added in order, then the epilogue; a thread per 8 columns, 256
 // threads a workgroup, PER workgroups a BM x BN tile (the last one not always full).  Latency
 // bounds it: 3 - 5 us.
-template <int TY, int BM, int BN>
+template <int TY, int BM, int BN, int MORE>
 __global__ void __launch_bounds__(256) lin_reduce(LinArgs p) {
   constexpr int Q = BN / 8, PER = (BM * Q + 255) / 256;
   const int i = blockIdx.x / PER, t = (blockIdx.x - i * PER) * 256 + threadIdx.x;
@@ -1333,7 +1352,7 @@ __global__ void __launch_bounds__(256) lin_reduce(LinArgs p) {
   int m0, n0;
   corner_of<BM, BN>(p, p.first_split + i, m0, n0);
   const int r = t / Q, c = (t - r * Q) * 8, row = m0 + r, col = n0 + c;
-  if (!takes_part(p, row, col)) return;
+  if (!takes_part<MORE>(p, row, col)) return;
   const float* w = p.W + (int64_t)i * p.splits * (BM * BN) + r * BN + c;
   float4v lo = *(const float4v*)w, hi = *(const float4v*)(w + 4);
 #pragma unroll 4
@@ -1347,7 +1366,7 @@ __global__ void __launch_bounds__(256) lin_reduce(LinArgs p) {
     }
   }
   float f[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-  finish8<TY>(p, row, col, f, load_columns<TY>(p, col));
+  finish8<TY, MORE>(p, row, col, f, load_columns<TY>(p, col));
 }
 
 }  // namespace lk

@@ -30,83 +30,102 @@ struct GemmPlan {
   int64_t grid() const { return whole + (programs - whole) * splits; }
 };
 
-template <int TY, bool AKM, bool BKM, bool HALVES>
+template <int TY, bool AKM, bool BKM, bool HALVES, int MORE>
 void launch_staged(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
   // operands of a panel are read as many k steps ahead as a panel of the type has, less one
   constexpr int RD = TY == kE4M3 ? 1 : 3;
   if (g.tile == kTile128)
-    hipLaunchKernelGGL((lin_staged<TY, 128, 128, 64, 2, RD, 2, 2, AKM, BKM, HALVES>), grid,
+    hipLaunchKernelGGL((lin_staged<TY, 128, 128, 64, 2, RD, 2, 2, AKM, BKM, HALVES, MORE>), grid,
                        dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((lin_staged<TY, 64, 64, 64, 4, RD, 2, 2, AKM, BKM, HALVES>), grid,
+    hipLaunchKernelGGL((lin_staged<TY, 64, 64, 64, 4, RD, 2, 2, AKM, BKM, HALVES, MORE>), grid,
                        dim3(256), 0, s, a);
 }
 
-template <int TY, bool AKM, bool BKM>
+template <int TY, bool AKM, bool BKM, int MORE>
 void launch_tile(const GemmPlan& g, const LinArgs& a, dim3 grid, hipStream_t s) {
   if (g.tile == kTile256) {
-    if constexpr (TY == kI8)
-      hipLaunchKernelGGL(lin_i8_ring, grid, dim3(256), 0, s, a);
+    if constexpr (TY == kI8 || MORE != kPlain)
+      hipLaunchKernelGGL((lin_more_ring<TY, AKM, BKM, MORE>), grid, dim3(256), 0, s, a);
     else
       hipLaunchKernelGGL((lin_ring<TY, AKM, BKM>), grid, dim3(256), 0, s, a);
-  } else if (TY == kE4M3 && a.K <= kHalvesK)
-    launch_staged<TY, AKM, BKM, TY == kE4M3>(g, a, grid, s);
-  else
-    launch_staged<TY, AKM, BKM, false>(g, a, grid, s);
+  } else if (TY == kE4M3 && a.K <= kHalvesK) {
+    launch_staged<TY, AKM, BKM, TY == kE4M3, MORE>(g, a, grid, s);
+  } else {
+    launch_staged<TY, AKM, BKM, false, MORE>(g, a, grid, s);
+  }
 }
 
-template <int TY, int BM, int BN>
+template <int TY, int BM, int BN, int MORE>
 void launch_reduce(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
   constexpr int PER = (BM * BN / 8 + 255) / 256;
-  hipLaunchKernelGGL((lin_reduce<TY, BM, BN>), dim3((uint32_t)((g.programs - g.whole) * PER)),
-                     dim3(256), 0, s, a);
+  hipLaunchKernelGGL((lin_reduce<TY, BM, BN, MORE>),
+                     dim3((uint32_t)((g.programs - g.whole) * PER)), dim3(256), 0, s, a);
 }
 
-template <int TY>
-hipError_t launch_type(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)(g.grid() + (a.sum_part ? (a.sum_cols + 31) / 32 : 0)));
+// MORE: see lin_staged; a launch that adds up column sums as well is da's product, whose first
+// operand is k-contiguous.
+template <int TY, int MORE>
+hipError_t launch_more(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
+  const dim3 grid((uint32_t)(g.grid() + (MORE == kSums ? (a.sum_cols + 31) / 32 : 0)));
   if (g.path == kPathSkinnyK) {
-    if (a.K < (kBytes<TY> ? 16 : 8)) {   // such rows need no more than one wave
-      if (g.cols == 16)
-        hipLaunchKernelGGL((lin_skinny_k<TY, 1, 1, true>), grid, dim3(64), 0, s, a);
-      else
-        hipLaunchKernelGGL((lin_skinny_k<TY, 2, 1, true>), grid, dim3(64), 0, s, a);
-    } else if (g.cols == 16)
-      hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8, false>), grid, dim3(512), 0, s, a);
-    else if (g.cols == 32)
-      hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8, false>), grid, dim3(512), 0, s, a);
-    else
-      hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8, false>), grid, dim3(512), 0, s, a);
+    if constexpr (MORE != kSums) {
+      if (a.K < (kBytes<TY> ? 16 : 8)) {   // such rows need no more than one wave
+        if (g.cols != 16)
+          hipLaunchKernelGGL((lin_skinny_k<TY, 2, 1, true, MORE>), grid, dim3(64), 0, s, a);
+        else if constexpr (MORE == kPlain)
+          hipLaunchKernelGGL((lin_skinny_k<TY, 1, 1, true, MORE>), grid, dim3(64), 0, s, a);
+      } else if (g.cols == 64) {
+        hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8, false, MORE>), grid, dim3(512), 0, s, a);
+      } else if (g.cols == 32) {
+        hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8, false, MORE>), grid, dim3(512), 0, s, a);
+      } else if constexpr (MORE == kPlain) {   // a packed block takes 32 columns
+        hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8, false, MORE>), grid, dim3(512), 0, s, a);
+      }
+    }
   } else if (g.path == kPathSkinnyN) {
-    if constexpr (!kBytes<TY>) {
-      hipLaunchKernelGGL((lin_skinny_n<TY, 4, 8>), grid, dim3(512), 0, s, a);
+    if constexpr (!kBytes<TY> && MORE != kSums) {
+      hipLaunchKernelGGL((lin_skinny_n<TY, 4, 8, MORE>), grid, dim3(512), 0, s, a);
     }
   } else if constexpr (kBytes<TY>) {
-    launch_tile<TY, true, true>(g, a, grid, s);
+    launch_tile<TY, true, true, MORE>(g, a, grid, s);
   } else if (g.akm) {
     if (g.bkm)
-      launch_tile<TY, true, true>(g, a, grid, s);
+      launch_tile<TY, true, true, MORE>(g, a, grid, s);
     else
-      launch_tile<TY, true, false>(g, a, grid, s);
-  } else {
+      launch_tile<TY, true, false, MORE>(g, a, grid, s);
+  } else if constexpr (MORE != kSums) {
     if (g.bkm)
-      launch_tile<TY, false, true>(g, a, grid, s);
+      launch_tile<TY, false, true, MORE>(g, a, grid, s);
     else
-      launch_tile<TY, false, false>(g, a, grid, s);
+      launch_tile<TY, false, false, MORE>(g, a, grid, s);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.splits == 1) return e;
-  if (g.path != kPathTiles)
-    g.cols == 16   ? launch_reduce<TY, 16, 16>(g, a, s)
-    : g.cols == 32 ? launch_reduce<TY, 16, 32>(g, a, s)
-                   : launch_reduce<TY, 16, 64>(g, a, s);
-  else if (g.tile == kTile256)
-    launch_reduce<TY, 256, 256>(g, a, s);
-  else if (g.tile == kTile128)
-    launch_reduce<TY, 128, 128>(g, a, s);
-  else
-    launch_reduce<TY, 64, 64>(g, a, s);
+  constexpr int REST = MORE == kPack ? kPack : kPlain;
+  if (g.path != kPathTiles) {
+    if (g.cols == 64)
+      launch_reduce<TY, 16, 64, REST>(g, a, s);
+    else if (g.cols == 32)
+      launch_reduce<TY, 16, 32, REST>(g, a, s);
+    else if constexpr (REST == kPlain)
+      launch_reduce<TY, 16, 16, REST>(g, a, s);
+  } else if (g.tile == kTile256) {
+    launch_reduce<TY, 256, 256, REST>(g, a, s);
+  } else if (g.tile == kTile128) {
+    launch_reduce<TY, 128, 128, REST>(g, a, s);
+  } else {
+    launch_reduce<TY, 64, 64, REST>(g, a, s);
+  }
   return hipGetLastError();
+}
+template <int TY>
+hipError_t launch_type(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
+  if (a.pre8 != nullptr) return launch_more<TY, kPack>(g, a, s);
+  if constexpr (!kBytes<TY>) {
+    if (a.sum_part != nullptr) return launch_more<TY, kSums>(g, a, s);
+  }
+  return launch_more<TY, kPlain>(g, a, s);
 }
 
 template <int TY>

@@ -393,7 +393,7 @@ int plan_forward(linear_forward_args& x, packed8_matrix* pre, ForwardPlan* f) {
 struct BackwardPlan {
   bool dact;                 // the element-wise pass runs
   bool copy;                 // ... and copies dc to aligned rows, for want of an activation
-  int carry;                 // dbias's last step goes with a product's launch: 1 da's, 2 db's; 0: not
+  bool carry;                // dbias's last step goes with the launch of da's product
   bool pair;                 // the products and dbias's last step go in one launch
   bool small;                // ... and the element-wise pass as well
   Operand b, a, dt;          // b as da's right operand; a and dpre as db's
@@ -549,12 +549,10 @@ int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
       }
     }
   }
-  // Else the bias gradient's last step goes with the first product on tiles.
-  auto carries = [&](const Product& q) {
-    return q.parts > 0 && q.part[0].g.path == lk::kPathTiles &&
-           (q.part[0].g.grid() + cdiv(x.n, 32)) * 256 < kThreads;
-  };
-  if (!f->pair && f->part_bytes > 0) f->carry = carries(f->qa) ? 1 : carries(f->qb) ? 2 : 0;
+  // Else the bias gradient's last step goes with da's product on tiles.
+  f->carry = !f->pair && f->part_bytes > 0 && f->qa.parts > 0 &&
+             f->qa.part[0].g.path == lk::kPathTiles &&
+             (f->qa.part[0].g.grid() + cdiv(x.n, 32)) * 256 < kThreads;
   return GEMM_F16F32_OK;
 }
 
@@ -1020,7 +1018,7 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
     prepare(x.type, d, u, before, dim3((uint32_t)before), s);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
-  if (last && !f.pair && f.carry == 0) {
+  if (last && !f.pair && !f.carry) {
     if (bf)
       launch_sum<lk::kBF16>(part, f.row_blocks, x.n, x.dbias, nullptr, s);
     else
@@ -1033,14 +1031,13 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
   if (f.qa.parts > 0) {
     da = product(x.type, x.n, {dpre, ldd, true}, f.b);
     da.out = (uint16_t*)x.da;
-    if (f.carry == 1) carry_sums(&da, part, f.row_blocks, x.n, x.dbias);
+    if (f.carry) carry_sums(&da, part, f.row_blocks, x.n, x.dbias);
     da.ldo = x.da_row;
   }
   if (f.qb.parts > 0) {
     const Operand d = {dpre, ldd, false};
     db = f.db_cols ? product(x.type, x.m, d, f.a) : product(x.type, x.m, f.a, d);
     db.out = (uint16_t*)x.db;
-    if (f.carry == 2) carry_sums(&db, part, f.row_blocks, x.n, x.dbias);
     db.ldo = f.db_cols ? x.db_col : x.db_row;
   }
   if (f.small) {

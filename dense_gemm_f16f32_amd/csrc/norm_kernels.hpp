@@ -804,12 +804,12 @@ struct DactArgs {
 // doubles their work (at 4096^3 from 216 us to 432) to take a gradient's error, relative in the
 // norm, from 0.0023 to the 0.0017 of its own rounding in bf16 (f16: from 0.00029 to 0.00021).  The
 // column sums take the unrounded values.
-// WHOLE: the workgroup's 512 columns all exist, and nothing is spent on a row's end.
+// WHOLE: the workgroup's 512 columns all exist, and nothing is spent on a row's end.  R: rows of a
+// thread whose loads are in flight at once.
 constexpr int kPre16 = 1, kPre8 = 2;
-template <int TY, int PRE, bool WHOLE>
+template <int TY, int PRE, bool WHOLE, int R>
 __device__ __forceinline__ void dact_rows(const DactArgs& p, int64_t r0, int rows, int g, int col,
                                           float (&sum)[8]) {
-  constexpr int R = 4;   // rows of a thread whose loads are in flight at once
   const int n = WHOLE ? 8 : p.n - col;
   const bool back = WHOLE || p.n >= 8;
   const uint16_t* const dc = p.dc + r0 * p.dc_row + col;
@@ -863,18 +863,23 @@ __device__ __forceinline__ void dact_block(const DactArgs& p, int block, float (
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  auto work = [&](auto whole) __attribute__((always_inline)) {
+  auto work = [&](auto whole, auto r) __attribute__((always_inline)) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    constexpr int R = decltype(r)::value;
     if (p.pre8)
-      dact_rows<TY, kPre8, decltype(whole)::value>(p, r0, rows, g, col, sum);
+      dact_rows<TY, kPre8, WHOLE, R>(p, r0, rows, g, col, sum);
     else if (p.pre)
-      dact_rows<TY, kPre16, decltype(whole)::value>(p, r0, rows, g, col, sum);
+      dact_rows<TY, kPre16, WHOLE, R>(p, r0, rows, g, col, sum);
     else
-      dact_rows<TY, 0, decltype(whole)::value>(p, r0, rows, g, col, sum);
+      dact_rows<TY, 0, WHOLE, R>(p, r0, rows, g, col, sum);
   };
-  if (p.n - cb * 512 >= 512)
-    work(std::true_type{});
-  else if (n > 0)
-    work(std::false_type{});
+  if (p.rows_per_block == 4) {   // a row a thread
+    if (n > 0) work(std::false_type{}, std::integral_constant<int, 1>{});
+  } else if (p.n - cb * 512 >= 512) {
+    work(std::true_type{}, std::integral_constant<int, 4>{});
+  } else if (n > 0) {
+    work(std::false_type{}, std::integral_constant<int, 4>{});
+  }
   if (p.part == nullptr && p.sum == nullptr) return;
   if (g > 0) {
 #pragma unroll

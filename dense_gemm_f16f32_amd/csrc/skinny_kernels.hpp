@@ -60,7 +60,7 @@ __device__ __forceinline__ int4v chunk_shift(u32x4 v, uint32_t k, uint32_t K, bo
 
 // The waves' sums of a 16 x NC block, acc(c)[v] of lane l being row 4 (l / 16) + v, column
 // col_of(c, l % 16), added in wave order, then the epilogue (or the split's partial sums).
-template <int TY, int NW, int NC, int NB, class ColOf>
+template <int TY, int NW, int NC, int MORE, int NB, class ColOf>
 __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc)[NB],
                                            float GK_LDS* s, int n0, float* W, ColOf col_of) {
   constexpr int LDC = NC + 4;
@@ -74,7 +74,7 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
   // 8 columns of one row a thread; each output element is one thread's sum in wave order
   for (int t = tid; t < 16 * NC / 8; t += NW * 64) {
     const int row = t / (NC / 8), cc = t % (NC / 8) * 8, col = n0 + cc;
-    if (!takes_part(p, row, col)) continue;
+    if (!takes_part<MORE>(p, row, col)) continue;
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = 0.f;
@@ -87,7 +87,7 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
       *(float4v*)o = float4v{f[0], f[1], f[2], f[3]};
       *(float4v*)(o + 4) = float4v{f[4], f[5], f[6], f[7]};
     } else {
-      finish8<TY>(p, row, col, f, load_columns<TY>(p, col));
+      finish8<TY, MORE>(p, row, col, f, load_columns<TY>(p, col));
     }
   }
 }
@@ -99,7 +99,7 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
 // x 4096 bf16 26.9 us (5.0 TB/s), 16 x 16384 x 4096 30.1 us (4.5 TB/s), 16 x 8192 x 8192 e4m3 17.0
 // us (3.9 TB/s) and 4.3 for its two slices' join.  The same weights again and again stay partly in
 // the last-level cache: 24.7, 23.4 and 13.7 us.
-template <int TY, int NB, int NW, bool SHORT>
+template <int TY, int NB, int NW, bool SHORT, int MORE>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   constexpr int UE = kBytes<TY> ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk
   constexpr int NC = 16 * NB, U = 4;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
       mul(c, av, bv);
     }
   }
-  join_waves<TY, NW, NC>(p, acc, (float GK_LDS*)s, n0, wk.w,
+  join_waves<TY, NW, NC, MORE>(p, acc, (float GK_LDS*)s, n0, wk.w,
                          [](int c, int i) { return c * 16 + i; });
 }
 
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
 // 25.7 us (5.2 TB/s) with other weights in between, 21.5 with these partly in the last-level cache.
 // Rows of b at any 2-byte address: a k row's 128 bytes touch two lines, 1 x 8191 x 8191 38.8 us
 // (3.5 TB/s) either way.
-template <int TY, int CP, int NW>
+template <int TY, int CP, int NW, int MORE>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
   constexpr int NC = 16 * CP;
   typedef uint32_t vec __attribute__((ext_vector_type(CP / 2)));
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
       mul(chunk_shift<TY, false>(a[i], k, p.K, live), b[i]);
     }
   }
-  join_waves<TY, NW, NC>(p, acc, (float GK_LDS*)s, n0, wk.w,
+  join_waves<TY, NW, NC, MORE>(p, acc, (float GK_LDS*)s, n0, wk.w,
                          [](int c, int i) { return i * CP + c; });
 }
 
