@@ -692,9 +692,12 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
   auto finish = [&](auto inside) __attribute__((always_inline)) {
     constexpr bool INSIDE = decltype(inside)::value;
     constexpr int U = S::U;
-#pragma unroll
+    // one copy of what follows for all t: the accumulators' numbers have to be constants, the rest not
+#pragma unroll 1
     for (int t = 0; t < T::TM / RB; ++t) {
-      deposit(t);
+#pragma unroll
+      for (int x = 0; x < T::TM / RB; ++x)
+        if (x == t) deposit(x);
       const int row_t = row0 + t * 32;
 #pragma unroll 1
       for (int i = 0; i < S::ITERS; i += U) {
