@@ -14,7 +14,7 @@ struct TileShape {
 constexpr TileShape kTileShapes[kTiles] = {{256, 256}, {128, 128}, {64, 64}};
 constexpr int kTileDepth = 64;   // slots
 
-enum { kPathTiles, kPathSkinnyK, kPathSkinnyN };
+enum { kPathTiles, kPathSkinnyK, kPathSkinnyN, kPathSkinnyFlip };
 constexpr int kSkinnyRows = 16;   // rows of the skinny kernels' one MFMA block
 
 // How one matrix product runs: `programs` workgroups a pass over the result, of which those from
@@ -72,17 +72,20 @@ hipError_t launch_more(const GemmPlan& g, const LinArgs& a, hipStream_t s) {
     if constexpr (MORE != kSums) {
       if (a.K < (kBytes<TY> ? 16 : 8)) {   // such rows need no more than one wave
         if (g.cols != 16)
-          hipLaunchKernelGGL((lin_skinny_k<TY, 2, 1, true, MORE>), grid, dim3(64), 0, s, a);
+          hipLaunchKernelGGL((lin_skinny_k<TY, 2, 1, true, MORE, false>), grid, dim3(64), 0, s, a);
         else if constexpr (MORE == kPlain)
-          hipLaunchKernelGGL((lin_skinny_k<TY, 1, 1, true, MORE>), grid, dim3(64), 0, s, a);
+          hipLaunchKernelGGL((lin_skinny_k<TY, 1, 1, true, MORE, false>), grid, dim3(64), 0, s, a);
       } else if (g.cols == 64) {
-        hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8, false, MORE>), grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((lin_skinny_k<TY, 4, 8, false, MORE, false>), grid, dim3(512), 0, s, a);
       } else if (g.cols == 32) {
-        hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8, false, MORE>), grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((lin_skinny_k<TY, 2, 8, false, MORE, false>), grid, dim3(512), 0, s, a);
       } else if constexpr (MORE == kPlain) {   // a packed block takes 32 columns
-        hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8, false, MORE>), grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8, false, MORE, false>), grid, dim3(512), 0, s, a);
       }
     }
+  } else if (g.path == kPathSkinnyFlip) {
+    if constexpr (MORE != kSums)
+      hipLaunchKernelGGL((lin_skinny_k<TY, 1, 8, false, MORE, true>), grid, dim3(512), 0, s, a);
   } else if (g.path == kPathSkinnyN) {
     if constexpr (!kBytes<TY> && MORE != kSums) {
       hipLaunchKernelGGL((lin_skinny_n<TY, 4, 8, MORE>), grid, dim3(512), 0, s, a);

@@ -197,6 +197,21 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
       for (int64_t z = 2; z <= 16 && rest > 0 && rest * z <= slots && panels >= 4 * z; ++z)
         consider(rounds * slots, z);
     }
+    // At most 16 columns: a pass over a, 16 of its rows a workgroup.  In us, on tiles / so, m x n x k:
+    // bf16 256 x 1 x 4096 8.9 / 6.8, 4095 x 1 x 4096 12.1 / 9.0, 4096 x 16 x 512 5.4 / 3.6, int8 4095 x
+    // 16 x 4096 10.2 / 6.9; the other way round bf16 64 x 16 x 4096 8.5 / 9.3, which this rule
+    // takes, and 8192 x 16 x 8192 33.9 / 38.1, which it does not.
+    const int64_t bytes = M * (K * 2 / E);
+    if (N <= lk::kSkinnyRows && a.km && b.km && K >= 8 * E && cdiv(M, 16) * 512 < kThreads &&
+        (N <= 8 || bytes <= (64 << 20))) {
+      const double deep = (double)K / E * (0.95e-3 + 0.05e-3 * N), wide = (double)bytes / 4.5e6;
+      best = 2.6 + (deep > wide ? deep : wide);
+      chosen.path = lk::kPathSkinnyFlip;
+      chosen.cols = 16;
+      chosen.programs = cdiv(M, 16);
+      chosen.w_bytes = 0;
+      set_split(&chosen, 0, panels, 1, 0);
+    }
     if (best == 0.0) return GEMM_F16F32_ERR_TOO_LARGE;
     *g = chosen;
     g->cost = best;

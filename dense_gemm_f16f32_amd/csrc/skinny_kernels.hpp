@@ -1,6 +1,8 @@
 // Device code of the linear layer for few rows (at most 16: the tokens of a decode step).  The
 // product is then a pass over the weights b, which are read once, straight into registers; the
-// k range is divided among the waves of a workgroup, whose sums meet in LDS.
+// k range is divided among the waves of a workgroup, whose sums meet in LDS.  A result of at most
+// 16 columns (a sliver past the last whole tile, a narrow layer) is the same with the operands
+// exchanged: a pass over a.
 #pragma once
 
 #include "linear_kernels.hpp"
@@ -59,8 +61,9 @@ __device__ __forceinline__ int4v chunk_shift(u32x4 v, uint32_t k, uint32_t K, bo
 }
 
 // The waves' sums of a 16 x NC block, acc(c)[v] of lane l being row 4 (l / 16) + v, column
-// col_of(c, l % 16), added in wave order, then the epilogue (or the split's partial sums).
-template <int TY, int NW, int NC, int MORE, int NB, class ColOf>
+// col_of(c, l % 16), added in wave order, then the epilogue (or the split's partial sums).  FLIP: the
+// block's rows are columns of the result, its columns rows from n0 on.
+template <int TY, int NW, int NC, int MORE, bool FLIP, int NB, class ColOf>
 __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc)[NB],
                                            float GK_LDS* s, int n0, float* W, ColOf col_of) {
   constexpr int LDC = NC + 4;
@@ -71,6 +74,25 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
     for (int v = 0; v < 4; ++v)
       s[(w * 16 + 4 * (lane >> 4) + v) * LDC + col_of(c, lane & 15)] = acc[c][v];
   __syncthreads();
+  if constexpr (FLIP) {
+    // 8 columns of one row a thread, with the other 16 of a packed block
+    constexpr int Q = MORE == kPack ? 4 : 2;
+    for (int t = tid; t < NC * Q; t += NW * 64) {
+      const int i = t / Q, col = t % Q * 8, row = n0 + i;
+      if (!takes_part<MORE>(p, row, col)) continue;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 0.f;
+      if (col < 16) {
+#pragma unroll
+        for (int u = 0; u < NW; ++u)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = sum_add<TY>(f[e], s[(u * 16 + col + e) * LDC + i]);
+      }
+      finish8<TY, MORE>(p, row, col, f, load_columns<TY>(p, col));
+    }
+    return;
+  }
   // 8 columns of one row a thread; each output element is one thread's sum in wave order
   for (int t = tid; t < 16 * NC / 8; t += NW * 64) {
     const int row = t / (NC / 8), cc = t % (NC / 8) * 8, col = n0 + cc;
@@ -99,7 +121,7 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
 // x 4096 bf16 26.9 us (5.0 TB/s), 16 x 16384 x 4096 30.1 us (4.5 TB/s), 16 x 8192 x 8192 e4m3 17.0
 // us (3.9 TB/s) and 4.3 for its two slices' join.  The same weights again and again stay partly in
 // the last-level cache: 24.7, 23.4 and 13.7 us.
-template <int TY, int NB, int NW, bool SHORT, int MORE>
+template <int TY, int NB, int NW, bool SHORT, int MORE, bool FLIP>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   constexpr int UE = kBytes<TY> ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk
   constexpr int NC = 16 * NB, U = 4;
@@ -111,13 +133,17 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   corner_of<16, NC>(p, wk.tile, m0, n0);
   const int x = lane & 15, g = lane >> 4;
   // rows and columns that do not exist repeat the last one; their sums are not stored
-  const uint16_t* const pa = p.A + (int64_t)(x < p.M ? x : p.M - 1) * p.lda;
+  const uint16_t* const A = FLIP ? p.B : p.A;
+  const uint16_t* const B = FLIP ? p.A : p.B;
+  const int64_t lda = FLIP ? p.ldb : p.lda, ldb = FLIP ? p.lda : p.ldb;
+  const int M = FLIP ? p.N : p.M, N = FLIP ? p.M : p.N;
+  const uint16_t* const pa = A + (int64_t)(x < M ? x : M - 1) * lda;
   const uint16_t* pb[NB];
   float4v acc[NB];
 #pragma unroll
   for (int c = 0; c < NB; ++c) {
     const int col = n0 + 16 * c + x;
-    pb[c] = p.B + (int64_t)(col < p.N ? col : p.N - 1) * p.ldb;
+    pb[c] = B + (int64_t)(col < N ? col : N - 1) * ldb;
     acc[c] = float4v{0.f, 0.f, 0.f, 0.f};
   }
   auto mul = [&](int c, const int4v (&a)[2], const int4v (&b)[2]) __attribute__((always_inline)) {
@@ -177,8 +203,8 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
       mul(c, av, bv);
     }
   }
-  join_waves<TY, NW, NC, MORE>(p, acc, (float GK_LDS*)s, n0, wk.w,
-                         [](int c, int i) { return c * 16 + i; });
+  join_waves<TY, NW, NC, MORE, FLIP>(p, acc, (float GK_LDS*)s, n0, wk.w,
+                                     [](int c, int i) { return c * 16 + i; });
 }
 
 // b stored n-contiguous (row-major): 16 CP columns a workgroup.  Lane l takes CP consecutive
@@ -277,8 +303,8 @@ __global__ void __launch_bounds__(64 * NW) lin_skinny_n(LinArgs p) {
       mul(chunk_shift<TY, false>(a[i], k, p.K, live), b[i]);
     }
   }
-  join_waves<TY, NW, NC, MORE>(p, acc, (float GK_LDS*)s, n0, wk.w,
-                         [](int c, int i) { return i * CP + c; });
+  join_waves<TY, NW, NC, MORE, false>(p, acc, (float GK_LDS*)s, n0, wk.w,
+                                      [](int c, int i) { return i * CP + c; });
 }
 
 }  // namespace lk
