@@ -483,12 +483,13 @@ int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
   // the element-wise pass: dpre (rows on 128-byte lines), and blocks of rows for its column sums
   f->dact = x.n > 0 && ((act && x.m > 0) || x.dbias);
   const bool to_da = x.da && x.m > 0 && x.k > 0, to_db = x.db && x.k > 0 && x.n > 0;
-  // Rows of dc that start off 16-byte boundaries slow the products' loads; where a pass over dc or one
-  // beside it runs anyway, and k pays for it, dc is copied as an activation's dpre would be.  In us,
+  // Rows of dc that lie off 16-byte boundaries slow the products' loads; where a pass over dc or one
+  // beside it runs anyway, and k pays for it, dc is copied as an activation's dpre would be.  (By the
+  // stride alone: the workspace's size goes by it, and not by where dc lies.)  In us,
   // both products read in place / copied: m x n x k 2047 x 1025 x 4097 84 / 72, 1000 x 2001 x 999
   // 28 / 27, 4095 x 4097 x 1023 115 / 105, for 2, 2 and 13 of copying.
   f->copy = !act && x.m > 1 && x.n > 0 && to_da && to_db && x.k >= 2048 && (f->dact || a8) &&
-            (((uintptr_t)x.dc | (uintptr_t)(x.dc_row * 2)) & 15);
+            x.dc_row % 8 != 0;
   f->dact |= f->copy;
   if (f->dact && (act || f->copy)) {
     f->ldd = round_up(x.n, 64);

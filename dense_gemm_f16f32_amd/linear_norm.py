@@ -116,14 +116,14 @@ class Packed8(NamedTuple):
 
 def linear(a, b, bias=None, residual=None, *, activation="none", scale_a=None, scale_b=None,
            out_dtype=None, with_pre=False, pack_pre=False, out=None, stream=None):
-    """act(a @ b + bias) + residual on the GPU: fp32 sums, one rounding (float8_e4m3fn operands with more
-    than 16 rows and k above 512: the matrix instruction's own sums, off by up to 2^-17 of the sum
-    of the products' magnitudes at k = 1000).
+    """act(a @ b + bias) + residual on the GPU: fp32 sums, one rounding (float8_e4m3fn operands with
+    more than 16 rows and k above 512: the matrix instruction's own sums, off by up to 2^-17 of the
+    sum of the products' magnitudes at k = 1000; int8 operands: exact 32-bit integer sums).
 
     a (m, k) and b (k, n): float16 or bfloat16, each row- or column-major with any leading
-    dimension (a weight stored (n, k) is passed as `w.t()`); or float8_e4m3fn or int8 (exact sums, k up
-    to 131071), k-contiguous (a row-major, b column-major) with 16-byte aligned rows, and `scale_a` (m,) and `scale_b` (n,)
-    float32 factors of the rows and columns (1 if not given).  bias (n,), residual (m, n): of
+    dimension (a weight stored (n, k) is passed as `w.t()`); or float8_e4m3fn or int8 (k up to
+    131071), k-contiguous (a row-major, b column-major) with 16-byte aligned rows, and `scale_a`
+    (m,) and `scale_b` (n,) float32 factors of the rows and columns (1 if not given).  bias (n,), residual (m, n): of
     the output's type, which is the operands' (8-bit operands: `out_dtype`, bfloat16 if not
     given).  activation: none, relu, gelu, gelu_tanh or silu.  Returns the (m, n) result, or
     (result, pre) with `with_pre`, where pre is the value before the activation, which

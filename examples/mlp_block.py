@@ -1,12 +1,15 @@
 """A transformer block's MLP, trained and then served, on the linear layer's and norm's operators.
 
-    h = x + residual;  y = rms_norm(h);  out = act(y W_up^T + b_up) W_down^T + b_down + h
+    h = x + residual;  y = norm(h);  out = act(y W_up^T + b_up) W_down^T + b_down + h
 
-Training keeps what the backward pass needs (h, rstd, y, the pre-activation, the activation) and
-chains linear_backward and rms_norm_backward; the weights are updated by plain SGD.  Serving
-quantises the up-projection once, norms each token into 8 bits and reads the 8-bit weights.
+Training keeps what the backward pass needs (h, the norm's statistics, y, the pre-activation, the
+activation) and chains linear_backward and the norm's backward pass; the weights are updated by
+plain SGD.  With keep8 it keeps y and the pre-activation in 8 bits, and the activation not at all:
+2 bytes a hidden value and token become 1 and none.  Serving quantises the up-projection once (with
+int8 both projections), norms each token into 8 bits and reads the 8-bit weights.
 
     python examples/mlp_block.py [--dim 1024 --hidden 4096 --tokens 2048 --steps 40 --rate 0.002]
+                                 [--norm layer --keep8 --int8]
 """
 from __future__ import annotations
 
@@ -25,7 +28,8 @@ import dense_gemm_f16f32_amd as g  # noqa: E402
 class MLPBlock:
     """Parameters as (out, in) matrices; every method runs on torch's current stream."""
 
-    def __init__(self, dim, hidden, activation="gelu_tanh", dtype=torch.bfloat16, seed=0):
+    def __init__(self, dim, hidden, activation="gelu_tanh", dtype=torch.bfloat16, seed=0,
+                 norm="rms", keep8=False):
         gen = torch.Generator(device="cuda")
         gen.manual_seed(seed)
 
@@ -33,35 +37,56 @@ class MLPBlock:
             w = torch.randn((rows, cols), generator=gen, device="cuda") * cols ** -0.5
             return w.to(dtype)
 
-        self.activation = activation
+        self.activation, self.keep8 = activation, keep8
+        self.norm_bias = torch.zeros(dim, dtype=dtype, device="cuda") if norm == "layer" else None
         self.norm = torch.ones(dim, dtype=dtype, device="cuda")
         self.up, self.up_bias = weight(hidden, dim), torch.zeros(hidden, dtype=dtype, device="cuda")
         self.down, self.down_bias = weight(dim, hidden), torch.zeros(dim, dtype=dtype,
                                                                      device="cuda")
-        self.up8 = self.up8_scale = None
+        self.up8 = self.up8_scale = self.down8 = None
 
     def parameters(self):
-        return [self.norm, self.up, self.up_bias, self.down, self.down_bias]
+        p = [self.norm, self.up, self.up_bias, self.down, self.down_bias]
+        return p if self.norm_bias is None else p + [self.norm_bias]
+
+    def normed(self, x, residual, stats=False, out_dtype=None):
+        if self.norm_bias is None:
+            return g.rms_norm(x, self.norm, residual, with_rstd=stats, out_dtype=out_dtype)
+        return g.layer_norm(x, self.norm, self.norm_bias, residual, with_stats=stats,
+                            out_dtype=out_dtype)
 
     def forward(self, x, residual):
-        n = g.rms_norm(x, self.norm, residual, with_rstd=True)
+        n = self.normed(x, residual, stats=True)
         u, pre = g.linear(n.y, self.up.t(), self.up_bias, activation=self.activation,
-                          with_pre=True)
+                          with_pre=not self.keep8, pack_pre=self.keep8)
         out = g.linear(u, self.down.t(), self.down_bias, n.h)
+        if self.keep8:   # y in 8 bits, u not: it is the activation of pre
+            n, u = n._replace(y=g.pack8(n.y)), None
         return out, (n, pre, u)
 
     def backward(self, dout, kept):
         """(gradient of x and of the residual, gradients in parameters() order)."""
         n, pre, u = kept
-        du, d_down, d_down_bias = g.linear_backward(dout, u, self.down.t(), bias_grad=True)
+        du, d_down, d_down_bias = g.linear_backward(
+            dout, pre if self.keep8 else u, self.down.t(), bias_grad=True,
+            a_activation=self.activation if self.keep8 else "none")
         dy, d_up, d_up_bias = g.linear_backward(du, n.y, self.up.t(), pre,
                                                 activation=self.activation, bias_grad=True)
         # dout reaches h directly too, as the residual of the down-projection
-        dx, d_norm = g.rms_norm_backward(dy, n.h, self.norm, n.rstd, dh=dout)
-        return dx, [d_norm, d_up.t(), d_up_bias, d_down.t(), d_down_bias]
+        if self.norm_bias is None:
+            dx, d_norm = g.rms_norm_backward(dy, n.h, self.norm, n.rstd, dh=dout)
+            return dx, [d_norm, d_up.t(), d_up_bias, d_down.t(), d_down_bias]
+        dx, d_norm, d_norm_bias = g.layer_norm_backward(dy, n.h, self.norm, n.mean, n.rstd, dh=dout)
+        return dx, [d_norm, d_up.t(), d_up_bias, d_down.t(), d_down_bias, d_norm_bias]
 
-    def prepare_serving(self):
-        """The up-projection in 8 bits with a scale an output, rows on 16-byte boundaries."""
+    def prepare_serving(self, int8=False):
+        """The up-projection in 8 bits with a scale an output, rows on 16-byte boundaries; with int8
+        the down-projection as well."""
+        if int8:
+            up, self.down8 = g.quantize_rows(self.up), g.quantize_rows(self.down)
+            self.up8, self.up8_scale = up.values, up.scale
+            return
+        self.down8 = None
         w = self.up.float()
         rows, cols = w.shape
         amax = w.abs().amax(1)
@@ -71,9 +96,13 @@ class MLPBlock:
         self.up8 = buf[:, :cols]
 
     def serve(self, x, residual):
-        n = g.rms_norm(x, self.norm, residual, out_dtype=torch.float8_e4m3fn)
+        n = self.normed(x, residual, out_dtype=self.up8.dtype)
         u = g.linear(n.y, self.up8.t(), self.up_bias, activation=self.activation,
                      scale_a=n.scale, scale_b=self.up8_scale, out_dtype=x.dtype)
+        if self.down8 is not None:
+            u8 = g.quantize_rows(u)
+            return g.linear(u8.values, self.down8.values.t(), self.down_bias, n.h,
+                            scale_a=u8.scale, scale_b=self.down8.scale, out_dtype=x.dtype)
         return g.linear(u, self.down.t(), self.down_bias, n.h)
 
 
@@ -96,14 +125,17 @@ def main():
                         ("--steps", 40)):
         ap.add_argument(name, type=int, default=value)
     ap.add_argument("--rate", type=float, default=0.002)
+    ap.add_argument("--norm", choices=("rms", "layer"), default="rms")
+    ap.add_argument("--keep8", action="store_true", help="8-bit checkpoints")
+    ap.add_argument("--int8", action="store_true", help="serve in int8 instead of e4m3")
     a = ap.parse_args()
     torch.manual_seed(1)
     x, residual, target = (torch.randn((a.tokens, a.dim), device="cuda").bfloat16()
                            for _ in range(3))
-    block = MLPBlock(a.dim, a.hidden)
+    block = MLPBlock(a.dim, a.hidden, norm=a.norm, keep8=a.keep8)
     losses = train(block, x, residual, target, a.steps, a.rate)
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {a.steps} steps")
-    block.prepare_serving()
+    block.prepare_serving(a.int8)
     full, _ = block.forward(x[:1], residual[:1])
     eight = block.serve(x[:1], residual[:1])
     print(f"one token, 8-bit against 16-bit: relative difference "

@@ -44,10 +44,12 @@
  * mean.  int8 results cannot hold a NaN: a row with a NaN or an infinity has scale NaN.
  *
  * int8 operands are summed exactly in 32-bit integers, which bounds k by 131071, and the sum is
- * rounded to fp32 before it is scaled.  e4m3 operands: with up to 16 rows (m) or k up to 512 the values are multiplied as f16,
- * exactly.  Beyond, they go through the 8-bit matrix instruction, which rounds inside: measured
- * over random operands, a sum is off by up to 2^-17 of the sum of its products' magnitudes at k
- * = 1000.
+ * rounded to fp32 before it is scaled.
+ *
+ * e4m3 operands: with up to 16 rows (m) or k up to 512 (and in slivers of up to 16 columns) the
+ * values are multiplied as f16, exactly.  Beyond, they go through the 8-bit matrix instruction,
+ * which rounds inside: measured over random operands, a sum is off by up to 2^-17 of the sum of its
+ * products' magnitudes at k = 1000.
  *
  * Activations: none, relu, gelu (0.5 v (1 + erf(v / sqrt 2))), gelu_tanh (the tanh form of it),
  * silu (v / (1 + exp(-v))).  relu's slope at 0 is 0.
@@ -288,7 +290,8 @@ int linear_forward_packed(const linear_forward_args* args, const packed8_matrix*
 int linear_backward_packed(const linear_backward_args* args, const linear_kept* kept);
 
 /* Bytes of workspace that the call needs (0: none), or a negative error code.  The workspace
- * is 16-byte aligned; workspace, workspace_bytes and stream are not read. */
+ * is 16-byte aligned; workspace, workspace_bytes and stream are not read.  Of pointers it counts
+ * which are NULL, and in layer_norm_backward whether dx is dy. */
 int64_t linear_forward_workspace(const linear_forward_args* args);
 int64_t linear_backward_workspace(const linear_backward_args* args);
 int64_t rms_norm_backward_workspace(const rms_norm_backward_args* args);
