@@ -419,7 +419,8 @@ __device__ __forceinline__ float sum_add(float v, float w) {
     return v + w;
 }
 // What a product's launch does besides the product; kernels of their own, so that a plain one is not
-// longer for it: nothing, pack what stands before the activation (pre8), or add up column sums.
+// longer for it: nothing, pack what stands before the activation (pre8), or add up column sums (in a
+// backward pass, whose products have nothing else in their epilogue).
 enum { kPlain, kPack, kSums };
 // Whether a lane takes part in what finish8 does: columns that do not exist still belong to a
 // block of the checkpoint.
@@ -658,7 +659,11 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
   const int row0 = m0 + wm * T::WTM + rr;
   const bool whole = T::BM <= p.M - m0 && T::BN <= p.N - n0;
   const int ot = kBytes<T::TY> ? p.out_type : T::TY;
-  const Columns c = load_columns<T::TY>(p, col);
+  Columns c;
+  if constexpr (MORE == kSums)
+    c.n = p.N - col;
+  else
+    c = load_columns<T::TY>(p, col);
   const float GK_LDS* const sr = s + rr * S::LDW + cc;
   // block t of the slab's rows
   auto deposit = [&](int t) __attribute__((always_inline)) {
@@ -713,7 +718,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
           return !INSIDE && r >= p.M ? (int64_t)p.M - 1 : r;
         };
         // one branch for all of a lane's loads: after each the compiler would wait for them
-        if (p.res) {
+        if (MORE != kSums && p.res) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const uint16_t* const at = p.res + row_of(u) * p.ldr + col;
@@ -735,7 +740,10 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float v = sum_value<T::TY>(e < 4 ? lo[e & 3] : hi[e & 3]);
-            f[u * 8 + e] = kBytes<T::TY> ? v * sa[u] * c.sb[e] + c.bias[e] : v + c.bias[e];
+            if constexpr (MORE == kSums)
+              f[u * 8 + e] = v;
+            else
+              f[u * 8 + e] = kBytes<T::TY> ? v * sa[u] * c.sb[e] + c.bias[e] : v + c.bias[e];
           }
         }
         auto values = [&](float (&v)[8], int u) __attribute__((always_inline)) {
@@ -754,7 +762,7 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
               store8(base + r * ld + col, v, c.n, ot);
           }
         };
-        if (p.pre) put(p.pre, p.ldp);
+        if (MORE != kSums && p.pre) put(p.pre, p.ldp);
         if constexpr (MORE == kPack) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
@@ -764,8 +772,8 @@ __device__ __forceinline__ void epilogue(const LinArgs& p, const typename T::Acc
             put_pre8(p, r, col, v, INSIDE ? 8 : r < p.M ? c.n : 0, ot);
           }
         }
-        act_n(f, p.act);
-        if (p.res) {
+        if constexpr (MORE != kSums) act_n(f, p.act);
+        if (MORE != kSums && p.res) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             float r[8];
@@ -1033,7 +1041,8 @@ __global__ void __launch_bounds__(256) lin_pair(PairArgs p) {
 // ---------------------------------------------------------------------------------------
 // A small backward pass in one launch: both products on 64 x 64 tiles, with dpre = dc act'(pre)
 // made on the way into LDS by every workgroup that needs it (a few times over, which costs less
-// than a pass of its own and its launch) and rounded there to the operands' type (see lin_dact), and its column sums by the workgroups of db's first
+// than a pass of its own and its launch) and rounded there to the operands' type (see dact_rows),
+// and its column sums by the workgroups of db's first
 // tiles along k.  Panels go through registers, three ahead, and two LDS stages.
 // ---------------------------------------------------------------------------------------
 struct SmallArgs {
@@ -1191,10 +1200,10 @@ __global__ void __launch_bounds__(256) lin_small_bwd(SmallArgs p) {
 // The 256 x 256 tile (64 slots deep, 4 waves of 128 x 128): the panels in five 32 KiB LDS slots,
 // B's in a ring of three and A's in a ring of two, two k steps per panel, each scheduled by
 // hand -- see ring_tile in gemm_kernels.hpp, whose order of loads, reads and barriers this is.
-// 16-bit types: 64 MFMAs of 16x16x32 a step (int8: of 16x16x64); e4m3: 16 of 32x32x64, the same cycles.  Bound by the
-// matrix cores at the chip's power limit: 8192^3 bf16 with bias, gelu and pre-activation 764 - 809
-// us (1.36 - 1.44 PFLOP/s, MFMA busy 72 %), e4m3 with bias and silu 398 - 423 us (2.6 - 2.76), no
-// LDS bank conflicts.
+// 16-bit types: 64 MFMAs of 16x16x32 a step (int8: of 16x16x64); e4m3: 16 of 32x32x64, the same
+// cycles.  Bound by the matrix cores at the chip's power limit: 8192^3 bf16 with bias, gelu and pre-activation 764 - 809
+// us (1.36 - 1.44 PFLOP/s, MFMA busy 72 %), e4m3 with bias and silu 390 - 423 us (2.6 - 2.8), int8
+// 397 - 418 us (2.6 - 2.8), no LDS bank conflicts.
 // ---------------------------------------------------------------------------------------
 template <int TY, bool AKM, bool BKM, int MORE>
 __device__ __forceinline__ void ring_tile(const LinArgs& p, int m0, int n0, const Work& k,

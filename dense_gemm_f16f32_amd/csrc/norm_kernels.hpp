@@ -189,7 +189,8 @@ __device__ __forceinline__ uint32_t max_bits8(const float (&v)[8], uint32_t m) {
 
 // One pass: the row's statistics, the 8-bit scale and y come from the row in registers.  HBM bounds
 // it: 8192 x 8192 bf16 with residual to e4m3 88 us (5.3 TB/s), 4095 x 4093 f16 29 us (4.6 TB/s; 24.5
-// where the rows are partly in the last-level cache).
+// where the rows are partly in the last-level cache); the layer norm 8192 x 8192 bf16 100 us (5.4 TB/s,
+// 106 with three barriers and sums through LDS), one row of 4096 to e4m3 3.6.
 // One row a workgroup of 64 NW threads, 8 columns a thread at a time.  C > 0: rows of at most
 // 512 NW C columns, held in registers.  C == 0: longer rows, read again for each step that
 // needs them.
@@ -394,7 +395,8 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
   }
 }
 
-// Rows in 8 bits with a scale a row, as the norm's: one row a workgroup.
+// Rows in 8 bits with a scale a row, as the norm's: one row a workgroup, held in registers.  HBM bounds
+// it: 8192 x 8192 bf16 to int8 30 - 40 us, 4095 x 4093 f16 10.6 (4.7 TB/s).
 struct QuantizeArgs {
   const uint16_t* x;
   uint8_t* y;
@@ -470,9 +472,10 @@ __device__ __forceinline__ void store_partial8(float* part, int groups, int grou
 // RW rows of at most 512 NW C columns at a time, NW waves each: workgroup b takes rows b RW ..,
 // (b + grid) RW .., ...; where registers allow, the next row's values are loaded before the
 // current row is worked on.  Each thread keeps its columns' dweight sums in registers; the
-// workgroup adds and writes them once (LN, the layer norm: dbias' sums too).  Short rows (one wave each) go four to a workgroup.  HBM
-// bounds it: 8192 x 4096 bf16 50 us (5.4 TB/s of dy, h, dh and dx), and 5 for sum_partials; with the
-// rows partly in the last-level cache 41 us, and there without the loads ahead 70.
+// workgroup adds and writes them once (LN, the layer norm: dbias' sums too).  Short rows (one wave
+// each) go four to a workgroup.  HBM bounds it: 8192 x 4096 bf16 50 us (5.4 TB/s of dy, h, dh and dx),
+// and 5 for sum_partials; with the rows partly in the last-level cache 41 us, and there without the
+// loads ahead 70.  The layer norm: 43 - 52 us, its two gradients' partial sums being twice as many.
 // Without SUMS dx alone.
 template <int TY, bool LN, int NW, int C, int RW, bool SUMS>
 __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& p, int group, int groups) {
@@ -900,7 +903,10 @@ __device__ __forceinline__ void dact_block(const DactArgs& p, int block, float (
 
 // ---- checkpoints in 8 bits (see pack_block8) -----------------------------------------------
 // A wave takes 8 << `lanes` columns of 64 >> lanes rows at once, 8 columns a lane; segs such pieces
-// cover a row.  kPackRows pieces of rows a wave one below the other, all of their loads in flight.
+// cover a row: one wave's columns are contiguous, and a row of 4097 columns wastes part of a wave, not
+// of a workgroup.  kPackRows pieces of rows a wave one below the other, all of their loads in flight.
+// HBM bounds both: pack8 8192 x 8190 bf16 35 us (5.8 TB/s), unpack8 8192 x 8192 34 us, through gelu_tanh
+// 38 (47 where every lane provides for a row's end).
 struct PackArgs {
   const uint16_t* x;      // packing; null: unpacking
   uint16_t* y;            // unpacking: act(values), in 16 bits
@@ -991,7 +997,8 @@ __global__ void __launch_bounds__(256) unpack8_rows(PackArgs p) {
 }
 
 // What stands before the products of a backward pass, in one launch: dpre and the column sums in the
-// first dact_blocks workgroups, a restored from 8 bits in the others.
+// first dact_blocks workgroups, a restored from 8 bits in the others.  HBM bounds it: 4096^3 bf16 with
+// both in 8 bits 29 - 33 us (134 MB, 4.4 TB/s); as two launches 26 + 11.
 template <int TY>
 __global__ void __launch_bounds__(256) lin_prepare(DactArgs d, PackArgs u, int dact_blocks) {
   __shared__ float s[3][512];

@@ -123,9 +123,9 @@ def linear(a, b, bias=None, residual=None, *, activation="none", scale_a=None, s
     a (m, k) and b (k, n): float16 or bfloat16, each row- or column-major with any leading
     dimension (a weight stored (n, k) is passed as `w.t()`); or float8_e4m3fn or int8 (k up to
     131071), k-contiguous (a row-major, b column-major) with 16-byte aligned rows, and `scale_a`
-    (m,) and `scale_b` (n,) float32 factors of the rows and columns (1 if not given).  bias (n,), residual (m, n): of
-    the output's type, which is the operands' (8-bit operands: `out_dtype`, bfloat16 if not
-    given).  activation: none, relu, gelu, gelu_tanh or silu.  Returns the (m, n) result, or
+    (m,) and `scale_b` (n,) float32 factors of the rows and columns (1 if not given).  bias (n,),
+    residual (m, n): of the output's type, which is the operands' (8-bit operands: `out_dtype`,
+    bfloat16 if not given).  activation: none, relu, gelu, gelu_tanh or silu.  Returns the (m, n) result, or
     (result, pre) with `with_pre`, where pre is the value before the activation, which
     linear_backward needs; with `pack_pre` pre is a Packed8, of half the size, made of the unrounded
     values.  `out` may be the residual's own tensor.
