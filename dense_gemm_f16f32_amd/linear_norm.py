@@ -207,8 +207,10 @@ def layer_norm(x, weight, bias=None, residual=None, *, eps=1e-5, out_dtype=None,
     `with_stats` also returns mean(h) and 1 / sqrt(var(h) + eps), which layer_norm_backward needs.
     """
     f = (_native or native()).layer_norm
-    args = (x, weight, bias, residual, eps, out_dtype, with_stats, LayerNormResult)
-    return f(*args) if stream is None else _on(stream, f, args, (x, weight, bias, residual))
+    if stream is None:
+        return f(x, weight, bias, residual, eps, out_dtype, with_stats, LayerNormResult)
+    return _on(stream, f, (x, weight, bias, residual, eps, out_dtype, with_stats, LayerNormResult),
+               (x, weight, bias, residual))
 
 
 def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, weight_grad=True, bias_grad=True,
@@ -219,10 +221,10 @@ def layer_norm_backward(dy, h, weight, mean, rstd, *, dh=None, weight_grad=True,
     that reaches h by another way (the residual stream), added to dx.
     """
     f = (_native or native()).layer_norm_backward
-    args = (dy, h, weight, mean, rstd, dh, weight_grad, bias_grad)
     if stream is None:
-        return f(*args)
-    return _on(stream, f, args, (dy, h, weight, mean, rstd, dh))
+        return f(dy, h, weight, mean, rstd, dh, weight_grad, bias_grad)
+    return _on(stream, f, (dy, h, weight, mean, rstd, dh, weight_grad, bias_grad),
+               (dy, h, weight, mean, rstd, dh))
 
 
 def quantize_rows(x, *, dtype=None, stream=None):
@@ -234,8 +236,9 @@ def quantize_rows(x, *, dtype=None, stream=None):
     row with a NaN or an infinity has scale NaN.
     """
     f = (_native or native()).quantize_rows
-    args = (x, dtype, QuantizedRows)
-    return f(*args) if stream is None else _on(stream, f, args, (x,))
+    if stream is None:
+        return f(x, dtype, QuantizedRows)
+    return _on(stream, f, (x, dtype, QuantizedRows), (x,))
 
 
 def pack8(x, *, stream=None):
@@ -249,8 +252,7 @@ def pack8(x, *, stream=None):
     holds a NaN or an infinity has scale NaN.
     """
     f = (_native or native()).pack8
-    args = (x, Packed8)
-    return f(*args) if stream is None else _on(stream, f, args, (x,))
+    return f(x, Packed8) if stream is None else _on(stream, f, (x, Packed8), (x,))
 
 
 def unpack8(packed, *, dtype=None, activation="none", stream=None):
