@@ -433,7 +433,9 @@ int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
   const bool pre8 = act && k8.pre.values, a8 = k8.a.values != nullptr;
   if (k8.a_activation < LINEAR_ACT_NONE || k8.a_activation > LINEAR_ACT_SILU)
     return GEMM_F16F32_ERR_OPTS;
-  if ((pre8 && x.pre) || (a8 && x.a) || (!a8 && k8.a_activation != LINEAR_ACT_NONE))
+  // an empty a has no address, packed or not
+  if ((pre8 && x.pre) || (a8 && x.a) ||
+      (!a8 && k8.a_activation != LINEAR_ACT_NONE && x.m > 0 && x.k > 0))
     return GEMM_F16F32_ERR_OPTS;
   int rc = check_rows(x.dc, x.m, x.n, &x.dc_row, 2, true);
   if (rc == 0 && act && !pre8) rc = check_rows(x.pre, x.m, x.n, &x.pre_row, 2, true);

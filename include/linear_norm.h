@@ -271,7 +271,7 @@ typedef struct unpack8_args {
  * in 16 bits. */
 typedef struct linear_kept {
     packed8_matrix a;
-    int64_t a_activation;     /* LINEAR_ACT_*; NONE unless a is given here */
+    int64_t a_activation;     /* LINEAR_ACT_*; NONE unless a is given here or empty (m or k 0) */
     packed8_matrix pre;
 } linear_kept;
 
