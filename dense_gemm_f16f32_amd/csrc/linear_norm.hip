@@ -197,20 +197,29 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
       for (int64_t z = 2; z <= 16 && rest > 0 && rest * z <= slots && panels >= 4 * z; ++z)
         consider(rounds * slots, z);
     }
-    // At most 16 columns: a pass over a, 16 of its rows a workgroup.  In us, on tiles / so, m x n x k:
-    // bf16 256 x 1 x 4096 8.9 / 6.8, 4095 x 1 x 4096 12.1 / 9.0, 4096 x 16 x 512 5.4 / 3.6, int8 4095 x
-    // 16 x 4096 10.2 / 6.9; the other way round bf16 64 x 16 x 4096 8.5 / 9.3, which this rule
-    // takes, and 8192 x 16 x 8192 33.9 / 38.1, which it does not.
-    const int64_t bytes = M * (K * 2 / E);
-    if (N <= lk::kSkinnyRows && a.km && b.km && K >= 8 * E && cdiv(M, 16) * 512 < kThreads &&
-        (N <= 8 || bytes <= (64 << 20))) {
-      const double deep = (double)K / E * (0.95e-3 + 0.05e-3 * N), wide = (double)bytes / 4.5e6;
-      best = 2.6 + (deep > wide ? deep : wide);
-      chosen.path = lk::kPathSkinnyFlip;
-      chosen.cols = 16;
-      chosen.programs = cdiv(M, 16);
-      chosen.w_bytes = 0;
-      set_split(&chosen, 0, panels, 1, 0);
+    // At most 16 columns: a pass over a, 16 of its rows a workgroup, in one piece of k, where the
+    // estimates say that it is faster than the tiles (whose own leaves out memory's rate: a tile is
+    // mostly empty here, and deep or many rows are a pass over a as well).  Few rows of a deep k stay
+    // with the tiles and their slices.  In us from memory in a graph, on tiles / so, m x n x k: bf16
+    // 64 x 16 x 1024 7.2 / 4.4, 4096 x 1 x 4096 13.8 / 10.5, 16384 x 1 x 16384 121 / 111; int8 256 x 16
+    // x 4096 8.2 / 6.8, 4096 x 8 x 16384 22 / 17; and left to the tiles bf16 64 x 16 x 4096 8.9 / 9.9,
+    // 32 x 16 x 16384 11.2 / 31, 17 x 1 x 65536 22 / 71, 16384 x 16 x 4096 32 / 39; int8 64 x 8 x 16384
+    // 9.5 / 14, 65536 x 16 x 256 10 / 15.  On 772 shapes (3 types, m 17 .. 65536, n 1 .. 16, k 64 ..
+    // 65536) the choice takes at most 4 % longer than the tiles and at most 17 % longer than the faster.
+    if (N <= lk::kSkinnyRows && a.km && b.km && K >= 8 * E && cdiv(M, 16) * 512 < kThreads) {
+      const double bytes = (double)M * (double)(K * 2 / E);
+      const double deep = (double)K / E * (0.95e-3 + 0.05e-3 * N);
+      const double wide = bytes * 1e-6 * (0.14 + 0.005 * N);
+      const double narrow = 2.2 + (deep > wide ? deep : wide) + 1.9e-3 * cdiv(M, 16);
+      const double memory = 2.0 + bytes / 5.3e6, tiles = best + 0.8 > memory ? best + 0.8 : memory;
+      if (best == 0.0 || narrow < tiles) {
+        best = narrow;
+        chosen.path = lk::kPathSkinnyFlip;
+        chosen.cols = 16;
+        chosen.programs = cdiv(M, 16);
+        chosen.w_bytes = 0;
+        set_split(&chosen, 0, panels, 1, 0);
+      }
     }
     if (best == 0.0) return GEMM_F16F32_ERR_TOO_LARGE;
     *g = chosen;
