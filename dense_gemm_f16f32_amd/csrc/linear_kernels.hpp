@@ -197,8 +197,10 @@ struct Block8 {
   uint32_t lo, hi;   // 8 integers
   uint32_t scale;    // the block's byte
 };
-// 8 values of a block, whose others the quad's other lanes hold (0 where there are none).
-__device__ __forceinline__ Block8 pack_block8(const float (&v)[8], int type) {
+// 8 values of a block, whose others the quad's other lanes hold (0 where there are none).  `least`:
+// what a positive value is stored as at least, where its sign has to stay (relu's slope goes by
+// it), or -127.
+__device__ __forceinline__ Block8 pack_block8(const float (&v)[8], int type, float least = -127.f) {
   uint32_t m = 0u;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -212,7 +214,8 @@ __device__ __forceinline__ Block8 pack_block8(const float (&v)[8], int type) {
 #pragma unroll
   for (int e = 0; e < 8; ++e)   // the addition rounds, and leaves the integer in the low bits
     q[e] = __builtin_bit_cast(
-        uint32_t, __builtin_amdgcn_fmed3f(v[e] * inv, -127.f, 127.f) + 12582912.f);
+        uint32_t,
+        __builtin_amdgcn_fmed3f(v[e] * inv, v[e] > 0.f ? least : -127.f, 127.f) + 12582912.f);
   auto bytes = [&](int i) __attribute__((always_inline)) {
     const uint32_t x = __builtin_amdgcn_perm(q[i + 1], q[i], 0x0C0C0400u);
     const uint32_t y = __builtin_amdgcn_perm(q[i + 3], q[i + 2], 0x0C0C0400u);
@@ -433,7 +436,8 @@ __device__ __forceinline__ void put_pre8(const LinArgs& p, int64_t row, int col,
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = e < n ? v[e] : 0.f;
-  const Block8 b = pack_block8(x, ot);
+  // rounded to 0, a positive value would lose relu's slope of 1
+  const Block8 b = pack_block8(x, ot, p.act == LINEAR_ACT_RELU ? 1.f : -127.f);
   if (n <= 0) return;
   store_bytes8(p.pre8 + row * p.ldp8 + col, b.lo, b.hi, n);
   if ((col & 31) == 0) p.pre8_scale[row * p.ldps + (col >> 5)] = (uint8_t)b.scale;

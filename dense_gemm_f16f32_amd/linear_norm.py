@@ -128,7 +128,8 @@ def linear(a, b, bias=None, residual=None, *, activation="none", scale_a=None, s
     bfloat16 if not given).  activation: none, relu, gelu, gelu_tanh or silu.  Returns the (m, n) result, or
     (result, pre) with `with_pre`, where pre is the value before the activation, which
     linear_backward needs; with `pack_pre` pre is a Packed8, of half the size, made of the unrounded
-    values.  `out` may be the residual's own tensor.
+    values (with relu, whose slope goes by the sign, a positive value is 1 scale at least).  `out` may be
+    the residual's own tensor.
     """
     f = (_native or native()).linear
     packed = Packed8 if pack_pre else None
@@ -247,7 +248,9 @@ def pack8(x, *, stream=None):
 
     Each 32 neighbours of a row share a power of two, by which the largest of them lies in [64, 128);
     values are rounded to the nearest integer, ties to even, and are at most 127 in magnitude, so
-    they are off by at most half a step (a whole one above 127.5 steps).  Scales are at least 2^-24
+    they are off by at most half a step (a whole one above 127.5 steps).  Positive values of up to half a
+    step become 0, where relu's slope is 0: for its backward pass keep linear's pack_pre, which leaves
+    them positive.  Scales are at least 2^-24
     (float16) or 2^-120 (bfloat16): values times scales are numbers of x's type.  A block that
     holds a NaN or an infinity has scale NaN.
     """

@@ -28,7 +28,8 @@
  *                       of the 16-bit type.  A block that holds an infinity or a NaN has scale NaN
  *   unpack8             y = act(values scale)
  *   linear_forward_packed    linear_forward, with pre in 8 bits as pack8 would make it of the
- *                       unrounded values
+ *                       unrounded values; with relu, whose slope goes by the sign, a positive value is
+ *                       1 scale at least (pack8 takes one of up to half a scale to 0, slope 0)
  *   linear_backward_packed   linear_backward, with a, pre or both in 8 bits.  With a_activation, a
  *                       holds the values before that activation: the layer's input is act(a),
  *                       rounded to the 16-bit type, and da the gradient of that
