@@ -848,6 +848,11 @@ __device__ __forceinline__ void dact_rows(const DactArgs& p, int64_t r0, int row
         else
           unpack8(x, raw8_shift(u[i], n, back), TY);
         slope8(v, x, p.act);
+        if constexpr (PRE == kPre8) {
+          // a lost block's slopes are not known: relu's of NaN is 0
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = b[i] == 255u ? __builtin_nanf("") : v[e];
+        }
         store8(dpre + r * p.dpre_row, v, n, TY);
       }
 #pragma unroll

@@ -248,11 +248,11 @@ def pack8(x, *, stream=None):
 
     Each 32 neighbours of a row share a power of two, by which the largest of them lies in [64, 128);
     values are rounded to the nearest integer, ties to even, and are at most 127 in magnitude, so
-    they are off by at most half a step (a whole one above 127.5 steps).  Positive values of up to half a
-    step become 0, where relu's slope is 0: for its backward pass keep linear's pack_pre, which leaves
-    them positive.  Scales are at least 2^-24
-    (float16) or 2^-120 (bfloat16): values times scales are numbers of x's type.  A block that
-    holds a NaN or an infinity has scale NaN.
+    they are off by at most half a step (a whole one above 127.5 steps).  Positive values of up to
+    half a step become 0, where relu's slope is 0: for its backward pass keep linear's pack_pre,
+    which leaves them positive.  Scales are at least 2^-24 (float16) or 2^-120 (bfloat16): values
+    times scales are numbers of x's type.  A block that holds a NaN or an infinity has scale NaN,
+    and linear_backward has NaN for its gradients.
     """
     f = (_native or native()).pack8
     return f(x, Packed8) if stream is None else _on(stream, f, (x, Packed8), (x,))

@@ -25,7 +25,8 @@
  *                       scale = 2^(f - 6), f = floor(log2(max |x|)) over the block, but not below
  *                       2^-24 (f16) or 2^-120 (bf16); values = x / scale, to the nearest integer
  *                       (ties to even), at most 127 in magnitude.  Integers times scales are values
- *                       of the 16-bit type.  A block that holds an infinity or a NaN has scale NaN
+ *                       of the 16-bit type.  A block that holds an infinity or a NaN has scale NaN,
+ *                       and NaN for its slopes, relu's too
  *   unpack8             y = act(values scale)
  *   linear_forward_packed    linear_forward, with pre in 8 bits as pack8 would make it of the
  *                       unrounded values; with relu, whose slope goes by the sign, a positive value is
