@@ -48,10 +48,11 @@
  * int8 operands are summed exactly in 32-bit integers, which bounds k by 131071, and the sum is
  * rounded to fp32 before it is scaled.
  *
- * e4m3 operands: with up to 16 rows (m) or k up to 512 (and in slivers of up to 16 columns) the
- * values are multiplied as f16, exactly.  Beyond, they go through the 8-bit matrix instruction,
- * which rounds inside: measured over random operands, a sum is off by up to 2^-17 of the sum of its
- * products' magnitudes at k = 1000.
+ * e4m3 operands: with up to 16 rows (m) or k up to 512 the values are multiplied as f16, exactly.
+ * Beyond, they may go through the 8-bit matrix instruction, which rounds inside: measured over random
+ * operands, a sum is off by up to 2^-17 of the sum of its products' magnitudes at k = 1000.  (Where a
+ * result of at most 16 columns, or a sliver of as many, is a pass over a, its values are multiplied
+ * as f16 too; that goes by an estimate of the time, and is no part of this contract.)
  *
  * Activations: none, relu, gelu (0.5 v (1 + erf(v / sqrt 2))), gelu_tanh (the tanh form of it),
  * silu (v / (1 + exp(-v))).  relu's slope at 0 is 0.
