@@ -128,6 +128,63 @@ double round_cost(const TileCost& c, int64_t workgroups, int64_t panels) {
   return workgroups <= kCUs ? c.fixed1 + panels * c.panel1 : c.fixed + panels * c.panel;
 }
 
+// The tile and split of an M x N x K product that are estimated to be the fastest, in at most `slices`
+// of k; returns the estimate, or 0 if no tile's panels fit.
+double plan_tiles(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b,
+                  int64_t slices, GemmPlan* g) {
+  const int64_t E = is8(type) ? 2 : 1, panels = cdiv(K, lk::kTileDepth * E);
+  double best = 0.0;
+  GemmPlan chosen = *g;
+  chosen.path = lk::kPathTiles;
+  for (int t = 0; t < lk::kTiles; ++t) {
+    const lk::TileShape& s = lk::kTileShapes[t];
+    const TileCost& c = kTileCosts[t];
+    // short 8-bit sums are taken as f16, which the largest tile does not do
+    if (t == lk::kTile256 && type == LINEAR_NORM_E4M3 && K <= lk::kHalvesK) continue;
+    // panels' 32-bit offsets
+    const int64_t ra = a.km ? s.bm : lk::kTileDepth, rb = b.km ? s.bn : lk::kTileDepth;
+    if (ra * (a.ld / E) >= kMax || rb * (b.ld / E) >= kMax) continue;
+    const int64_t P = cdiv(M, s.bm) * cdiv(N, s.bn), slots = (int64_t)kCUs * c.per_cu;
+    const int64_t rounds = P / slots, rest = P % slots;
+    auto consider = [&](int64_t whole, int64_t splits) {
+      // full rounds, then the rest in slices; the second launch and the sums' way through
+      // memory (mostly through the caches) for a split
+      const int64_t per = cdiv(panels, splits), tail = P - whole;
+      if ((whole + tail * splits) * 256 >= kThreads) return;
+      double cost = (double)(whole / slots) * round_cost(c, slots, panels);
+      cost += round_cost(c, tail * splits, per);
+      if (splits > 1) cost += 3.0 + (double)(tail * splits) * s.bm * s.bn * 8 / 8.0e6;
+      if (best == 0.0 || cost < best) {
+        best = cost;
+        chosen.tile = t;
+        chosen.programs = P;
+        chosen.w_bytes = 0;
+        set_split(&chosen, whole, panels, splits, (int64_t)s.bm * s.bn);
+      }
+    };
+    consider(rounds * slots, 1);
+    for (int64_t z = 2; z <= slices && rest > 0 && rest * z <= slots && panels >= 4 * z; ++z)
+      consider(rounds * slots, z);
+  }
+  *g = chosen;
+  return best;
+}
+
+// A result of at most 16 columns as a pass over a (E: operands' values in a 16-bit slot): whether the
+// kernel takes it, and its estimated time.  `odd_a`, `odd_b`: rows off 4-byte boundaries, whose loads
+// take longer than their multiplication and than memory (bf16, a's rows / b's / both at odd addresses:
+// 64 x 8 x 4096 17.1 / 14.0 / 22.7 us, all even 8.7; 16384 x 1 x 4096 55, even 24).
+bool narrow_fits(int64_t E, int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b) {
+  return N <= lk::kSkinnyRows && a.km && b.km && K >= 8 * E && cdiv(M, 16) * 512 < kThreads;
+}
+double narrow_cost(int64_t E, int64_t M, int64_t N, int64_t K, bool odd_a, bool odd_b) {
+  const double mbytes = (double)M * (double)(K * 2 / E) * 1e-6;
+  const double deep = (double)K / E * (0.95e-3 + 0.05e-3 * N + (odd_a ? 2.1e-3 : 0.0) +
+                                       (odd_b ? 0.15e-3 * N : 0.0));
+  const double wide = mbytes * (0.14 + 0.005 * N + (odd_a ? 0.23 : 0.0) + (odd_b ? 0.0145 * N : 0.0));
+  return 2.2 + (deep > wide ? deep : wide) + 1.9e-3 * cdiv(M, 16);
+}
+
 // The path, tile and split of an M x N x K product (M, N > 0).  `blocks`: the epilogue packs blocks
 // of 32 columns, which one workgroup has to hold.
 int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, const Operand& b,
@@ -164,39 +221,7 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     set_split(g, 0, depth, z, 16 * g->cols);
     g->cost = 4.0 + (double)(N * K * 2 / E) / 4.5e6 + (g->splits > 1 ? 3.0 : 0.0);
   } else {
-    g->path = lk::kPathTiles;
-    double best = 0.0;
-    GemmPlan chosen = *g;
-    for (int t = 0; t < lk::kTiles; ++t) {
-      const lk::TileShape& s = lk::kTileShapes[t];
-      const TileCost& c = kTileCosts[t];
-      // short 8-bit sums are taken as f16, which the largest tile does not do
-      if (t == lk::kTile256 && type == LINEAR_NORM_E4M3 && K <= lk::kHalvesK) continue;
-      // panels' 32-bit offsets
-      const int64_t ra = a.km ? s.bm : lk::kTileDepth, rb = b.km ? s.bn : lk::kTileDepth;
-      if (ra * (a.ld / E) >= kMax || rb * (b.ld / E) >= kMax) continue;
-      const int64_t P = cdiv(M, s.bm) * cdiv(N, s.bn), slots = (int64_t)kCUs * c.per_cu;
-      const int64_t rounds = P / slots, rest = P % slots;
-      auto consider = [&](int64_t whole, int64_t splits) {
-        // full rounds, then the rest in slices; the second launch and the sums' way through
-        // memory (mostly through the caches) for a split
-        const int64_t per = cdiv(panels, splits), tail = P - whole;
-        if ((whole + tail * splits) * 256 >= kThreads) return;
-        double cost = (double)(whole / slots) * round_cost(c, slots, panels);
-        cost += round_cost(c, tail * splits, per);
-        if (splits > 1) cost += 3.0 + (double)(tail * splits) * s.bm * s.bn * 8 / 8.0e6;
-        if (best == 0.0 || cost < best) {
-          best = cost;
-          chosen.tile = t;
-          chosen.programs = P;
-          chosen.w_bytes = 0;
-          set_split(&chosen, whole, panels, splits, (int64_t)s.bm * s.bn);
-        }
-      };
-      consider(rounds * slots, 1);
-      for (int64_t z = 2; z <= 16 && rest > 0 && rest * z <= slots && panels >= 4 * z; ++z)
-        consider(rounds * slots, z);
-    }
+    g->cost = plan_tiles(type, M, N, K, a, b, 16, g);
     // At most 16 columns: a pass over a, 16 of its rows a workgroup, in one piece of k, where the
     // estimates say that it is faster than the tiles (whose own leaves out memory's rate: a tile is
     // mostly empty here, and deep or many rows are a pass over a as well).  Few rows of a deep k stay
@@ -205,25 +230,23 @@ int plan_gemm(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a, c
     // x 4096 8.2 / 6.8, 4096 x 8 x 16384 22 / 17; and left to the tiles bf16 64 x 16 x 4096 8.9 / 9.9,
     // 32 x 16 x 16384 11.2 / 31, 17 x 1 x 65536 22 / 71, 16384 x 16 x 4096 32 / 39; int8 64 x 8 x 16384
     // 9.5 / 14, 65536 x 16 x 256 10 / 15.  On 772 shapes (3 types, m 17 .. 65536, n 1 .. 16, k 64 ..
-    // 65536) the choice takes at most 4 % longer than the tiles and at most 17 % longer than the faster.
-    if (N <= lk::kSkinnyRows && a.km && b.km && K >= 8 * E && cdiv(M, 16) * 512 < kThreads) {
-      const double bytes = (double)M * (double)(K * 2 / E);
-      const double deep = (double)K / E * (0.95e-3 + 0.05e-3 * N);
-      const double wide = bytes * 1e-6 * (0.14 + 0.005 * N);
-      const double narrow = 2.2 + (deep > wide ? deep : wide) + 1.9e-3 * cdiv(M, 16);
-      const double memory = 2.0 + bytes / 5.3e6, tiles = best + 0.8 > memory ? best + 0.8 : memory;
-      if (best == 0.0 || narrow < tiles) {
-        best = narrow;
-        chosen.path = lk::kPathSkinnyFlip;
-        chosen.cols = 16;
-        chosen.programs = cdiv(M, 16);
-        chosen.w_bytes = 0;
-        set_split(&chosen, 0, panels, 1, 0);
+    // 65536) the choice takes at most 4 % longer than the tiles (where a is partly in the last-level
+    // cache up to 19 %), at most 20 % longer than the faster of the two, and 22 % less in the mean.
+    if (narrow_fits(E, M, N, K, a, b)) {
+      const bool odd_a = E == 1 && a.ld % 2 != 0, odd_b = E == 1 && N > 1 && b.ld % 2 != 0;
+      const double narrow = narrow_cost(E, M, N, K, odd_a, odd_b);
+      const double memory = 2.0 + (double)M * (double)(K * 2 / E) / 5.6e6;
+      const double tiles = g->cost + 0.8 > memory ? g->cost + 0.8 : memory;
+      if (g->cost == 0.0 || narrow < tiles) {
+        g->path = lk::kPathSkinnyFlip;
+        g->cols = 16;
+        g->programs = cdiv(M, 16);
+        g->w_bytes = 0;
+        set_split(g, 0, panels, 1, 0);
+        g->cost = narrow;
       }
     }
-    if (best == 0.0) return GEMM_F16F32_ERR_TOO_LARGE;
-    *g = chosen;
-    g->cost = best;
+    if (g->cost == 0.0) return GEMM_F16F32_ERR_TOO_LARGE;
   }
   return GEMM_F16F32_OK;
 }
@@ -271,6 +294,18 @@ int plan_product(int64_t type, int64_t M, int64_t N, int64_t K, const Operand& a
   p->w_bytes = 0;
   for (int i = 0; i < p->parts; ++i)
     if (p->part[i].g.w_bytes > p->w_bytes) p->w_bytes = p->part[i].g.w_bytes;
+  // So far everything goes by strides, and with it the workspace.  A pass over a whose rows lie off
+  // 4-byte boundaries by their first address alone gives way to tiles that need none (bf16 16384 x 1
+  // x 4096 62 us so, 28 on tiles).
+  const bool off_a = (uintptr_t)a.p & 2, off_b = (uintptr_t)b.p & 2;
+  for (int i = 0; i < p->parts && !is8(type) && (off_a || off_b); ++i) {
+    Part& t = p->part[i];
+    if (t.g.path != lk::kPathSkinnyFlip) continue;
+    const double cost = narrow_cost(1, t.M, t.N, K, off_a || a.ld % 2 != 0, off_b || b.ld % 2 != 0);
+    GemmPlan tiles = t.g;
+    const double other = plan_tiles(type, t.M, t.N, K, a, b, 1, &tiles);
+    if (other > 0.0 && other + 0.8 < cost) t.g = tiles;
+  }
   return GEMM_F16F32_OK;
 }
 
@@ -521,14 +556,15 @@ int plan_backward(linear_backward_args& x, linear_kept* kept, BackwardPlan* f) {
     }
   }
   const int64_t ldd = act || f->copy ? f->ldd : x.dc_row;
+  const void* const dpre = act || f->copy ? nullptr : x.dc;   // null: in the workspace, aligned
   if (to_da) {
-    const Operand d = {x.dc, ldd, true};
+    const Operand d = {dpre, ldd, true};
     rc = plan_product(x.type, x.m, x.k, x.n, d, f->b, false, &f->qa);
     if (rc != 0) return rc;
     if (f->qa.w_bytes > f->w_bytes) f->w_bytes = f->qa.w_bytes;
   }
   if (to_db) {
-    f->dt = {x.dc, ldd, false};
+    f->dt = {dpre, ldd, false};
     rc = f->db_cols ? plan_product(x.type, x.n, x.k, x.m, f->dt, f->a, false, &f->qb)
                     : plan_product(x.type, x.k, x.n, x.m, f->a, f->dt, false, &f->qb);
     if (rc != 0) return rc;

@@ -40,3 +40,24 @@ def test_whole_numbers(m, n, k, kind):
     else:
         assert torch.equal(got, v.float().to(dt).double())
     assert bool((buf[:, n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@pytest.mark.parametrize("a_off,b_off,pad", [(1, 0, 0), (0, 1, 0), (1, 1, 0), (1, 0, 1), (0, 0, 1), (0, 0, 2)])
+@pytest.mark.parametrize("m,n,k", [(17, 1, 64), (300, 7, 512), (4096, 1, 4096), (16384, 1, 1024),
+                                   (2000, 16, 1000), (513, 260, 96)])
+def test_any_address(m, n, k, a_off, b_off, pad, ty):
+    """Rows at any 2-byte address, by the matrix's first one or by its stride."""
+    q = torch.Generator(device="cuda")
+    q.manual_seed(m + n + k)
+
+    def operand(rows, off):
+        buf = torch.full((off + rows * (k + pad) + 8,), float("nan"), device="cuda").to(TYPES[ty])
+        v = torch.as_strided(buf, (rows, k), (k + pad, 1), off)
+        v.copy_((torch.randint(0, 2, (rows, k), generator=q, device="cuda") * 2 - 1).to(TYPES[ty]))
+        return v
+
+    a, w = operand(m, a_off), operand(n, b_off)
+    print(f"narrow {m}x{n}x{k} {ty} {a_off} {b_off} {pad}", flush=True)
+    out = g.linear(a, w.t())
+    assert torch.equal(out, mm(a.double(), w.double().t()).float().to(TYPES[ty]))
