@@ -1078,7 +1078,12 @@ int linear_backward_packed(const linear_backward_args* args, const linear_kept* 
     if (rc != GEMM_F16F32_OK) return rc;
   }
   if (before > 0) {
-    prepare(x.type, d, u, before, dim3((uint32_t)before), s);
+    if (d.pre8 || f.copy)
+      prepare(x.type, d, u, before, dim3((uint32_t)before), s);
+    else if (bf)
+      hipLaunchKernelGGL((nk::lin_dact<lk::kBF16>), dim3((uint32_t)before), dim3(256), 0, s, d);
+    else
+      hipLaunchKernelGGL((nk::lin_dact<lk::kF16>), dim3((uint32_t)before), dim3(256), 0, s, d);
     if (hipGetLastError() != hipSuccess) return GEMM_F16F32_ERR_HIP;
   }
   if (last && !f.pair && !f.carry) {

@@ -860,6 +860,64 @@ __device__ __forceinline__ void dact_rows(const DactArgs& p, int64_t r0, int row
     }
   }
 }
+// The sums of a workgroup's four waves joined and stored.
+template <int TY>
+__device__ __forceinline__ void dact_sums(const DactArgs& p, int rb, int t, int g, int col,
+                                          float (&sum)[8], float (&s)[3][512]) {
+  if (p.part == nullptr && p.sum == nullptr) return;
+  const int n = p.n - col;
+  if (g > 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[g - 1][t * 8 + e] = sum[e];
+  }
+  __syncthreads();
+  if (g == 0 && n > 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += s[i][t * 8 + e];
+    if (p.sum != nullptr)
+      store8(p.sum + col, sum, n, TY);
+    else
+      store_partial8(p.part, p.row_blocks, rb, col, sum);
+  }
+}
+// Without checkpoints, nor a copy of dc: a kernel of its own, not longer for them.  In us, so / as the
+// other's 16-bit rows: 8192 x 8192 bf16 with relu 82 / 90, 4095 x 4097 with silu 26 / 31, 2704 x 3654
+// with relu 16.4 / 17.7, 4544 x 6 5.9 / 8.5, 256 x 256 2.9 / 3.1.
+template <int TY>
+__global__ void __launch_bounds__(256) lin_dact(DactArgs p) {
+  __shared__ float s[3][512];
+  const int cb = blockIdx.x / p.row_blocks, rb = blockIdx.x - cb * p.row_blocks;
+  const int t = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int col = cb * 512 + t * 8, n = p.n - col;
+  // rows counted from the block's first: numbers past the last row need not fit 31 bits
+  const int64_t r0 = (int64_t)rb * p.rows_per_block;
+  const int rows = p.m - r0 < p.rows_per_block ? (int)(p.m - r0) : p.rows_per_block;
+  const uint16_t* const dc = p.dc + r0 * p.dc_row + col;
+  const uint16_t* const pre = p.pre + r0 * p.pre_row + col;
+  uint16_t* const dpre = p.dpre + r0 * p.dpre_row + col;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  if (n > 0) {
+#pragma unroll 4
+    for (int row = g; row < rows; row += 4) {
+      float v[8];
+      load8(v, dc + row * p.dc_row, n, TY, p.n >= 8);
+      if (p.pre) {
+        float u[8];
+        load8(u, pre + row * p.pre_row, n, TY, p.n >= 8);
+        slope8(v, u, p.act);
+        store8(dpre + row * p.dpre_row, v, n, TY);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[e];
+    }
+  }
+  dact_sums<TY>(p, rb, t, g, col, sum, s);
+}
+// With checkpoints or a copy.
 template <int TY>
 __device__ __forceinline__ void dact_block(const DactArgs& p, int block, float (&s)[3][512]) {
   const int cb = block / p.row_blocks, rb = block - cb * p.row_blocks;
@@ -888,22 +946,7 @@ __device__ __forceinline__ void dact_block(const DactArgs& p, int block, float (
   } else if (n > 0) {
     work(std::false_type{}, std::integral_constant<int, 4>{});
   }
-  if (p.part == nullptr && p.sum == nullptr) return;
-  if (g > 0) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[g - 1][t * 8 + e] = sum[e];
-  }
-  __syncthreads();
-  if (g == 0 && n > 0) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += s[i][t * 8 + e];
-    if (p.sum != nullptr)
-      store8(p.sum + col, sum, n, TY);
-    else
-      store_partial8(p.part, p.row_blocks, rb, col, sum);
-  }
+  dact_sums<TY>(p, rb, t, g, col, sum, s);
 }
 
 // ---- checkpoints in 8 bits (see pack_block8) -----------------------------------------------
