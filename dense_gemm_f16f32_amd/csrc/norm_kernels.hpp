@@ -189,8 +189,10 @@ __device__ __forceinline__ uint32_t max_bits8(const float (&v)[8], uint32_t m) {
 
 // One pass: the row's statistics, the 8-bit scale and y come from the row in registers.  HBM bounds
 // it: 8192 x 8192 bf16 with residual to e4m3 88 us (5.3 TB/s), 4095 x 4093 f16 29 us (4.6 TB/s; 24.5
-// where the rows are partly in the last-level cache); the layer norm 8192 x 8192 bf16 100 us (5.4 TB/s,
-// 106 with three barriers and sums through LDS), one row of 4096 to e4m3 3.6.
+// where the rows are partly in the last-level cache); the layer norm 8192 x 8192 bf16 100 - 107 us (5.0 -
+// 5.4 TB/s; with three barriers and sums through LDS 106 where this takes 100), to int8 or e4m3 96, 4096 x
+// 16384 105, one row of 4096 to e4m3 3.6.  Rows above 16384 are read three times, four to 8 bits: 4096 x
+// 32768 362 us, to int8 402.
 // One row a workgroup of 64 NW threads, 8 columns a thread at a time.  C > 0: rows of at most
 // 512 NW C columns, held in registers.  C == 0: longer rows, read again for each step that
 // needs them.
@@ -396,7 +398,8 @@ __global__ void __launch_bounds__(64 * NW) norm_fwd(NormArgs p) {
 }
 
 // Rows in 8 bits with a scale a row, as the norm's: one row a workgroup, held in registers.  HBM bounds
-// it: 8192 x 8192 bf16 to int8 30 - 40 us, 4095 x 4093 f16 10.6 (4.7 TB/s).
+// it: 8192 x 8192 bf16 to int8 38 us from and to memory (5.3 TB/s; e4m3 the same), 4095 x 4093 f16 14.3
+// (3.5 TB/s), 10.6 on the same matrices, partly in the last-level cache.
 struct QuantizeArgs {
   const uint16_t* x;
   uint8_t* y;
@@ -475,7 +478,9 @@ __device__ __forceinline__ void store_partial8(float* part, int groups, int grou
 // workgroup adds and writes them once (LN, the layer norm: dbias' sums too).  Short rows (one wave
 // each) go four to a workgroup.  HBM bounds it: 8192 x 4096 bf16 50 us (5.4 TB/s of dy, h, dh and dx),
 // and 5 for sum_partials; with the rows partly in the last-level cache 41 us, and there without the
-// loads ahead 70.  The layer norm: 43 - 52 us, its two gradients' partial sums being twice as many.
+// loads ahead 70.  The layer norm: 43 - 52 us, its two gradients' partial sums being twice as many (with
+// their sum 57 - 63 from and to memory, 8192 x 8192 114).  Above 8192 columns, without loads ahead: 4096 x
+// 12288 107 us with the sums (3.8 TB/s), 4096 x 16384 139 (3.9); the RMS norm 93 and 120.
 // Without SUMS dx alone.
 // (The arguments by value: by reference the RMS norm's kernels took up to 7 % longer, 9 x 2365 f16 3.53
 // against 3.24 us.)
@@ -710,7 +715,8 @@ __global__ void __launch_bounds__(64 * NW * RW) layer_norm_bwd_small(NormBwdArgs
 }
 
 // Rows too long for registers: read twice, the dweight and dbias sums kept in the workgroup's
-// part of the workspace.
+// part of the workspace, read and written again for every row, which is most of its time: 4096 x 32768
+// bf16 1135 us, the RMS norm 736 (16384 columns, in registers, 139 and 120).
 template <int TY, bool LN, int NW>
 __global__ void __launch_bounds__(64 * NW) norm_bwd_long(NormBwdArgs p) {
   const bool back = p.dim >= 8;
@@ -955,8 +961,9 @@ __device__ __forceinline__ void dact_block(const DactArgs& p, int block, float (
 // A wave takes 8 << `lanes` columns of 64 >> lanes rows at once, 8 columns a lane; segs such pieces
 // cover a row: one wave's columns are contiguous, and a row of 4097 columns wastes part of a wave, not
 // of a workgroup.  kPackRows pieces of rows a wave one below the other, all of their loads in flight.
-// HBM bounds both: pack8 8192 x 8190 bf16 35 us (5.8 TB/s), unpack8 8192 x 8192 34 us, through gelu_tanh
-// 38 (47 where every lane provides for a row's end).
+// HBM bounds both.  bf16, from memory and to memory / on the same matrices, partly in the last-level
+// cache: pack8 8192 x 8190 43 us (4.7 TB/s) / 35, unpack8 8192 x 8192 38 us (5.3 TB/s) / 34, through
+// gelu_tanh 46 / 38 (47 where every lane provides for a row's end), 8192 x 8190 50, through gelu_tanh 56.
 struct PackArgs {
   const uint16_t* x;      // packing; null: unpacking
   uint16_t* y;            // unpacking: act(values), in 16 bits

@@ -120,9 +120,11 @@ __device__ __forceinline__ void join_waves(const LinArgs& p, const float4v (&acc
 // flight at once.  HBM bounds it.  With other weights in between (2 GiB of them in turn): 1 x 16384
 // x 4096 bf16 26.9 us (5.0 TB/s), 16 x 16384 x 4096 30.1 us (4.5 TB/s), 16 x 8192 x 8192 e4m3 17.0
 // us (3.9 TB/s) and 4.3 for its two slices' join.  The same weights again and again stay partly in
-// the last-level cache: 24.7, 23.4 and 13.7 us.  1 x 16384 x 4096 int8 14.8 us (4.5 TB/s).  FLIP: the
-// rows of the product are b's (at most 16 columns of the result) and what streams is a: 4095 x 1 x
-// 4096 bf16 9.0 us (3.7 TB/s), int8 6.1.
+// the last-level cache: 24.7, 23.4 and 13.7 us.  int8 with bias and
+// gelu_tanh, from memory / the same weights: 1 x 16384 x 4096 16.2 / 15.5 us (4.1 TB/s), 8 rows 18.9 /
+// 17.8, 16 rows 17.5 / 15.1, 16 x 8192 x 8192 20.2 / 17.4 with its join.  FLIP: the rows of the product
+// are b's (at most 16 columns of the result) and what streams is a: 4096 x 1 x 4096 bf16 10.5 us from
+// memory (3.2 TB/s), 6.4 with a partly in the last-level cache; int8 6.3 from memory.
 template <int TY, int NB, int NW, bool SHORT, int MORE, bool FLIP>
 __global__ void __launch_bounds__(64 * NW) lin_skinny_k(LinArgs p) {
   constexpr int UE = kBytes<TY> ? 128 : 64, CE = UE / 8;   // elements of a unit, of a chunk

@@ -1,5 +1,5 @@
-"""The backward pass from checkpoints of empty batches and of layers without inputs, with every
-activation that recomputes the layer's input."""
+"""Checkpoints of empty batches and of layers without inputs: made by the linear layer, and read by its
+backward pass with every activation that recomputes the layer's input."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -39,3 +39,18 @@ def test_block_on_no_tokens():
     assert out.shape == dx.shape == (0, 64)
     for grad, p in zip(grads, block.parameters()):
         assert grad.shape == p.shape and not grad.any()
+
+
+@pytest.mark.parametrize("ty", [torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn])
+@pytest.mark.parametrize("m,n,k", [(5, 45, 0), (40, 77, 0), (300, 7, 0), (0, 45, 16), (5, 0, 16)])
+def test_linear(m, n, k, ty):
+    """Without inputs the value before the activation is the bias."""
+    dt = ty if ty.itemsize == 2 else torch.float16
+    a, w = (torch.ones((x, k), device="cuda").to(ty) for x in (m, n))
+    bias = (torch.arange(n, device="cuda") % 9).to(dt)
+    print(f"empty linear {m}x{n}x{k} {ty}", flush=True)
+    out, p = g.linear(a, w.t(), bias, activation="relu", out_dtype=dt, pack_pre=True)
+    assert out.shape == p.values.shape == (m, n) and p.scale.shape == (m, -(-n // 32))
+    if k == 0:
+        assert torch.equal(out, bias.expand(m, n))
+        assert torch.equal(g.unpack8(p, dtype=dt), bias.expand(m, n))
